@@ -9,6 +9,7 @@
 namespace {
 
 constexpr int kMaxGridYZ = 65535;
+constexpr int kMaxPagedQueries = 1 << 24;   // (sequence, head) pairs of one paged call: grid x, 32-bit counts
 
 bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 
@@ -104,6 +105,26 @@ tq_status run_packed(const float* A, const float* T, const uint8_t* idx_plane,
                                                  scores, P, B, S, D, idx_bits, after_prepare, stream));
 }
 
+// The cache struct of the paged calls, and the sizes they share.
+tq_status check_paged(const tq_paged_cache* c, const int* page_table, int B, int max_pages) {
+  if (c == nullptr) return TQ_ERR_INVALID_VALUE;
+  tq_status st = check_ptrs(c->k_plane, c->k_norm, c->v_plane, c->v_norm, c->Pi_k, c->Pi_v, c->k_codebook,
+                            c->v_codebook, page_table);
+  if (st != TQ_OK) return st;
+  if (c->n_pages < 1 || c->H < 1 || c->H > kMaxGridYZ || c->rot_heads < 1 || c->rot_heads > c->H)
+    return TQ_ERR_INVALID_VALUE;
+  if (c->k_bits < 2 || c->k_bits > 4 || c->v_bits < 2 || c->v_bits > 4 || c->D < 1 || c->page_size < 1)
+    return TQ_ERR_INVALID_VALUE;
+  if (c->D != 128) return TQ_ERR_UNSUPPORTED;
+  const int ps = c->page_size;
+  if (ps < 16 || ps > 256 || (ps & (ps - 1)) != 0) return TQ_ERR_UNSUPPORTED;
+  if (B < 1 || B > kMaxGridYZ || max_pages < 1 || max_pages > (INT_MAX - 4096) / ps) return TQ_ERR_INVALID_VALUE;
+  return TQ_OK;
+}
+
+// An array that may be left out: null, or aligned.
+bool bad_optional(const void* p) { return p != nullptr && misaligned(p); }
+
 tq_status check_pack_sizes(int64_t n_keys, int D, int bits) {
   if (n_keys < 1 || D < 8 || D > 4096 || D % 8 != 0 || bits < 1 || bits > 8)
     return TQ_ERR_INVALID_VALUE;
@@ -141,6 +162,9 @@ tq_status tq_device_faults(unsigned int* bits) {
   if (e == cudaSuccess) e = tq::take_faults_decode(&v);
   if (e == cudaSuccess) e = tq::take_faults_compress(&v);
   if (e == cudaSuccess) e = tq::take_faults_check(&v);
+  if (e == cudaSuccess) e = tq::take_faults_append(&v);
+  if (e == cudaSuccess) e = tq::take_faults_paged(&v);
+  if (e == cudaSuccess) e = tq::take_faults_evict(&v);
   if (e != cudaSuccess) return TQ_ERR_LAUNCH;
   *bits |= v;
   return TQ_OK;
@@ -327,6 +351,78 @@ tq_status tq_decode_prod(const float* A, const float* T, const uint8_t* k_plane,
   return from_cuda(tq::launch_decode_prod(A, T, k_plane, k_sign_plane, k_gamma, k_codebook, k_bits, v_plane,
                                           v_norm, v_codebook, v_bits, Pi_v, out,
                                           static_cast<float*>(workspace), P, H, B, S, scale, stream));
+}
+
+tq_status tq_append_paged(const tq_paged_cache* cache, const void* K, const void* V, tq_qtype type,
+                          const int* rows, int n, const int* page_table, int B, int max_pages,
+                          float* mass, int* positions, int S, cudaStream_t stream) {
+  tq_status st = check_paged(cache, page_table, B, max_pages);
+  if (st != TQ_OK) return st;
+  if (n < 0 || S < 0 || (type != TQ_Q_F32 && type != TQ_Q_BF16)) return TQ_ERR_INVALID_VALUE;
+  if ((mass != nullptr || positions != nullptr) && (S < 1 || S > INT_MAX - 4096)) return TQ_ERR_INVALID_VALUE;
+  if (bad_optional(mass) || bad_optional(positions)) return TQ_ERR_MISALIGNED;
+  if (n == 0) return TQ_OK;
+  if (static_cast<int64_t>(n) * cache->H > INT_MAX - 4096) return TQ_ERR_INVALID_VALUE;
+  if ((st = check_ptrs(K, V, rows)) != TQ_OK) return st;
+  return from_cuda(tq::launch_append_paged(*cache, K, V, type, rows, n, page_table, B, max_pages, mass,
+                                           positions, S, stream));
+}
+
+size_t tq_decode_paged_workspace_bytes(int B, int H, int G, int S, int with_mass) {
+  if (B < 1 || H < 1 || G < 1 || S < 0 || static_cast<int64_t>(B) * H * G > kMaxPagedQueries) return 0;
+  return tq::decode_paged_bytes(B, H, G, S, with_mass != 0);
+}
+
+tq_status tq_decode_paged(const tq_paged_cache* cache, const void* Q, tq_qtype qtype,
+                          const int* page_table, const int* lengths, int B, int G, int max_pages,
+                          float scale, float* mass, int S, void* out, void* workspace,
+                          size_t workspace_bytes, cudaStream_t stream) {
+  tq_status st = check_paged(cache, page_table, B, max_pages);
+  if (st != TQ_OK) return st;
+  if ((st = check_ptrs(Q, lengths, out)) != TQ_OK) return st;
+  if (bad_optional(mass)) return TQ_ERR_MISALIGNED;
+  if (G < 1 || !std::isfinite(scale) || (qtype != TQ_Q_F32 && qtype != TQ_Q_BF16)) return TQ_ERR_INVALID_VALUE;
+  if (mass != nullptr ? (S < 1 || S > INT_MAX - 4096) : S < 0) return TQ_ERR_INVALID_VALUE;
+  if (static_cast<int64_t>(B) * cache->H * G > kMaxPagedQueries) return TQ_ERR_INVALID_VALUE;
+  // the key tiles of all (sequence, head, query tile) units are counted in 32 bits
+  if (static_cast<int64_t>(B) * cache->H * ((G + 3) / 4) >
+      INT_MAX / ((static_cast<int64_t>(max_pages) * cache->page_size + 15) / 16))
+    return TQ_ERR_INVALID_VALUE;
+  if (workspace == nullptr) return TQ_ERR_WORKSPACE;
+  if (misaligned(workspace)) return TQ_ERR_MISALIGNED;
+  if (workspace_bytes < tq_decode_paged_workspace_bytes(B, cache->H, G, S, mass != nullptr)) return TQ_ERR_WORKSPACE;
+  return from_cuda(tq::launch_decode_paged(*cache, Q, qtype, page_table, lengths, B, G, max_pages, scale, mass,
+                                           S, out, workspace, stream));
+}
+
+size_t tq_evict_paged_workspace_bytes(int B, int H, int S, int budget) {
+  if (B < 1 || H < 1 || S < 1 || budget < 1) return 0;
+  return tq::evict_paged_bytes(B, H, S, budget);
+}
+
+tq_status tq_evict_paged(const tq_paged_cache* cache, const int* page_table, const int* lengths,
+                         const int* seen, int B, int max_pages, const float* mass,
+                         const int* positions, int S, int budget, int recent, float* mass_out,
+                         int* positions_out, void* workspace, size_t workspace_bytes,
+                         cudaStream_t stream) {
+  tq_status st = check_paged(cache, page_table, B, max_pages);
+  if (st != TQ_OK) return st;
+  if ((st = check_ptrs(lengths, seen, mass, positions, mass_out, positions_out)) != TQ_OK) return st;
+  if (S < 1 || S > INT_MAX - 4096 || budget < 1 || recent < 0) return TQ_ERR_INVALID_VALUE;
+  if (static_cast<int64_t>(B) * cache->H > kMaxPagedQueries) return TQ_ERR_INVALID_VALUE;
+  const size_t bytes = static_cast<size_t>(B) * cache->H * S * 4;
+  auto overlap = [bytes](const void* a, const void* b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + bytes && y < x + bytes;
+  };
+  if (overlap(mass, mass_out) || overlap(mass, positions_out) || overlap(positions, mass_out) ||
+      overlap(positions, positions_out) || overlap(mass_out, positions_out))
+    return TQ_ERR_INVALID_VALUE;
+  if (workspace == nullptr) return TQ_ERR_WORKSPACE;
+  if (misaligned(workspace)) return TQ_ERR_MISALIGNED;
+  if (workspace_bytes < tq_evict_paged_workspace_bytes(B, cache->H, S, budget)) return TQ_ERR_WORKSPACE;
+  return from_cuda(tq::launch_evict_paged(*cache, page_table, lengths, seen, B, max_pages, mass, positions, S,
+                                          budget, recent, mass_out, positions_out, workspace, stream));
 }
 
 tq_status tq_pack_indices(const uint8_t* K_idx, uint8_t* idx_plane, int64_t n_keys, int D,

@@ -1,0 +1,49 @@
+// Shared pieces of the paged-cache kernels (tq_append.cu, tq_paged_*.cu, tq_evict.cu).
+#pragma once
+
+#include "tq_internal.cuh"
+
+namespace tq {
+namespace {
+
+constexpr int kPD = 128;   // head dimension
+
+// The cache as the kernels see it.  page_size is a power of two.
+struct Paged {
+  uint8_t* kp;
+  uint8_t* vp;
+  uint16_t* kn;
+  uint16_t* vn;
+  const int* table;
+  int n_pages, H, shift, max_pages;   // page_size = 1 << shift
+
+  // Page of slot s of sequence b, or -1 (absent: a number out of range, recorded).
+  __device__ __forceinline__ int page(int b, int s) const {
+    const int id = table[static_cast<size_t>(b) * max_pages + (s >> shift)];
+    if (static_cast<unsigned>(id) < static_cast<unsigned>(n_pages)) return id;
+    atomicOr(&g_wait_fault, static_cast<unsigned int>(kFaultPaged));
+    return -1;
+  }
+  // Row number of slot s on a page, in the planes of head h.
+  __device__ __forceinline__ size_t row(int pg, int h, int s) const {
+    return ((static_cast<size_t>(pg) * H + h) << shift) + (s & ((1 << shift) - 1));
+  }
+  // A sequence's length, cut to the capacity (recorded when it had to be).
+  __device__ __forceinline__ int length(const int* lengths, int b, int cap) const {
+    const int n = lengths[b];
+    if (n >= 0 && n <= cap) return n;
+    atomicOr(&g_wait_fault, static_cast<unsigned int>(kFaultPaged));
+    return n < 0 ? 0 : cap;
+  }
+};
+
+inline Paged paged_view(const tq_paged_cache& c, const int* table, int max_pages) {
+  int shift = 0;
+  while ((1 << shift) < c.page_size) ++shift;
+  return {c.k_plane, c.v_plane, c.k_norm, c.v_norm, table, c.n_pages, c.H, shift, max_pages};
+}
+
+inline size_t paged_round(size_t v) { return (v + 255) / 256 * 256; }
+
+}  // namespace
+}  // namespace tq

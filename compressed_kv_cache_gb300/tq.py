@@ -64,6 +64,11 @@ _SIGNATURES = {
     "tq_compress_keys_packed": ([_P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _P], _I),
     "tq_lloyd_max_codebook": ([_I, _I, _I, _I, _P], _I),
     "tq_haar_rotation": ([_P, _I, _P], _I),
+    "tq_append_paged": ([_P, _P, _P, _I, _P, _I, _P, _I, _I, _P, _P, _I, _P], _I),
+    "tq_decode_paged_workspace_bytes": ([_I, _I, _I, _I, _I], ctypes.c_size_t),
+    "tq_decode_paged": ([_P, _P, _I, _P, _P, _I, _I, _I, ctypes.c_float, _P, _I, _P, _P, _Z, _P], _I),
+    "tq_evict_paged_workspace_bytes": ([_I, _I, _I, _I], ctypes.c_size_t),
+    "tq_evict_paged": ([_P, _P, _P, _P, _I, _I, _P, _P, _I, _I, _I, _P, _P, _P, _Z, _P], _I),
     "tq_solve_packed_noalloc": ([_P, _I, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P], _I),
 }
 
@@ -103,7 +108,8 @@ def auto_path(B: int, D: int) -> str:
 def device_faults() -> int:
     """Fault bits the bounded waits of libtq's kernels set on the current device since the
     last call (0 = none; 1 lookup-table scorers, 2 tensor-core scorer, 4 decode, 8
-    compressor, 16 check_wait_expiry); reading clears them.  Synchronises with the device."""
+    compressor, 16 check_wait_expiry, 32 a length, slot or page number out of range in a paged
+    call); reading clears them.  Synchronises with the device."""
     v = ctypes.c_uint(0)
     _check("tq_device_faults", lib().tq_device_faults(ctypes.byref(v)))
     return int(v.value)
@@ -492,3 +498,173 @@ def compress_keys_packed(keys, Pi, S_mat, codebook, idx_bits, out=None):
         _dev(ip, "idx_plane", (torch.uint8,)), _dev(sp, "sign_plane", (torch.uint8,)),
         _dev(g, "gamma", (torch.float16,)), P, H, S, D, _stream()))
     return ip, sp, g
+
+
+class _PagedCacheStruct(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("k_plane", "k_norm", "v_plane", "v_norm", "Pi_k", "Pi_v", "k_codebook",
+                                  "v_codebook")] + \
+               [(n, _I) for n in ("n_pages", "H", "page_size", "D", "k_bits", "v_bits", "rot_heads")]
+
+
+class PagedCache:
+    """A paged cache of MSE-quantized keys and values: the handle the paged calls take, made
+    once per layer.  k_plane uint8 [N,H,page,D*k_bits/8], k_norm float16 [N,H,page], v_plane
+    and v_norm likewise; Pi_k, Pi_v fp32 [h,D,D] (or [D,D]), KV head i using rotation i % h;
+    k_codebook, v_codebook fp32 of 2^bits ascending centroids.  D is 128, bits 2 to 4, page a
+    power of two from 16 to 256.  The tensors stay the caller's (they may be written between
+    calls, not resized); all are on one device, and the calls run there."""
+
+    __slots__ = ("k_plane", "k_norm", "v_plane", "v_norm", "Pi_k", "k_codebook", "Pi_v", "v_codebook", "device",
+                 "H", "page_size", "D", "k_bits", "v_bits", "_struct", "_ref")
+
+    def __init__(self, k_plane, k_norm, v_plane, v_norm, Pi_k, k_codebook, Pi_v, v_codebook):
+        names = ("k_plane", "k_norm", "v_plane", "v_norm", "Pi_k", "Pi_v", "k_codebook", "v_codebook")
+        tensors = (k_plane, k_norm, v_plane, v_norm, Pi_k, Pi_v, k_codebook, v_codebook)
+        dtypes = (torch.uint8, torch.float16) * 2 + (torch.float32,) * 4
+        ptrs = [_dev(t, n, (d,)) for t, n, d in zip(tensors, names, dtypes)]
+        if any(t.device != k_plane.device for t in tensors):
+            raise ValueError("the tensors of a cache must be on one device")
+        if k_plane.dim() != 4 or v_plane.dim() != 4:
+            raise ValueError("k_plane and v_plane must be [pages, H, page, bytes]")
+        N, H, page, krow = k_plane.shape
+        D = Pi_k.shape[-1]
+        if (tuple(v_plane.shape[:3]) != (N, H, page) or tuple(k_norm.shape) != (N, H, page)
+                or tuple(v_norm.shape) != (N, H, page)):
+            raise ValueError("inconsistent page shapes")
+        if Pi_k.dim() not in (2, 3) or tuple(Pi_k.shape[-2:]) != (D, D) or Pi_v.shape != Pi_k.shape:
+            raise ValueError("Pi_k and Pi_v must be [h,D,D] or [D,D]")
+        kb, vb = krow * 8 // D, v_plane.shape[3] * 8 // D
+        if (krow * 8 != D * kb or v_plane.shape[3] * 8 != D * vb or k_codebook.numel() != 1 << kb
+                or v_codebook.numel() != 1 << vb):
+            raise ValueError("row bytes and codebook sizes do not match")
+        self.k_plane, self.k_norm, self.v_plane, self.v_norm = k_plane, k_norm, v_plane, v_norm
+        self.Pi_k, self.k_codebook, self.Pi_v, self.v_codebook = Pi_k, k_codebook, Pi_v, v_codebook
+        self.device, self.H, self.page_size, self.D, self.k_bits, self.v_bits = k_plane.device, H, page, D, kb, vb
+        self._struct = _PagedCacheStruct(*ptrs, N, H, page, D, kb, vb, 1 if Pi_k.dim() == 2 else Pi_k.shape[0])
+        self._ref = ctypes.addressof(self._struct)
+
+
+def _on(cache: PagedCache, t: torch.Tensor, name: str, dtype, shape) -> int:
+    """Pointer of a tensor of a paged call: its type, device, shape and contiguity are checked."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.device != cache.device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _paged_call(name: str, cache: PagedCache, *args) -> None:
+    """Calls `name` on the cache's device and that device's current stream."""
+    dev = cache.device.index
+    if dev == torch.cuda.current_device():
+        status = getattr(_lib or lib(), name)(cache._ref, *args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(_lib or lib(), name)(cache._ref, *args, torch.cuda.current_stream(dev).cuda_stream)
+    if status != TQ_OK:
+        raise TQError(name, status)
+
+
+def _table(cache: PagedCache, page_table: torch.Tensor) -> tuple[int, int, int]:
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be a [B, max_pages] tensor")
+    B, M = page_table.shape
+    return _on(cache, page_table, "page_table", torch.int32, (B, M)), B, M
+
+
+def _workspace_of(cache: PagedCache, workspace, need: int) -> tuple[torch.Tensor, int]:
+    if workspace is None:
+        workspace = torch.empty(need, device=cache.device, dtype=torch.uint8)
+    return workspace, _on(cache, workspace, "workspace", torch.uint8, (workspace.numel(),))
+
+
+def append_paged(K, V, rows, cache: PagedCache, page_table, mass=None, positions=None) -> None:
+    """Quantises new tokens' keys and values and writes them to their slots.  K, V [n,H,D]
+    fp32/bf16; rows int32 [n,3] of (sequence, slot, position), a negative sequence or slot
+    skipping the row; page_table int32 [B,max_pages].  mass fp32 and positions int32 [B,H,S]
+    (optional) get 0 and the position at the slots written.  No two rows may name one slot."""
+    if not isinstance(K, torch.Tensor) or K.dim() != 3 or K.dtype not in QTYPE:
+        raise ValueError("K must be a [n, H, D] fp32 or bf16 tensor")
+    n = K.shape[0]
+    shape = (n, cache.H, cache.D)
+    tp, B, M = _table(cache, page_table)
+    S = 0
+    for t in (mass, positions):
+        if t is not None:
+            S = t.shape[-1] if t.dim() == 3 else 0
+            if S < 1:
+                raise ValueError("mass and positions must be [B, H, S] tensors with S >= 1")
+    _paged_call("tq_append_paged", cache, _on(cache, K, "K", K.dtype, shape), _on(cache, V, "V", K.dtype, shape),
+                QTYPE[K.dtype], _on(cache, rows, "rows", torch.int32, (n, 3)), n, tp, B, M,
+                None if mass is None else _on(cache, mass, "mass", torch.float32, (B, cache.H, S)),
+                None if positions is None else _on(cache, positions, "positions", torch.int32, (B, cache.H, S)), S)
+
+
+def decode_paged_workspace_bytes(B: int, H: int, G: int, S: int, with_mass: bool) -> int:
+    return int(lib().tq_decode_paged_workspace_bytes(B, H, G, S, 1 if with_mass else 0))
+
+
+def decode_paged(Q, cache: PagedCache, page_table, lengths, mass=None, scale=None, workspace=None, out=None):
+    """Attention output of one new token per sequence over the paged cache.  Q [B,H*G,D]
+    fp32/bf16 (query head i reads KV head i // G); page_table int32 [B,max_pages], lengths
+    int32 [B].  mass fp32 [B,H,S] (optional): the weights each slot received, summed over its
+    group's queries, are added to it.  scale defaults to 1/sqrt(D).  Returns Q's shape and
+    type; zeros for a sequence of length 0."""
+    if not isinstance(Q, torch.Tensor) or Q.dim() != 3 or Q.dtype not in QTYPE:
+        raise ValueError("Q must be a [B, heads, D] fp32 or bf16 tensor")
+    tp, B, M = _table(cache, page_table)
+    H, D = cache.H, cache.D
+    heads = Q.shape[1]
+    if heads < H or heads % H:
+        raise ValueError(f"{heads} query heads over {H} KV heads")
+    G = heads // H
+    qp = _on(cache, Q, "Q", Q.dtype, (B, heads, D))
+    S, mp = 0, None
+    if mass is not None:
+        S = mass.shape[-1] if mass.dim() == 3 else 0
+        if S < 1:
+            raise ValueError("mass must be a [B, H, S] tensor with S >= 1")
+        mp = _on(cache, mass, "mass", torch.float32, (B, H, S))
+    ws, wp = _workspace_of(cache, workspace, 0 if workspace is not None else
+                           decode_paged_workspace_bytes(B, H, G, S, mass is not None))
+    if out is None:
+        out = torch.empty_like(Q)
+    _paged_call("tq_decode_paged", cache, qp, QTYPE[Q.dtype], tp, _on(cache, lengths, "lengths", torch.int32, (B,)),
+                B, G, M, 1.0 / D ** 0.5 if scale is None else float(scale), mp, S,
+                _on(cache, out, "out", Q.dtype, (B, heads, D)), wp, ws.numel())
+    return out
+
+
+def evict_paged_workspace_bytes(B: int, H: int, S: int, budget: int) -> int:
+    return int(lib().tq_evict_paged_workspace_bytes(B, H, S, budget))
+
+
+def evict_paged(cache: PagedCache, page_table, lengths, seen, mass, positions, budget, recent, workspace=None,
+                out=None):
+    """Cuts each sequence and KV head to min(length, budget) slots: first those whose position
+    is at least seen - recent, then by mass, ties to the lower slot.  Kept rows behind the
+    budget move to the slots given up.  lengths, seen int32 [B]; mass fp32, positions int32
+    [B,H,S].  Returns (mass, positions) of the slots as they are now (`out`, or new tensors of
+    0 and -1 behind the kept slots); `lengths` is the caller's to cut once all layers are done."""
+    tp, B, M = _table(cache, page_table)
+    if not isinstance(mass, torch.Tensor) or mass.dim() != 3:
+        raise ValueError("mass must be a [B, H, S] tensor")
+    shape = (B, cache.H, mass.shape[-1])
+    S = shape[2]
+    mp, pp = _on(cache, mass, "mass", torch.float32, shape), _on(cache, positions, "positions", torch.int32, shape)
+    budget, recent = max(-1, min(int(budget), S)), max(-1, min(int(recent), 2 ** 31 - 1))   # both fit an int
+    if out is None:
+        out = torch.zeros_like(mass), torch.full_like(positions, -1)
+    ws, wp = _workspace_of(cache, workspace, 0 if workspace is not None else
+                           evict_paged_workspace_bytes(B, cache.H, S, budget))
+    _paged_call("tq_evict_paged", cache, tp, _on(cache, lengths, "lengths", torch.int32, (B,)),
+                _on(cache, seen, "seen", torch.int32, (B,)), B, M, mp, pp, S, budget, recent,
+                _on(cache, out[0], "mass_out", torch.float32, shape),
+                _on(cache, out[1], "positions_out", torch.int32, shape), wp, ws.numel())
+    return out

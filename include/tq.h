@@ -83,8 +83,10 @@ tq_path tq_auto_path(int B, int D);
  * not compute and sets a fault bit on the device instead of hanging it.
  * tq_device_faults ORs into *bits the fault bits set on the CURRENT device since the
  * last call and clears them: 1 = fp32 lookup-table scorers, 2 = tensor-core scorer,
- * 4 = fused decode, 8 = compressor, 16 = tq_check_wait_expiry.  It synchronises with the device (it reads device
- * memory) and is not for use inside stream capture.  bits: host pointer, not NULL.
+ * 4 = fused decode, 8 = compressor, 16 = tq_check_wait_expiry, 32 = a paged call met a
+ * length, slot or page number out of range (see the paged cache below).  It synchronises
+ * with the device (it reads device memory) and is not for use inside stream capture.
+ * bits: host pointer, not NULL.
  * Errors: TQ_ERR_INVALID_VALUE (bits NULL), TQ_ERR_LAUNCH (the device read failed). */
 tq_status tq_device_faults(unsigned int* bits);
 
@@ -268,6 +270,107 @@ tq_status tq_decode_prod(const float* A, const float* T, const uint8_t* k_plane,
                          const uint16_t* v_norm, const float* v_codebook, int v_bits,
                          const float* Pi_v, float* out, int P, int H, int B, int S, int D,
                          float scale, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Paged cache of TurboQuant-MSE keys and values (kanthi.in §8 "Kernel view" for the row
+ * format, the tq_decode_mse format; paging, ragged lengths and eviction are this
+ * library's own and have no counterpart in the pages).
+ *
+ * The cache is n_pages pages of page_size rows for each of H KV heads:
+ *   k_plane [n_pages, H, page_size, D*k_bits/8] bytes, k_norm [n_pages, H, page_size] fp16,
+ *   v_plane [n_pages, H, page_size, D*v_bits/8] bytes, v_norm [n_pages, H, page_size] fp16,
+ * rows as in tq_scores_mse.  Pi_k, Pi_v: [rot_heads, D, D] fp32, KV head h uses rotation
+ * h % rot_heads.  k_codebook, v_codebook: 2^bits fp32 centroids, sorted ascending.
+ * The struct lives in HOST memory and is read during the call only.
+ *
+ * page_table [B, max_pages] int32: slot s of sequence b is row s % page_size of page
+ * page_table[b, s / page_size].  Entries behind a sequence's last page are not read.
+ * lengths [B] int32: slots in use.  A length outside [0, capacity] is cut to it (capacity:
+ * max_pages * page_size, and S where mass is given); a page number outside [0, n_pages)
+ * makes its slots absent.  Both set fault bit 32 (tq_device_faults) and read nothing out
+ * of range.
+ * mass [B, H, S] fp32 and positions [B, H, S] int32 go by slot, not by page: the
+ * attention weight each slot has received, and the number of its token.
+ *
+ * D == 128, k_bits and v_bits in {2,3,4}, page_size in {16,32,64,128,256}, H <= 65535,
+ * 1 <= rot_heads <= H.  Errors of the three calls: TQ_ERR_INVALID_VALUE (null pointer,
+ * size out of range), TQ_ERR_MISALIGNED, TQ_ERR_UNSUPPORTED (D or page_size),
+ * TQ_ERR_WORKSPACE, TQ_ERR_LAUNCH.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  uint8_t* k_plane;
+  uint16_t* k_norm;
+  uint8_t* v_plane;
+  uint16_t* v_norm;
+  const float* Pi_k;
+  const float* Pi_v;
+  const float* k_codebook;
+  const float* v_codebook;
+  int n_pages, H, page_size, D, k_bits, v_bits, rot_heads;
+} tq_paged_cache;
+
+/* ------------------------------------------------------------------------
+ * The write side: new tokens' keys and values are quantised and written to their slots.
+ *
+ * K, V: [n, H, D] of `type`.  rows: [n, 3] int32 (sequence, slot, position); a negative
+ * sequence or slot skips the row (padding), a sequence >= B or a slot outside the capacity
+ * (or a slot on an absent page) skips it too and sets fault bit 32.  For row i and head h
+ *   length = ||k||_2, rounded to fp16 (to nearest, infinity above 65504),
+ *   idx_d = number of codebook midpoints strictly below (Pi k / ||k||)_d, decided as in
+ *   64 bits (a coordinate near a midpoint is summed again in 64 bits; the rows of Pi are
+ *   taken as unit vectors there); a zero key takes the cells of 0, a key that holds a NaN
+ *   or an infinity takes cell 0 throughout;
+ * values likewise with Pi_v and the value codebook.  Where mass is given, mass[b,h,slot] =
+ * 0; where positions is given, positions[b,h,slot] = position; either may be NULL (S is
+ * then only checked against 0).  Two rows of one call must not name the same slot, nor two
+ * sequences the same page (the caller's contract: the row would mix both).  n >= 0.
+ * ---------------------------------------------------------------------- */
+tq_status tq_append_paged(const tq_paged_cache* cache, const void* K, const void* V, tq_qtype type,
+                          const int* rows, int n, const int* page_table, int B, int max_pages,
+                          float* mass, int* positions, int S, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Attention of one new token per sequence over the paged cache, split over the cache's
+ * length and joined, in the rotated domain (the paged form of tq_decode_mse):
+ *
+ *   s[i] = scale * nk_i * <Pi_k q, ck[kidx_i]>,  i < lengths[b]
+ *   p = softmax(s),  out = Pi_v^T sum_i p[i] nv_i cv[vidx_i]   (zeros for length 0)
+ *   mass[b, h, i] += sum of p[i] over the G queries of KV head h   (mass may be NULL)
+ *
+ * Q: [B, H*G, D] of `qtype`, query head h*G + g reads KV head h.  out: the same shape and
+ * type.  fp32 queries: every product to fp32 accuracy, |err| <= 1e-5 (1 + |out|) for value
+ * lengths of order one.  bf16 queries: products of fp16 operands (each rounded to 2^-11)
+ * summed in fp32, the output rounded to bf16; with mass the logits keep fp32 accuracy.
+ * The same inputs give the same bits.  Sequences may share pages.  scale: finite.
+ * workspace: at least tq_decode_paged_workspace_bytes(B, H, G, S, mass != NULL) bytes,
+ * scratch, not shared by concurrent calls or by graphs that may run concurrently.
+ * ---------------------------------------------------------------------- */
+size_t tq_decode_paged_workspace_bytes(int B, int H, int G, int S, int with_mass);
+tq_status tq_decode_paged(const tq_paged_cache* cache, const void* Q, tq_qtype qtype,
+                          const int* page_table, const int* lengths, int B, int G, int max_pages,
+                          float scale, float* mass, int S, void* out, void* workspace,
+                          size_t workspace_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Eviction by accumulated attention weight: every (sequence, KV head) keeps
+ * keep = min(lengths[b], budget) of its slots, in this order of preference: slots with
+ * positions >= seen[b] - recent; then by mass, larger first (NaN counts as minus infinity);
+ * then the lower slot.  Kept rows in slots >= keep move to the slots < keep that are given
+ * up, both in ascending order, so that the kept rows fill slots 0 .. keep-1 (attention does
+ * not depend on the order of slots) and nothing else of the cache is written.
+ * mass_out, positions_out [B, H, S]: slots < keep get the mass and position of the row that
+ * is there now, other slots stay as they were; neither may overlap mass or positions.
+ * seen: [B] int32, tokens of the sequence so far (a position is the number of a token).
+ * lengths is read only: the caller sets it to keep once every layer's cache is done.  The
+ * pages must belong to one sequence each.  1 <= budget, 0 <= recent.  workspace: at least
+ * tq_evict_paged_workspace_bytes(B, H, S, budget) bytes, scratch as above.
+ * ---------------------------------------------------------------------- */
+size_t tq_evict_paged_workspace_bytes(int B, int H, int S, int budget);
+tq_status tq_evict_paged(const tq_paged_cache* cache, const int* page_table, const int* lengths,
+                         const int* seen, int B, int max_pages, const float* mass,
+                         const int* positions, int S, int budget, int recent, float* mass_out,
+                         int* positions_out, void* workspace, size_t workspace_bytes,
+                         cudaStream_t stream);
 
 /* ------------------------------------------------------------------------
  * Fused query transform + scoring: the challenge's `solve` without its

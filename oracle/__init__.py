@@ -12,3 +12,4 @@ cases that reduce to a library routine, and brute force on small inputs (see
 ``tests/test_oracle_pins.py``).  No exported function is "parity unpinned".
 """
 from .tq_oracle import *  # noqa: F401,F403
+from . import paged  # noqa: F401  (the paged-cache operators)
