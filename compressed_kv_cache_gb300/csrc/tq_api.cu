@@ -369,7 +369,8 @@ tq_status tq_append_paged(const tq_paged_cache* cache, const void* K, const void
 }
 
 size_t tq_decode_paged_workspace_bytes(int B, int H, int G, int S, int with_mass) {
-  if (B < 1 || H < 1 || G < 1 || S < 0 || static_cast<int64_t>(B) * H * G > kMaxPagedQueries) return 0;
+  if (B < 1 || H < 1 || G < 1 || G > kMaxGridYZ || S < 0 || static_cast<int64_t>(B) * H * G > kMaxPagedQueries)
+    return 0;
   return tq::decode_paged_bytes(B, H, G, S, with_mass != 0);
 }
 
@@ -381,7 +382,7 @@ tq_status tq_decode_paged(const tq_paged_cache* cache, const void* Q, tq_qtype q
   if (st != TQ_OK) return st;
   if ((st = check_ptrs(Q, lengths, out)) != TQ_OK) return st;
   if (bad_optional(mass)) return TQ_ERR_MISALIGNED;
-  if (G < 1 || !std::isfinite(scale) || (qtype != TQ_Q_F32 && qtype != TQ_Q_BF16)) return TQ_ERR_INVALID_VALUE;
+  if (G < 1 || G > kMaxGridYZ || !std::isfinite(scale) || (qtype != TQ_Q_F32 && qtype != TQ_Q_BF16)) return TQ_ERR_INVALID_VALUE;
   if (mass != nullptr ? (S < 1 || S > INT_MAX - 4096) : S < 0) return TQ_ERR_INVALID_VALUE;
   if (static_cast<int64_t>(B) * cache->H * G > kMaxPagedQueries) return TQ_ERR_INVALID_VALUE;
   // the key tiles of all (sequence, head, query tile) units are counted in 32 bits

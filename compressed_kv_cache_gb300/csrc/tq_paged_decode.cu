@@ -1,5 +1,10 @@
-// Attention of one new token over the paged cache (tq_decode_paged).
-#include "tq_paged.cuh"
+// Attention of one new token over the paged cache (tq_decode_paged): four launches, each a
+// programmatic dependent of the one before.
+//   plan     a = Pi_k q for every query, and the tiles before each sequence
+//   split    tq_paged_split.cuh: a partial (maximum, sum, value sum) per run and unit
+//   combine  the partials of each query joined, out = Pi_v^T of it
+//   mass     where asked for: every slot's weights from its logits, added to mass
+#include "tq_paged_split.cuh"
 
 namespace tq {
 namespace {
@@ -9,117 +14,326 @@ __device__ __forceinline__ float load_q(const __nv_bfloat16* q, size_t i) { retu
 __device__ __forceinline__ void store_o(float* o, size_t i, float v) { o[i] = v; }
 __device__ __forceinline__ void store_o(__nv_bfloat16* o, size_t i, float v) { o[i] = __float2bfloat16_rn(v); }
 
-__device__ __forceinline__ unsigned code_at(const uint8_t* row, int bits, int d) {
-  const int at = bits * d;
-  unsigned w = row[at >> 3];
-  if ((at & 7) + bits > 8) w |= static_cast<unsigned>(row[(at >> 3) + 1]) << 8;
-  return (w >> (at & 7)) & ((1u << bits) - 1);
-}
+constexpr int kPlanThreads = 256;
+constexpr int kPlanRows = 32;        // rows of Pi_k a block takes
+constexpr int kPlanQ = 8;            // queries at a time
 
-// One block per (sequence, head): its queries in turn, the keys in tiles of 128, the softmax
-// with a running maximum and sum, fp32 throughout.  z keeps the logits where mass is asked for.
+// Block (unit, quarter): 32 rows of Pi_k against the unit's queries; a warp per row, the
+// row's 128 columns across its lanes.  The last block counts tiles.
 template <typename T>
-__global__ void __launch_bounds__(kPD)
-decode_simple_kernel(Paged pg, const T* __restrict__ Q, const int* __restrict__ lengths, int G,
-                     const float* __restrict__ Pik, const float* __restrict__ Piv,
-                     const float* __restrict__ kcb, const float* __restrict__ vcb, int kbits, int vbits,
-                     int rot, float scale, float* __restrict__ mass, int S, int cap, T* __restrict__ out,
-                     float* __restrict__ z) {
-  __shared__ float q[kPD], a[kPD], w[kPD], red[4], ck[16], cv[16];
-  __shared__ size_t rows[kPD];
-  const int b = blockIdx.x, h = blockIdx.y, d = threadIdx.x;
-  const int n = pg.length(lengths, b, cap);
-  if (d < 1 << kbits) ck[d] = kcb[d];
-  if (d < 1 << vbits) cv[d] = vcb[d];
-  const float* Pk = Pik + static_cast<size_t>(h % rot) * kPD * kPD;
-  const float* Pv = Piv + static_cast<size_t>(h % rot) * kPD * kPD;
-  for (int g = 0; g < G; ++g) {
-    const size_t qo = (static_cast<size_t>(b) * pg.H + h) * G + g;
-    float* zq = z == nullptr ? nullptr : z + qo * S;
-    __syncthreads();
-    q[d] = load_q(Q, qo * kPD + d);
-    __syncthreads();
-    float y = 0.f;
-    for (int j = 0; j < kPD; ++j) y = fmaf(Pk[d * kPD + j], q[j], y);
-    a[d] = y;
-    float M = -INFINITY, L = 0.f, acc = 0.f;
-    for (int s0 = 0; s0 < n; s0 += kPD) {
-      const int s = s0 + d;
-      __syncthreads();
-      float v = -INFINITY, nv = 0.f;
-      rows[d] = 0;
-      if (s < n) {
-        const int page = pg.page(b, s);
-        if (page >= 0) {
-          const size_t r = pg.row(page, h, s);
-          rows[d] = r;
-          const uint8_t* kr = pg.kp + r * 16 * kbits;
-          float t = 0.f;
-          for (int j = 0; j < kPD; ++j) t = fmaf(a[j], ck[code_at(kr, kbits, j)], t);
-          v = t * __half2float(__ushort_as_half(pg.kn[r])) * scale;
-          nv = __half2float(__ushort_as_half(pg.vn[r]));
+__global__ void __launch_bounds__(kPlanThreads)
+plan_kernel(const T* __restrict__ Q, const int* __restrict__ lengths, const float* __restrict__ Pik, int B, int H,
+            int G, int rot, int cap, float* __restrict__ A, int* __restrict__ tiles, int* __restrict__ cut) {
+  __shared__ __align__(16) float q[kPlanQ][kPD];
+  __shared__ int red[kPlanThreads / 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (blockIdx.x == gridDim.x - 1) {
+    int before = 0;
+    for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
+      const int b = b0 + tid;
+      int n = 0;
+      if (b < B) {
+        n = lengths[b];
+        if (n < 0 || n > cap) {
+          atomicOr(&g_wait_fault, static_cast<unsigned int>(kFaultPaged));
+          n = n < 0 ? 0 : cap;
         }
-        if (zq != nullptr) zq[s] = v;
+        cut[b] = n;
       }
-      float m = v;
-      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if ((d & 31) == 0) red[d >> 5] = m;
+      const int v = (n + kTile - 1) / kTile;
+      int x = v;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
       __syncthreads();
-      m = fmaxf(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])), M);
-      const float r = M > -INFINITY ? expf(M - m) : 0.f;
-      const float p = v > -INFINITY ? expf(v - m) : 0.f;
-      M = m;
-      w[d] = p > 0.f ? p * nv : 0.f;
-      float l = p;
-      for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      if (lane == 31) red[warp] = x;
       __syncthreads();
-      if ((d & 31) == 0) red[d >> 5] = l;
-      __syncthreads();
-      L = L * r + (red[0] + red[1] + red[2] + red[3]);
-      acc *= r;
-      const int cnt = min(kPD, n - s0);
-      for (int j = 0; j < cnt; ++j)
-        if (w[j] != 0.f) acc = fmaf(w[j], cv[code_at(pg.vp + rows[j] * 16 * vbits, vbits, d)], acc);
+      int pre = 0, all = 0;
+      for (int w = 0; w < kPlanThreads / 32; ++w) {
+        if (w < warp) pre += red[w];
+        all += red[w];
+      }
+      if (b < B) tiles[b] = before + pre + x - v;
+      before += all;
     }
+    if (tid == 0) tiles[B] = before;
+    return;
+  }
+  const int unit = blockIdx.x >> 2, row0 = (blockIdx.x & 3) * kPlanRows + warp * 4;
+  const int h = unit % H;
+  const float* P = Pik + (static_cast<size_t>(h % rot) * kPD + row0) * kPD + 4 * lane;
+  float4 m[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) m[r] = __ldg(reinterpret_cast<const float4*>(P + r * kPD));
+  for (int g0 = 0; g0 < G; g0 += kPlanQ) {
+    const int ng = min(kPlanQ, G - g0);
+    const size_t qo = (static_cast<size_t>(unit) * G + g0) * kPD;
     __syncthreads();
-    q[d] = L > 0.f ? acc / L : 0.f;
+    for (int e = tid; e < ng * kPD; e += kPlanThreads) q[e / kPD][e % kPD] = load_q(Q, qo + e);
     __syncthreads();
-    y = 0.f;
-    for (int j = 0; j < kPD; ++j) y = fmaf(Pv[j * kPD + d], q[j], y);
-    store_o(out, qo * kPD + d, y);
-    if (mass != nullptr && L > 0.f)
-      for (int s = d; s < n; s += kPD)
-        mass[(static_cast<size_t>(b) * pg.H + h) * S + s] += expf(zq[s] - M) / L;
+    for (int i = 0; i < ng; ++i) {
+      const float4 x = *reinterpret_cast<const float4*>(&q[i][4 * lane]);
+      float s[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s[r] = fmaf(m[r].x, x.x, fmaf(m[r].y, x.y, fmaf(m[r].z, x.z, m[r].w * x.w)));
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s[r] += __shfl_xor_sync(0xffffffffu, s[r], o);
+      }
+      if (lane == 0) *reinterpret_cast<float4*>(A + qo + i * kPD + row0) = make_float4(s[0], s[1], s[2], s[3]);
+    }
   }
 }
 
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinQ = 8;
+
+// Block (sequence and head, group of up to 8 queries): the partials of each query are read by
+// all warps, four coordinates a lane; then Pi_v is read once for the group.
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads)
+join_kernel(const float* __restrict__ part, const int* __restrict__ tiles, const float* __restrict__ Piv, int B, int H,
+            int G, int rot, int QT, int nqt, int W, int group, T* __restrict__ out, float* __restrict__ fin) {
+  __shared__ float wm[kJoinWarps], wl[kJoinWarps];
+  __shared__ __align__(16) float wacc[kJoinWarps][kPD];
+  __shared__ float norm[kJoinQ][kPD];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int bh = blockIdx.x, b = bh / H, h = bh - b * H, q0 = blockIdx.y * group;
+  const int nq = min(group, G - q0);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int per = H * nqt, T0 = tiles[b], nt = tiles[b + 1] - T0, total = tiles[B] * per;
+  const int rq = total / W, rr = total - rq * W;
+  for (int i = 0; i < nq; ++i) {
+    const int qi = q0 + i, j = qi / QT, c = qi - j * QT;
+    const int unit = b * per + h * nqt + j, t0 = T0 * per + (h * nqt + j) * nt;
+    float M = -INFINITY, Ls = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (nt > 0) {
+      const int first = run_of(t0, rq, rr), last = run_of(t0 + nt - 1, rq, rr);
+      constexpr int U = 4;
+      for (int w = first + warp; w <= last; w += kJoinWarps * U) {
+        float2 ml[U];
+        float4 x[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          const int wk = w + k * kJoinWarps;
+          if (wk <= last) {
+            const float* pp = part + (static_cast<size_t>(wk + unit) * QT + c) * kPartF;
+            ml[k] = *reinterpret_cast<const float2*>(pp + kPD);
+            x[k] = *reinterpret_cast<const float4*>(pp + 4 * lane);
+          } else {
+            ml[k] = make_float2(-INFINITY, 0.f);
+            x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+        }
+        float m = M;
+#pragma unroll
+        for (int k = 0; k < U; ++k) m = fmaxf(m, ml[k].x);
+        const float ref = m > -INFINITY ? m : 0.f;
+        const float r = exp2f(M - ref);                    // 0 while there is no weight
+        Ls *= r;
+        a.x *= r; a.y *= r; a.z *= r; a.w *= r;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          const float e = exp2f(ml[k].x - ref);
+          Ls = fmaf(ml[k].y, e, Ls);
+          a.x = fmaf(x[k].x, e, a.x);
+          a.y = fmaf(x[k].y, e, a.y);
+          a.z = fmaf(x[k].z, e, a.z);
+          a.w = fmaf(x[k].w, e, a.w);
+        }
+        M = m;
+      }
+    }
+    __syncthreads();
+    if (lane == 0) {
+      wm[warp] = M;
+      wl[warp] = Ls;
+    }
+    *reinterpret_cast<float4*>(&wacc[warp][4 * lane]) = a;
+    __syncthreads();
+    if (tid < kPD) {
+      float m = wm[0];
+      for (int w = 1; w < kJoinWarps; ++w) m = fmaxf(m, wm[w]);
+      const float ref = m > -INFINITY ? m : 0.f;
+      float s = 0.f, l = 0.f;
+      for (int w = 0; w < kJoinWarps; ++w) {
+        const float e = exp2f(wm[w] - ref);
+        s = fmaf(wacc[w][tid], e, s);
+        l = fmaf(wl[w], e, l);
+      }
+      norm[i][tid] = l != 0.f ? s / l : 0.f;               // no slot at all: zeros
+      if (fin != nullptr && tid == 0)
+        *reinterpret_cast<float2*>(fin + 2 * (static_cast<size_t>(bh) * G + qi)) = make_float2(ref, l != 0.f ? 1.f / l : 0.f);
+    }
+  }
+  __syncthreads();
+  // out[d] = sum_j norm[j] Pi_v[j][d]: two halves of the rows, one column a thread
+  const int d = tid & (kPD - 1), half = tid >> 7;
+  const float* P = Piv + static_cast<size_t>(h % rot) * kPD * kPD + d;
+  float o[kJoinQ];
+#pragma unroll
+  for (int i = 0; i < kJoinQ; ++i) o[i] = 0.f;
+  if (nq == 1) {
+#pragma unroll 16
+    for (int j = 64 * half; j < 64 * half + 64; ++j) o[0] = fmaf(norm[0][j], __ldg(P + j * kPD), o[0]);
+  } else {
+#pragma unroll 8
+    for (int j = 64 * half; j < 64 * half + 64; ++j) {
+      const float v = __ldg(P + j * kPD);
+#pragma unroll
+      for (int i = 0; i < kJoinQ; ++i)
+        if (i < nq) o[i] = fmaf(norm[i][j], v, o[i]);
+    }
+  }
+  __syncthreads();
+  float* both = &norm[0][0];
+  if (half == 1)
+    for (int i = 0; i < kJoinQ; ++i)
+      if (i < nq) both[i * kPD + d] = o[i];
+  __syncthreads();
+  if (half == 0)
+#pragma unroll
+    for (int i = 0; i < kJoinQ; ++i)
+      if (i < nq) store_o(out, (static_cast<size_t>(bh) * G + q0 + i) * kPD + d, o[i] + both[i * kPD + d]);
+}
+
+// mass[b,h,s] += sum over the group's queries of 2^(z - M) / L.  One thread a slot.
+__global__ void __launch_bounds__(256)
+mass_kernel(const float* __restrict__ z, const float* __restrict__ fin, const int* __restrict__ cut, int H, int G,
+            int QT, int nqt, int cap, int S, float* __restrict__ mass) {
+  const int chunks = (cap + 255) / 256;
+  const int bh = blockIdx.x / chunks, s = (blockIdx.x - bh * chunks) * 256 + threadIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (s >= cut[bh / H]) return;
+  float sum = 0.f;
+  for (int j = 0; j < nqt; ++j) {
+    const float* zs = z + (static_cast<size_t>(bh * nqt + j) * S + s) * QT;
+    for (int c0 = 0; c0 < QT; c0 += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(zs + c0);
+      const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int qi = j * QT + c0 + c;
+        if (qi < G) {
+          const float2 f = *reinterpret_cast<const float2*>(fin + 2 * (static_cast<size_t>(bh) * G + qi));
+          sum = fmaf(exp2f(x[c] - f.x), f.y, sum);
+        }
+      }
+    }
+  }
+  mass[static_cast<size_t>(bh) * S + s] += sum;
+}
+
+// Workspace: rotated queries, tiles, cut lengths, maxima and sums, partials, logits.
+struct Space {
+  size_t A, tiles, cut, fin, part, z, all;
+  Space(int B, int H, int G, int S, bool mass) {
+    const size_t units = static_cast<size_t>(B) * H;
+    size_t at = 0;
+    auto take = [&at](size_t bytes) { const size_t o = at; at += paged_round(bytes); return o; };
+    A = take(units * G * kPD * 4);
+    tiles = take((static_cast<size_t>(B) + 1) * 4);
+    cut = take(static_cast<size_t>(B) * 4);
+    fin = take(units * G * 8);
+    // query tiles of 8, or twice as many of 4: at most this many floats either way
+    part = take((kMaxCtas * kSplitWarps + units * ((G + 7) / 8)) * 8 * kPartF * 4);
+    z = take(mass ? units * (G <= 4 ? 4 : (G + 7) / 8 * 8) * static_cast<size_t>(S) * 4 : 0);
+    all = at;
+  }
+};
+
 template <typename T>
 cudaError_t launch(const tq_paged_cache& c, const T* Q, const int* table, const int* lengths, int B, int G,
-                   int max_pages, float scale, float* mass, int S, T* out, void* ws, cudaStream_t st) {
+                   int max_pages, float scale, float* mass, int S, T* out, char* ws, cudaStream_t st) {
+  static std::atomic<int> sms_cache[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int sms = sms_cache[dev & 63].load(std::memory_order_relaxed);
+  if (sms == 0) {
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    sms_cache[dev & 63].store(sms, std::memory_order_relaxed);
+  }
+  const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   int cap = max_pages * c.page_size;
   if (mass != nullptr && S < cap) cap = S;
-  decode_simple_kernel<T><<<dim3(B, c.H), kPD, 0, st>>>(
-      paged_view(c, table, max_pages), Q, lengths, G, c.Pi_k, c.Pi_v, c.k_codebook, c.v_codebook, c.k_bits,
-      c.v_bits, c.rot_heads, scale, mass, S, cap, out, mass != nullptr ? static_cast<float*>(ws) : nullptr);
-  return cudaGetLastError();
+  const bool f32 = sizeof(T) == 4;
+  const int variant = f32 ? kVarF32 : mass == nullptr ? kVarFast : G <= 4 ? kVarMass4 : kVarMass8;
+  const int QT = variant == kVarFast || variant == kVarMass8 ? 8 : 4, nqt = (G + QT - 1) / QT;
+  const Space sp(B, c.H, G, S, mass != nullptr);
+  float* A = reinterpret_cast<float*>(ws + sp.A);
+  int* tiles = reinterpret_cast<int*>(ws + sp.tiles);
+  int* cut = reinterpret_cast<int*>(ws + sp.cut);
+  float* fin = mass == nullptr ? nullptr : reinterpret_cast<float*>(ws + sp.fin);
+  float* part = reinterpret_cast<float*>(ws + sp.part);
+  float* z = mass == nullptr ? nullptr : reinterpret_cast<float*>(ws + sp.z);
+
+  plan_kernel<T><<<B * c.H * 4 + 1, kPlanThreads, 0, st>>>(Q, lengths, c.Pi_k, B, c.H, G, c.rot_heads, cap, A, tiles, cut);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const Paged pg = paged_view(c, table, max_pages);
+  const SplitArgs a = {c.k_plane, c.v_plane, c.k_norm, c.v_norm, table, c.n_pages, c.H, pg.shift, max_pages, A, tiles,
+                       cut, c.k_codebook, c.v_codebook, part, z, B, G, nqt, S, scale * 1.4426950408889634f};
+  switch (c.k_bits) {
+    case 2: e = launch_split_k2(a, c.v_bits, variant, ctas, st); break;
+    case 3: e = launch_split_k3(a, c.v_bits, variant, ctas, st); break;
+    default: e = launch_split_k4(a, c.v_bits, variant, ctas, st); break;
+  }
+  if (e != cudaSuccess) return e;
+
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // one query a block while that leaves SMs idle, up to 8 (Pi_v is then read once for them)
+  const int64_t queries = static_cast<int64_t>(B) * c.H * G;
+  int group = static_cast<int>(queries / (2 * sms));
+  group = group < 1 ? 1 : (group > kJoinQ ? kJoinQ : group);
+  group = group > G ? G : group;
+  cfg.gridDim = dim3(B * c.H, (G + group - 1) / group);
+  cfg.blockDim = dim3(kJoinThreads);
+  e = cudaLaunchKernelEx(&cfg, join_kernel<T>, static_cast<const float*>(part), static_cast<const int*>(tiles), c.Pi_v,
+                         B, c.H, G, c.rot_heads, QT, nqt, ctas * kSplitWarps, group, out, fin);
+  if (e != cudaSuccess || mass == nullptr) return e;
+  cfg.gridDim = dim3((cap + 255) / 256 * B * c.H);
+  cfg.blockDim = dim3(256);
+  return cudaLaunchKernelEx(&cfg, mass_kernel, static_cast<const float*>(z), static_cast<const float*>(fin),
+                            static_cast<const int*>(cut), c.H, G, QT, nqt, cap, S, mass);
 }
 
 }  // namespace
 
-size_t decode_paged_bytes(int B, int H, int G, int S, bool with_mass) {
-  return paged_round(with_mass ? static_cast<size_t>(B) * H * G * S * 4 : 256);
-}
+cudaError_t take_faults_split_k2(unsigned int* bits);
+cudaError_t take_faults_split_k3(unsigned int* bits);
+cudaError_t take_faults_split_k4(unsigned int* bits);
+
+size_t decode_paged_bytes(int B, int H, int G, int S, bool with_mass) { return Space(B, H, G, S, with_mass).all; }
 
 cudaError_t launch_decode_paged(const tq_paged_cache& c, const void* Q, tq_qtype qtype, const int* table,
                                 const int* lengths, int B, int G, int max_pages, float scale, float* mass,
                                 int S, void* out, void* ws, cudaStream_t st) {
   if (qtype == TQ_Q_F32)
     return launch(c, static_cast<const float*>(Q), table, lengths, B, G, max_pages, scale, mass, S,
-                  static_cast<float*>(out), ws, st);
+                  static_cast<float*>(out), static_cast<char*>(ws), st);
   return launch(c, static_cast<const __nv_bfloat16*>(Q), table, lengths, B, G, max_pages, scale, mass, S,
-                static_cast<__nv_bfloat16*>(out), ws, st);
+                static_cast<__nv_bfloat16*>(out), static_cast<char*>(ws), st);
 }
 
-cudaError_t take_faults_paged(unsigned int* bits) { return take_unit_faults(bits); }
+cudaError_t take_faults_paged(unsigned int* bits) {
+  cudaError_t e = take_unit_faults(bits);
+  if (e == cudaSuccess) e = take_faults_split_k2(bits);
+  if (e == cudaSuccess) e = take_faults_split_k3(bits);
+  if (e == cudaSuccess) e = take_faults_split_k4(bits);
+  return e;
+}
 
 }  // namespace tq

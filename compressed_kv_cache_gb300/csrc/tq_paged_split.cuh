@@ -1,0 +1,597 @@
+// The split of tq_decode_paged over the cache's length: logits, softmax and value sum of
+// one token per sequence, read straight from the packed codes of the pages.
+//
+// Work: the cache of every unit (sequence, KV head, query tile) in tiles of 32 slots, all
+// units end to end; every warp of the grid (one CTA of 16 warps per SM) takes an equal run of
+// that line (the tiles are counted on the device: lengths are not known to the host) and
+// leaves one partial (maximum, sum, weighted value sum) for each unit it touched.  No two
+// warps ever wait for each other.
+//
+// Products: mma.m16n8k16 (fp16 operands, fp32 sums) with the keys or values as the 16-row
+// operand and up to 8 queries as its 8 columns, so grouped heads cost what one head costs.
+// The 16-row operand is made in registers: two neighbouring codes select a pair of centroids
+// from a table in shared memory.  Every lane (every 16th with 8-byte entries) has a copy of the
+// table in its own banks, so a look-up never conflicts.  tcgen05 would need that operand
+// written to shared memory and read back (512 bytes a slot instead of none); at 4 to 8 queries
+// the tensor work is a small part either way.
+//
+// The order of the sum over coordinates and over slots is free, and is chosen for the loads:
+// lane (g, t) of a warp (g = lane / 4, t = lane % 4) takes coordinates 32t .. 32t+31 of two
+// keys (whole words of their rows), and coordinates 16g .. 16g+15 of four values.
+//
+// Precision: a factor x is an fp16 pair hi + lo (22 bits) where KX / VX ask for it; then
+// hi hi + hi lo + lo hi are summed.  COL: four queries, whose hi and lo parts are columns
+// 0..3 and 4..7 of one product.  Centroids, queries, and values' lengths are scaled by
+// powers of two to 2^7 before they become fp16, so that lo stays out of the subnormals.
+#pragma once
+
+#include "tq_paged.cuh"
+
+namespace tq {
+
+constexpr int kSplitWarps = 16;
+constexpr int kTile = 32;            // slots a warp takes at a time
+constexpr int kPartF = 132;          // partial of a query: 128 sums, maximum, sum, 2 unused
+constexpr int kMaxCtas = 192;        // partials are laid out for at most this many CTAs
+
+// A unit's share of the tiles is cut where the warps' runs are cut: run w covers
+// [w q + min(w, r), ...) of T = q W + r tiles.
+__host__ __device__ __forceinline__ int run_start(int w, int q, int r) { return w * q + (w < r ? w : r); }
+__device__ __forceinline__ int run_of(int tile, int q, int r) {
+  const int big = r * (q + 1);
+  return tile < big ? tile / (q + 1) : r + (tile - big) / q;
+}
+
+struct SplitArgs {
+  const uint8_t* kp;
+  const uint8_t* vp;
+  const uint16_t* kn;
+  const uint16_t* vn;
+  const int* table;
+  int n_pages, H, shift, max_pages;
+  const float* A;        // [B, H*G, 128] rotated queries
+  const int* tiles;      // [B + 1] tiles before each sequence
+  const int* lengths;    // [B] as cut by the plan
+  const float* kcb;
+  const float* vcb;
+  float* part;           // [runs + units][QT][kPartF]
+  float* z;              // [units][Sz][QT] logits times log2(e), or null
+  int B, G, nqt, Sz;
+  float scale2;          // scale * log2(e)
+};
+
+cudaError_t launch_split_k2(const SplitArgs& a, int vbits, int variant, int ctas, cudaStream_t st);
+cudaError_t launch_split_k3(const SplitArgs& a, int vbits, int variant, int ctas, cudaStream_t st);
+cudaError_t launch_split_k4(const SplitArgs& a, int vbits, int variant, int ctas, cudaStream_t st);
+
+// Variants: bf16 queries; bf16 with mass, up to 4 and up to 8 queries a unit; fp32.
+enum { kVarFast = 0, kVarMass4 = 1, kVarMass8 = 2, kVarF32 = 3 };
+
+#ifdef TQ_SPLIT_KERNEL
+namespace {
+
+template <int KB, int VB>
+struct Lay {
+  static constexpr int kTab = (1 << (2 * KB)) * 128;
+  static constexpr int vTab = (1 << (2 * VB)) * 128;
+  static constexpr int kBytes = kTile * 16 * KB, vBytes = kTile * 16 * VB;
+  static constexpr int norms = kBytes + vBytes;          // 32 fp16 of keys, 32 of values
+  static constexpr int mask = norms + 4 * kTile;         // which slots of the tile are there
+  static constexpr int stage = mask + 16;
+  static constexpr int room = 232448 - kTab - vTab;
+  static constexpr int fit = room / (kSplitWarps * stage);
+  static constexpr int stages = fit > 4 ? 4 : fit;       // tiles in flight or in use, per warp
+  static constexpr int bytes = kTab + vTab + kSplitWarps * stage * stages;
+  static_assert(stages >= 2, "two stages have to fit");
+};
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float lds_half(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return __half2float(__ushort_as_half(v));
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  return d;
+}
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float half_round(float x) { return __half2float(__float2half_rn(x)); }
+
+// Power of two that takes |x| = m to [2^7, 2^8) (1 for zero, infinity, NaN), and its inverse.
+__device__ __forceinline__ float scale_to_2p7(float m, float* inv) {
+  const int e = static_cast<int>((__float_as_uint(m) >> 23) & 255u);
+  if (e == 0 || e == 255) { *inv = 1.f; return 1.f; }
+  int k = 134 - e;                              // 2^(k) m lies in [2^7, 2^8)
+  k = k > 126 ? 126 : (k < -126 ? -126 : k);
+  *inv = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+  return __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+}
+
+// Table of centroid pairs: entry e = (c[e % 2^bits], c[e / 2^bits]) times `s`, 128 bytes of
+// copies each: 32 of the fp16 pair, or 16 of (pair of hi parts, pair of lo parts).
+template <int BITS, bool X>
+__device__ __forceinline__ void build_table(char* tab, const float* cb, float s) {
+  constexpr int n = 1 << (2 * BITS);
+  for (int e = threadIdx.x; e < n * 8; e += blockDim.x) {
+    const int i = e >> 3;
+    const float a = cb[i & ((1 << BITS) - 1)] * s, b = cb[i >> BITS] * s;
+    const uint32_t hi = pack2(a, b);
+    const uint32_t lo = X ? pack2(a - half_round(a), b - half_round(b)) : hi;
+    reinterpret_cast<uint4*>(tab)[e] = make_uint4(hi, lo, hi, lo);
+  }
+}
+
+// Byte offset (128 times the number) of the pair of codes at bit 2 * BITS * I of w, with
+// the lane's own bank offset in the low bits.
+template <int BITS, int I, int N>
+__device__ __forceinline__ uint32_t pair_at(const uint32_t (&w)[N], uint32_t lane_off) {
+  constexpr int at = 2 * BITS * I, wi = at / 32, sh = at % 32;
+  constexpr uint32_t m = ((1u << (2 * BITS)) - 1) << 7;
+  uint32_t x;
+  if constexpr (sh + 2 * BITS > 32) {
+    x = __funnelshift_r(w[wi], w[wi + 1], sh - 7);
+  } else if constexpr (sh >= 7) {
+    x = w[wi] >> (sh - 7);
+  } else {
+    x = w[wi] << (7 - sh);
+  }
+  return (x & m) | lane_off;
+}
+
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&w)[N], uint32_t a) {
+  if constexpr (N == 2) {
+    const uint2 v = lds64(a);
+    w[0] = v.x; w[1] = v.y;
+  } else if constexpr (N == 4) {
+    const uint4 v = lds128(a);
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = lds32(a + 4 * i);
+  }
+}
+
+// The 16 codes 16g .. 16g+15 of a value row, from bit 0 of w.
+template <int VB>
+__device__ __forceinline__ void load_value(uint32_t (&w)[2], uint32_t row, int g) {
+  if constexpr (VB == 2) {
+    w[0] = lds32(row + 4 * g);
+    w[1] = 0;
+  } else if constexpr (VB == 4) {
+    const uint2 v = lds64(row + 8 * g);
+    w[0] = v.x; w[1] = v.y;
+  } else {
+    const uint32_t a = row + ((6 * g) & ~3);
+    const uint32_t x = lds32(a), y = lds32(a + 4);
+    const int sh = (g & 1) * 16;
+    w[0] = __funnelshift_r(x, y, sh);
+    w[1] = y >> sh;
+  }
+}
+
+template <int KB, bool KX, int M>
+struct KeyProducts {
+  // Products of the coordinates of pairs 2M, 2M+1 and on, of two keys (rows g and g + 8).
+  template <int NB>
+  static __device__ __forceinline__ void run(float (&c)[4], float (&cl)[4], const uint32_t (&w0)[KB], const uint32_t (&w1)[KB],
+                                             uint32_t tab, uint32_t lo, const uint32_t (&q)[16], const uint32_t (&ql)[NB]) {
+    const uint32_t p0 = tab + pair_at<KB, 2 * M>(w0, lo), p1 = tab + pair_at<KB, 2 * M>(w1, lo);
+    const uint32_t p2 = tab + pair_at<KB, 2 * M + 1>(w0, lo), p3 = tab + pair_at<KB, 2 * M + 1>(w1, lo);
+    if constexpr (KX) {
+      const uint2 a0 = lds64(p0), a1 = lds64(p1), a2 = lds64(p2), a3 = lds64(p3);
+      mma(c, a0.x, a1.x, a2.x, a3.x, q[2 * M], q[2 * M + 1]);
+      mma(cl, a0.y, a1.y, a2.y, a3.y, q[2 * M], q[2 * M + 1]);
+      if constexpr (NB == 16) mma(cl, a0.x, a1.x, a2.x, a3.x, ql[2 * M], ql[2 * M + 1]);
+    } else {
+      mma(c, lds32(p0), lds32(p1), lds32(p2), lds32(p3), q[2 * M], q[2 * M + 1]);
+    }
+    if constexpr (M < 7) KeyProducts<KB, KX, M + 1>::run(c, cl, w0, w1, tab, lo, q, ql);
+  }
+};
+
+template <int VB, bool VX, int M>
+struct ValueProducts {
+  static __device__ __forceinline__ void run(float (&acc)[8][4], const uint32_t (&wa)[2], const uint32_t (&wb)[2],
+                                             const uint32_t (&wc)[2], const uint32_t (&wd)[2], uint32_t tab, uint32_t lo,
+                                             uint32_t b0, uint32_t b1) {
+    const uint32_t pa = tab + pair_at<VB, M>(wa, lo), pb = tab + pair_at<VB, M>(wb, lo);
+    const uint32_t pc = tab + pair_at<VB, M>(wc, lo), pd = tab + pair_at<VB, M>(wd, lo);
+    if constexpr (VX) {
+      const uint2 a = lds64(pa), b = lds64(pb), c = lds64(pc), d = lds64(pd);
+      mma(acc[M], __byte_perm(a.x, b.x, 0x5410), __byte_perm(a.x, b.x, 0x7632), __byte_perm(c.x, d.x, 0x5410),
+          __byte_perm(c.x, d.x, 0x7632), b0, b1);
+      mma(acc[M], __byte_perm(a.y, b.y, 0x5410), __byte_perm(a.y, b.y, 0x7632), __byte_perm(c.y, d.y, 0x5410),
+          __byte_perm(c.y, d.y, 0x7632), b0, b1);
+    } else {
+      const uint32_t a = lds32(pa), b = lds32(pb), c = lds32(pc), d = lds32(pd);
+      mma(acc[M], __byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632), __byte_perm(c, d, 0x5410),
+          __byte_perm(c, d, 0x7632), b0, b1);
+    }
+    if constexpr (M < 7) ValueProducts<VB, VX, M + 1>::run(acc, wa, wb, wc, wd, tab, lo, b0, b1);
+  }
+};
+
+// Largest b with tiles[b] * per <= t, by 32-way steps of the whole warp.
+__device__ __forceinline__ int find_sequence(const int* tiles, int B, int per, int t, int lane) {
+  int lo = 0, n = B;                                      // the answer lies in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int i = lane * step;
+    const bool le = i < n && tiles[lo + i] * per <= t;    // lane 0 always
+    const int k = 31 - __clz(__ballot_sync(0xffffffffu, le));
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  return lo;
+}
+
+template <int KB, int VB, bool KX, bool VX, bool COL>
+__global__ void __launch_bounds__(kSplitWarps * 32, 1)
+paged_split_kernel(const SplitArgs p) {
+  using L = Lay<KB, VB>;
+  constexpr int QT = COL ? 4 : 8;
+  constexpr int NL = (KX && !COL) ? 16 : 1;
+  extern __shared__ __align__(128) char smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+
+  // tables: inputs of the call, so they may be read before the plan is there
+  float kinv, vinv;
+  {
+    float mk = 0.f, mv = 0.f;
+    for (int i = 0; i < 1 << KB; ++i) mk = fmaxf(mk, fabsf(p.kcb[i]));
+    for (int i = 0; i < 1 << VB; ++i) mv = fmaxf(mv, fabsf(p.vcb[i]));
+    const float ks = scale_to_2p7(mk, &kinv), vs = scale_to_2p7(mv, &vinv);
+    build_table<KB, KX>(smem, p.kcb, ks);
+    build_table<VB, VX>(smem + L::kTab, p.vcb, vs);
+  }
+  __syncthreads();
+  const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+  const uint32_t ktab = base, vtab = base + L::kTab;
+  const uint32_t klo = KX ? (lane & 15) * 8 : lane * 4, vlo = VX ? (lane & 15) * 8 : lane * 4;
+  const uint32_t ring = base + L::kTab + L::vTab + warp * (L::stage * L::stages);
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int per = p.H * p.nqt;
+  const int T = p.tiles[p.B] * per;
+  const int W = gridDim.x * kSplitWarps;
+  const int run = warp * gridDim.x + blockIdx.x;          // short lines reach every SM
+  const int rq = T / W, rr = T % W;
+  const int end = run_start(run + 1, rq, rr);
+  for (int at = run_start(run, rq, rr); at < end;) {
+    const int b = find_sequence(p.tiles, p.B, per, at, lane);
+    const int first = p.tiles[b], nt = p.tiles[b + 1] - first;
+    const int in = at - first * per;
+    const int u = in / nt;                                 // (head, query tile) of the sequence
+    const int tile0 = in - u * nt;
+    const int tile1 = min(nt, tile0 + (end - at));
+    at += tile1 - tile0;
+    const int h = u / p.nqt, j = u - h * p.nqt;
+    const int n = p.lengths[b];
+    const int unit = b * per + u;
+    const int* table = p.table + static_cast<size_t>(b) * p.max_pages;
+
+    // queries: column g is query g (COL: g % 4; its hi part for g < 4, its lo part above)
+    uint32_t q[16], ql[NL];
+    float qinv;
+    {
+      const int qi = j * QT + (COL ? (g & 3) : g);
+      const float4* src = reinterpret_cast<const float4*>(
+          p.A + (static_cast<size_t>(b * p.H + h) * p.G + min(qi, p.G - 1)) * kPD + 32 * t);
+      float x[32], m = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 v = src[i];
+        x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(x[i]));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      float s = scale_to_2p7(m, &qinv);
+      if (qi >= p.G) s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float a = x[2 * i] * s, c = x[2 * i + 1] * s;
+        const float al = a - half_round(a), cl = c - half_round(c);
+        if constexpr (COL) q[i] = g < 4 ? pack2(a, c) : pack2(al, cl);
+        else q[i] = pack2(a, c);
+        if constexpr (NL == 16) ql[i] = pack2(al, cl);
+      }
+      if (qi >= p.G) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          q[i] = 0;
+          if constexpr (NL == 16) ql[i] = 0;
+        }
+      }
+    }
+    // logit factors of columns 2t and 2t + 1 (COL: of their queries)
+    const int c0 = COL ? 2 * (t & 1) : 2 * t;
+    const float f0 = __shfl_sync(0xffffffffu, qinv, 4 * c0) * kinv * p.scale2;
+    const float f1 = __shfl_sync(0xffffffffu, qinv, 4 * (c0 + 1)) * kinv * p.scale2;
+
+    float acc[8][4];
+#pragma unroll
+    for (int m = 0; m < 8; ++m) acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float vs = 0.f, vsinv = 0.f, vtop = 0.f;               // values' lengths: scale, inverse, largest so far
+    float* zrow = p.z == nullptr ? nullptr : p.z + (static_cast<size_t>(unit) * p.Sz) * QT;
+
+    // a tile is two runs of 16 rows, each on one page
+    int pg0 = -1, pg1 = -1;
+    auto look_up = [&](int tile) {
+      const int s = tile * kTile;
+      pg0 = tile < tile1 ? table[s >> p.shift] : -1;
+      pg1 = tile < tile1 && s + 16 < n ? table[(s + 16) >> p.shift] : -1;
+    };
+    auto issue = [&](int tile, uint32_t st) {
+      if (tile < tile1) {
+        const int s = tile * kTile, in_page = s & ((1 << p.shift) - 1), in_page1 = (s + 16) & ((1 << p.shift) - 1);
+        const bool ok0 = static_cast<unsigned>(pg0) < static_cast<unsigned>(p.n_pages);
+        const bool ok1 = static_cast<unsigned>(pg1) < static_cast<unsigned>(p.n_pages);
+        const size_t r0 = ((static_cast<size_t>(ok0 ? pg0 : 0) * p.H + h) << p.shift) + in_page;
+        const size_t r1 = ((static_cast<size_t>(ok1 ? pg1 : 0) * p.H + h) << p.shift) + in_page1;
+#pragma unroll
+        for (int i = 0; i < KB; ++i) {
+          const int c = i * 32 + lane;
+          const bool second = c >= 16 * KB;
+          if (second ? ok1 : ok0)
+            cp16(st + c * 16, p.kp + (second ? r1 : r0) * (16 * KB) + (second ? c - 16 * KB : c) * 16);
+        }
+#pragma unroll
+        for (int i = 0; i < VB; ++i) {
+          const int c = i * 32 + lane;
+          const bool second = c >= 16 * VB;
+          if (second ? ok1 : ok0)
+            cp16(st + L::kBytes + c * 16, p.vp + (second ? r1 : r0) * (16 * VB) + (second ? c - 16 * VB : c) * 16);
+        }
+        {
+          const int k = 2 * (lane & 15);
+          const bool second = k >= 16;
+          if (second ? ok1 : ok0)
+            cp4(st + L::norms + lane * 4, (lane < 16 ? p.kn : p.vn) + (second ? r1 : r0) + (k & 15));
+        }
+        if (lane == 0) {
+          const int left = n - s;
+          uint32_t there = left >= 32 ? 0xffffffffu : (1u << left) - 1;
+          if (!ok0) there &= 0xffff0000u;
+          if (!ok1) there &= 0x0000ffffu;
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(st + L::mask), "r"(there) : "memory");
+          if (!ok0 || (left > 16 && !ok1)) atomicOr(&g_wait_fault, static_cast<unsigned int>(kFaultPaged));
+        }
+        look_up(tile + 1);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    __syncwarp();                                          // the ring is free
+    look_up(tile0);
+#pragma unroll
+    for (int i = 0; i < L::stages - 1; ++i) issue(tile0 + i, ring + i * L::stage);
+    int rs = 0, ws = L::stages - 1;
+    for (int tile = tile0; tile < tile1; ++tile) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(L::stages - 2) : "memory");
+      __syncwarp();
+      issue(tile + L::stages - 1, ring + ws * L::stage);
+      ws = ws + 1 == L::stages ? 0 : ws + 1;
+      const uint32_t st = ring + rs * L::stage;
+      rs = rs + 1 == L::stages ? 0 : rs + 1;
+
+      const uint32_t there = lds32(st + L::mask);
+      const int r0 = (g >> 1) + (g & 1) * 4;               // row g of the product is this key of its 8
+      float z[2][4];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        uint32_t w0[KB], w1[KB];
+        load_words(w0, st + (16 * mt + r0) * (16 * KB) + t * 4 * KB);
+        load_words(w1, st + (16 * mt + 8 + r0) * (16 * KB) + t * 4 * KB);
+        float c[4] = {0.f, 0.f, 0.f, 0.f}, cl[4] = {0.f, 0.f, 0.f, 0.f};
+        KeyProducts<KB, KX, 0>::run(c, cl, w0, w1, ktab, klo, q, ql);
+        if constexpr (KX) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) c[i] += cl[i];
+        }
+        if constexpr (COL) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) c[i] += __shfl_xor_sync(0xffffffffu, c[i], 2);
+        }
+        const int ka = 16 * mt + r0, kb = ka + 8;
+        const float na = lds_half(st + L::norms + 2 * ka), nb = lds_half(st + L::norms + 2 * kb);
+        const bool ha = (there >> ka) & 1, hb = (there >> kb) & 1;
+        z[mt][0] = ha ? c[0] * na * f0 : -INFINITY;
+        z[mt][1] = ha ? c[1] * na * f1 : -INFINITY;
+        z[mt][2] = hb ? c[2] * nb * f0 : -INFINITY;
+        z[mt][3] = hb ? c[3] * nb * f1 : -INFINITY;
+        if (zrow != nullptr && (!COL || t < 2)) {
+          float* zt = zrow + static_cast<size_t>(tile * kTile) * QT + c0;
+          if (tile * kTile + ka < n) *reinterpret_cast<float2*>(zt + ka * QT) = make_float2(z[mt][0], z[mt][1]);
+          if (tile * kTile + kb < n) *reinterpret_cast<float2*>(zt + kb * QT) = make_float2(z[mt][2], z[mt][3]);
+        }
+      }
+      // The running maximum moves only when a logit passes it by 2^8 (so weights stay below
+      // 2^8 and their fp16 form below 2^16), which is rare after the first tiles.
+      const float nv = ((there >> lane) & 1) ? lds_half(st + L::norms + 64 + 2 * lane) : 0.f;
+      const float z0 = fmaxf(fmaxf(z[0][0], z[0][2]), fmaxf(z[1][0], z[1][2]));
+      const float z1 = fmaxf(fmaxf(z[0][1], z[0][3]), fmaxf(z[1][1], z[1][3]));
+      if (__any_sync(0xffffffffu, z0 > m0 + 8.f || z1 > m1 + 8.f || nv > vtop)) {
+        float a = z0, c = z1, v = nv;
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+          c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, o));
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+        a = fmaxf(a, m0);
+        c = fmaxf(c, m1);
+        const float e0 = m0 > -INFINITY ? ex2(m0 - a) : 0.f, e1 = m1 > -INFINITY ? ex2(m1 - c) : 0.f;
+        m0 = a;
+        m1 = c;
+        l0 *= e0;
+        l1 *= e1;
+        float r = 1.f;
+        if (v > vtop) {                                    // to the next power of two, and no further this way
+          float inv;
+          const float s = scale_to_2p7(v, &inv) * 0.5f;    // lengths up to 2^7 after it
+          r = vs > 0.f ? s * vsinv : 0.f;
+          vs = s;
+          vsinv = 2.f * inv;
+          vtop = __uint_as_float(__float_as_uint(v) | 0x7fffffu);
+        }
+        const float x0 = e0 * r, x1 = e1 * r;
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+          acc[m][0] *= x0;
+          acc[m][1] *= x1;
+          acc[m][2] *= x0;
+          acc[m][3] *= x1;
+        }
+      }
+      const float s0 = m0 > -INFINITY ? m0 : 0.f, s1 = m1 > -INFINITY ? m1 : 0.f;
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        const int ka = 16 * mt + r0, kb = ka + 8;
+        const float va = __shfl_sync(0xffffffffu, nv, ka) * vs, vb = __shfl_sync(0xffffffffu, nv, kb) * vs;
+        const float p0 = ex2(z[mt][0] - s0), p1 = ex2(z[mt][1] - s1), p2 = ex2(z[mt][2] - s0), p3 = ex2(z[mt][3] - s1);
+        l0 += p0 + p2;
+        l1 += p1 + p3;
+        float w0 = p0 * va, w1 = p1 * va, w2 = p2 * vb, w3 = p3 * vb;
+        if constexpr (COL) {
+          if (t >= 2) {
+            w0 -= half_round(w0);
+            w1 -= half_round(w1);
+            w2 -= half_round(w2);
+            w3 -= half_round(w3);
+          }
+        }
+        const uint32_t b0 = transpose8x8(pack2(w0, w1)), b1 = transpose8x8(pack2(w2, w3));
+        // slots 2t and 2t + 1 of the product are keys t and t + 4 of their 8
+        const uint32_t row = st + L::kBytes + (16 * mt + t) * (16 * VB);
+        uint32_t wa[2], wb[2], wc[2], wd[2];
+        load_value<VB>(wa, row, g);
+        load_value<VB>(wb, row + 4 * 16 * VB, g);
+        load_value<VB>(wc, row + 8 * 16 * VB, g);
+        load_value<VB>(wd, row + 12 * 16 * VB, g);
+        ValueProducts<VB, VX, 0>::run(acc, wa, wb, wc, wd, vtab, vlo, b0, b1);
+      }
+    }
+
+    // this warp's partial of the unit
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, o);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+    }
+    if constexpr (COL) {
+#pragma unroll
+      for (int m = 0; m < 8; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][i] += __shfl_xor_sync(0xffffffffu, acc[m][i], 2);
+    }
+    const float fin = vs > 0.f ? vsinv * vinv : 0.f;
+    float* part = p.part + static_cast<size_t>(run + unit) * (QT * kPartF);
+    const int live = min(QT, p.G - j * QT);
+    if (!COL || t < 2) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (c0 + i < live) {
+          float* o = part + (c0 + i) * kPartF;
+          float4* o4 = reinterpret_cast<float4*>(o + 16 * g);
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            o4[m] = make_float4(acc[2 * m][i] * fin, acc[2 * m][2 + i] * fin, acc[2 * m + 1][i] * fin,
+                                acc[2 * m + 1][2 + i] * fin);
+          if (g == 0) *reinterpret_cast<float2*>(o + kPD) = make_float2(i ? m1 : m0, i ? l1 : l0);
+        }
+      }
+    }
+  }
+}
+
+template <int KB, int VB, bool KX, bool VX, bool COL>
+cudaError_t launch_one(const SplitArgs& a, int ctas, cudaStream_t st) {
+  auto kernel = paged_split_kernel<KB, VB, KX, VX, COL>;
+  static std::atomic<uint64_t> configured{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(configured.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<KB, VB>::bytes);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kSplitWarps * 32);
+  cfg.dynamicSmemBytes = Lay<KB, VB>::bytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <int KB, int VB>
+cudaError_t launch_variant(const SplitArgs& a, int variant, int ctas, cudaStream_t st) {
+  switch (variant) {
+    case kVarFast: return launch_one<KB, VB, false, false, false>(a, ctas, st);
+    case kVarMass4: return launch_one<KB, VB, true, false, true>(a, ctas, st);
+    case kVarMass8: return launch_one<KB, VB, true, false, false>(a, ctas, st);
+    default: return launch_one<KB, VB, true, true, true>(a, ctas, st);
+  }
+}
+
+template <int KB>
+cudaError_t launch_split(const SplitArgs& a, int vbits, int variant, int ctas, cudaStream_t st) {
+  switch (vbits) {
+    case 2: return launch_variant<KB, 2>(a, variant, ctas, st);
+    case 3: return launch_variant<KB, 3>(a, variant, ctas, st);
+    default: return launch_variant<KB, 4>(a, variant, ctas, st);
+  }
+}
+
+}  // namespace
+#endif  // TQ_SPLIT_KERNEL
+
+}  // namespace tq
