@@ -115,6 +115,7 @@ tq_status check_paged(const tq_paged_cache* c, const int* page_table, int B, int
     return TQ_ERR_INVALID_VALUE;
   if (c->k_bits < 2 || c->k_bits > 4 || c->v_bits < 2 || c->v_bits > 4 || c->D < 1 || c->page_size < 1)
     return TQ_ERR_INVALID_VALUE;
+  if (static_cast<int64_t>(c->n_pages) * c->H > INT_MAX) return TQ_ERR_INVALID_VALUE;
   if (c->D != 128) return TQ_ERR_UNSUPPORTED;
   const int ps = c->page_size;
   if (ps < 16 || ps > 256 || (ps & (ps - 1)) != 0) return TQ_ERR_UNSUPPORTED;

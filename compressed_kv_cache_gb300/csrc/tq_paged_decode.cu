@@ -88,23 +88,31 @@ plan_kernel(const T* __restrict__ Q, const int* __restrict__ lengths, const floa
   }
 }
 
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 512;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kJoinQ = 8;
+constexpr int kJoinSlots = 8;        // partials a warp has in flight
 
-// Block (sequence and head, group of up to 8 queries): the partials of each query are read by
-// all warps, four coordinates a lane; then Pi_v is read once for the group.
+// Block (sequence and head, group of up to 8 queries).  Thread (r, d) of 4 x 128 holds rows
+// 32r .. 32r+31 of column d of Pi_v, requested before the wait for the split.  The partials
+// of each query are read by all warps, eight in flight a warp, four coordinates a lane.
 template <typename T>
 __global__ void __launch_bounds__(kJoinThreads)
 join_kernel(const float* __restrict__ part, const int* __restrict__ tiles, const float* __restrict__ Piv, int B, int H,
             int G, int rot, int QT, int nqt, int W, int group, T* __restrict__ out, float* __restrict__ fin) {
+  constexpr int kRows = kPD * kPD / kJoinThreads;
   __shared__ float wm[kJoinWarps], wl[kJoinWarps];
   __shared__ __align__(16) float wacc[kJoinWarps][kPD];
-  __shared__ float norm[kJoinQ][kPD];
+  __shared__ __align__(16) float norm[kPD];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int bh = blockIdx.x, b = bh / H, h = bh - b * H, q0 = blockIdx.y * group;
   const int nq = min(group, G - q0);
+  const int d = tid & (kPD - 1), r = tid / kPD;
+  const float* P = Piv + (static_cast<size_t>(h % rot) * kPD + r * kRows) * kPD + d;
+  float pv[kRows];
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) pv[k] = __ldg(P + k * kPD);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int per = H * nqt, T0 = tiles[b], nt = tiles[b + 1] - T0, total = tiles[B] * per;
   const int rq = total / W, rr = total - rq * W;
@@ -115,12 +123,11 @@ join_kernel(const float* __restrict__ part, const int* __restrict__ tiles, const
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     if (nt > 0) {
       const int first = run_of(t0, rq, rr), last = run_of(t0 + nt - 1, rq, rr);
-      constexpr int U = 4;
-      for (int w = first + warp; w <= last; w += kJoinWarps * U) {
-        float2 ml[U];
-        float4 x[U];
+      for (int w = first + warp; w <= last; w += kJoinWarps * kJoinSlots) {
+        float2 ml[kJoinSlots];
+        float4 x[kJoinSlots];
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
+        for (int k = 0; k < kJoinSlots; ++k) {
           const int wk = w + k * kJoinWarps;
           if (wk <= last) {
             const float* pp = part + (static_cast<size_t>(wk + unit) * QT + c) * kPartF;
@@ -133,13 +140,13 @@ join_kernel(const float* __restrict__ part, const int* __restrict__ tiles, const
         }
         float m = M;
 #pragma unroll
-        for (int k = 0; k < U; ++k) m = fmaxf(m, ml[k].x);
+        for (int k = 0; k < kJoinSlots; ++k) m = fmaxf(m, ml[k].x);
         const float ref = m > -INFINITY ? m : 0.f;
-        const float r = exp2f(M - ref);                    // 0 while there is no weight
-        Ls *= r;
-        a.x *= r; a.y *= r; a.z *= r; a.w *= r;
+        const float f = exp2f(M - ref);                    // 0 while there is no weight
+        Ls *= f;
+        a.x *= f; a.y *= f; a.z *= f; a.w *= f;
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
+        for (int k = 0; k < kJoinSlots; ++k) {
           const float e = exp2f(ml[k].x - ref);
           Ls = fmaf(ml[k].y, e, Ls);
           a.x = fmaf(x[k].x, e, a.x);
@@ -150,7 +157,6 @@ join_kernel(const float* __restrict__ part, const int* __restrict__ tiles, const
         M = m;
       }
     }
-    __syncthreads();
     if (lane == 0) {
       wm[warp] = M;
       wl[warp] = Ls;
@@ -159,48 +165,35 @@ join_kernel(const float* __restrict__ part, const int* __restrict__ tiles, const
     __syncthreads();
     if (tid < kPD) {
       float m = wm[0];
+#pragma unroll
       for (int w = 1; w < kJoinWarps; ++w) m = fmaxf(m, wm[w]);
       const float ref = m > -INFINITY ? m : 0.f;
       float s = 0.f, l = 0.f;
+#pragma unroll
       for (int w = 0; w < kJoinWarps; ++w) {
         const float e = exp2f(wm[w] - ref);
         s = fmaf(wacc[w][tid], e, s);
         l = fmaf(wl[w], e, l);
       }
-      norm[i][tid] = l != 0.f ? s / l : 0.f;               // no slot at all: zeros
+      norm[tid] = l != 0.f ? s / l : 0.f;                  // no slot at all: zeros
       if (fin != nullptr && tid == 0)
         *reinterpret_cast<float2*>(fin + 2 * (static_cast<size_t>(bh) * G + qi)) = make_float2(ref, l != 0.f ? 1.f / l : 0.f);
     }
-  }
-  __syncthreads();
-  // out[d] = sum_j norm[j] Pi_v[j][d]: two halves of the rows, one column a thread
-  const int d = tid & (kPD - 1), half = tid >> 7;
-  const float* P = Piv + static_cast<size_t>(h % rot) * kPD * kPD + d;
-  float o[kJoinQ];
+    __syncthreads();
+    float o = 0.f;
 #pragma unroll
-  for (int i = 0; i < kJoinQ; ++i) o[i] = 0.f;
-  if (nq == 1) {
-#pragma unroll 16
-    for (int j = 64 * half; j < 64 * half + 64; ++j) o[0] = fmaf(norm[0][j], __ldg(P + j * kPD), o[0]);
-  } else {
-#pragma unroll 8
-    for (int j = 64 * half; j < 64 * half + 64; ++j) {
-      const float v = __ldg(P + j * kPD);
-#pragma unroll
-      for (int i = 0; i < kJoinQ; ++i)
-        if (i < nq) o[i] = fmaf(norm[i][j], v, o[i]);
+    for (int k = 0; k < kRows; k += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(&norm[r * kRows + k]);
+      o = fmaf(v.x, pv[k], o);
+      o = fmaf(v.y, pv[k + 1], o);
+      o = fmaf(v.z, pv[k + 2], o);
+      o = fmaf(v.w, pv[k + 3], o);
     }
+    wacc[r][d] = o;
+    __syncthreads();
+    if (r == 0) store_o(out, (static_cast<size_t>(bh) * G + qi) * kPD + d, wacc[0][d] + wacc[1][d] + wacc[2][d] + wacc[3][d]);
+    __syncthreads();
   }
-  __syncthreads();
-  float* both = &norm[0][0];
-  if (half == 1)
-    for (int i = 0; i < kJoinQ; ++i)
-      if (i < nq) both[i * kPD + d] = o[i];
-  __syncthreads();
-  if (half == 0)
-#pragma unroll
-    for (int i = 0; i < kJoinQ; ++i)
-      if (i < nq) store_o(out, (static_cast<size_t>(bh) * G + q0 + i) * kPD + d, o[i] + both[i * kPD + d]);
 }
 
 // mass[b,h,s] += sum over the group's queries of 2^(z - M) / L.  One thread a slot.
@@ -279,7 +272,8 @@ cudaError_t launch(const tq_paged_cache& c, const T* Q, const int* table, const 
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const Paged pg = paged_view(c, table, max_pages);
   const SplitArgs a = {c.k_plane, c.v_plane, c.k_norm, c.v_norm, table, c.n_pages, c.H, pg.shift, max_pages, A, tiles,
-                       cut, c.k_codebook, c.v_codebook, part, z, B, G, nqt, S, scale * 1.4426950408889634f};
+                       cut, c.k_codebook, c.v_codebook, part, z, B, G, nqt, S, scale * 1.4426950408889634f,
+                       {1, 2, 4, 8, 16, 32, 64, 128}};
   switch (c.k_bits) {
     case 2: e = launch_split_k2(a, c.v_bits, variant, ctas, st); break;
     case 3: e = launch_split_k3(a, c.v_bits, variant, ctas, st); break;

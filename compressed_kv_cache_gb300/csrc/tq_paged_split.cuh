@@ -58,6 +58,7 @@ struct SplitArgs {
   float* z;              // [units][Sz][QT] logits times log2(e), or null
   int B, G, nqt, Sz;
   float scale2;          // scale * log2(e)
+  uint32_t pow2[8];      // 1, 2, 4 ... 128
 };
 
 cudaError_t launch_split_k2(const SplitArgs& a, int vbits, int variant, int ctas, cudaStream_t st);
@@ -70,18 +71,22 @@ enum { kVarFast = 0, kVarMass4 = 1, kVarMass8 = 2, kVarF32 = 3 };
 #ifdef TQ_SPLIT_KERNEL
 namespace {
 
+// Shared memory: the two tables, each at an address that is a multiple of its size (so that an
+// entry's address is made by one AND-OR), the larger one first; the warps' rings of stages in
+// what is left before and behind them.
 template <int KB, int VB>
 struct Lay {
-  static constexpr int kTab = (1 << (2 * KB)) * 128;
-  static constexpr int vTab = (1 << (2 * VB)) * 128;
+  static constexpr int kTab = (1 << (2 * KB)) * 128, vTab = (1 << (2 * VB)) * 128;
+  static constexpr int big = kTab > vTab ? kTab : vTab;
   static constexpr int kBytes = kTile * 16 * KB, vBytes = kTile * 16 * VB;
   static constexpr int norms = kBytes + vBytes;          // 32 fp16 of keys, 32 of values
   static constexpr int mask = norms + 4 * kTile;         // which slots of the tile are there
   static constexpr int stage = mask + 16;
-  static constexpr int room = 232448 - kTab - vTab;
-  static constexpr int fit = room / (kSplitWarps * stage);
+  static constexpr int bytes = 232448;                   // all a CTA can have
+  // 17 rings: the room before the tables may be cut short of one
+  static constexpr int fit = (bytes - kTab - vTab) / ((kSplitWarps + 1) * stage);
   static constexpr int stages = fit > 4 ? 4 : fit;       // tiles in flight or in use, per warp
-  static constexpr int bytes = kTab + vTab + kSplitWarps * stage * stages;
+  static constexpr int ring = stage * stages;
   static_assert(stages >= 2, "two stages have to fit");
 };
 
@@ -95,6 +100,17 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
+// Table entries: the tables never change, so these may move freely.
+__device__ __forceinline__ uint32_t lds32t(uint32_t a) {
+  uint32_t v;
+  asm("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64t(uint32_t a) {
+  uint2 v;
+  asm("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
@@ -105,11 +121,12 @@ __device__ __forceinline__ float lds_half(uint32_t a) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
   return __half2float(__ushort_as_half(v));
 }
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// Copies of 16 and 4 bytes; nothing is read where ok is false (zeros are written).
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -127,6 +144,14 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same with sums that begin at zero.
+__device__ __forceinline__ void mma0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                     uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -158,21 +183,46 @@ __device__ __forceinline__ void build_table(char* tab, const float* cb, float s)
   }
 }
 
-// Byte offset (128 times the number) of the pair of codes at bit 2 * BITS * I of w, with
-// the lane's own bank offset in the low bits.
-template <int BITS, int I, int N>
-__device__ __forceinline__ uint32_t pair_at(const uint32_t (&w)[N], uint32_t lane_off) {
-  constexpr int at = 2 * BITS * I, wi = at / 32, sh = at % 32;
-  constexpr uint32_t m = ((1u << (2 * BITS)) - 1) << 7;
-  uint32_t x;
-  if constexpr (sh + 2 * BITS > 32) {
-    x = __funnelshift_r(w[wi], w[wi + 1], sh - 7);
-  } else if constexpr (sh >= 7) {
-    x = w[wi] >> (sh - 7);
-  } else {
-    x = w[wi] << (7 - sh);
+// Codes are read in words of `kCodes`: 16 two-bit codes or 8 wider ones (24 bits of 3-bit
+// codes), of which two neighbouring ones make a field, the number of an entry of the table.
+template <int BITS>
+struct Word {
+  static constexpr int kCodes = BITS == 2 ? 16 : 8;
+  static constexpr int kFields = kCodes / 2;
+  static constexpr int kWidth = 2 * BITS;
+  static constexpr uint32_t kMask = ((1u << kWidth) - 1) << 7;
+
+  // Addresses of the fields' entries: field i moved to bits 7 and up, the table's address and
+  // the lane's bank offset around it.  Shifts to the left are products with a number the compiler does not know,
+  // which run on the FMA pipe: the kernel is bound by the ALU pipe, which would take them all
+  // (131072 slots, 3-bit: see the kernel).
+  static __device__ __forceinline__ void offsets(uint32_t w, uint32_t lane_off, const SplitArgs& p, uint32_t (&o)[kFields]) {
+#pragma unroll
+    for (int i = kFields - 1; i >= 0; --i) {
+      const int at = kWidth * i;
+      uint32_t x;
+      if (at < 7) {
+        x = w * p.pow2[7 - at];
+      } else if (kWidth < 7 && (i & 1) == 0) {            // the next field's shift, and back by one field
+        x = (w >> (at + kWidth - 7)) * p.pow2[kWidth];
+      } else {
+        x = w >> (at - 7);
+      }
+      o[i] = (x & kMask) | lane_off;
+    }
   }
-  return (x & m) | lane_off;
+};
+
+// Word I of the 32 codes of a key row that a lane takes (BITS raw words of the row).
+template <int KB, int I>
+__device__ __forceinline__ uint32_t key_word(const uint32_t (&w)[KB]) {
+  if constexpr (KB == 3) {
+    if constexpr (I == 0) return w[0];
+    else if constexpr (I == 3) return w[2] >> 8;
+    else return __funnelshift_r(w[I - 1], w[I], 32 - 8 * I);
+  } else {
+    return w[I];
+  }
 }
 
 template <int N>
@@ -189,9 +239,10 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[N], uint32_t a) {
   }
 }
 
-// The 16 codes 16g .. 16g+15 of a value row, from bit 0 of w.
+// The 16 codes 16g .. 16g+15 of a value row as words (3-bit rows: six bytes, picked from the
+// two aligned words around them by the lane's selectors).
 template <int VB>
-__device__ __forceinline__ void load_value(uint32_t (&w)[2], uint32_t row, int g) {
+__device__ __forceinline__ void load_value(uint32_t (&w)[2], uint32_t row, int g, uint32_t sel0, uint32_t sel1) {
   if constexpr (VB == 2) {
     w[0] = lds32(row + 4 * g);
     w[1] = 0;
@@ -201,53 +252,83 @@ __device__ __forceinline__ void load_value(uint32_t (&w)[2], uint32_t row, int g
   } else {
     const uint32_t a = row + ((6 * g) & ~3);
     const uint32_t x = lds32(a), y = lds32(a + 4);
-    const int sh = (g & 1) * 16;
-    w[0] = __funnelshift_r(x, y, sh);
-    w[1] = y >> sh;
+    w[0] = __byte_perm(x, y, sel0);
+    w[1] = __byte_perm(x, y, sel1);
   }
 }
 
-template <int KB, bool KX, int M>
-struct KeyProducts {
-  // Products of the coordinates of pairs 2M, 2M+1 and on, of two keys (rows g and g + 8).
-  template <int NB>
-  static __device__ __forceinline__ void run(float (&c)[4], float (&cl)[4], const uint32_t (&w0)[KB], const uint32_t (&w1)[KB],
-                                             uint32_t tab, uint32_t lo, const uint32_t (&q)[16], const uint32_t (&ql)[NB]) {
-    const uint32_t p0 = tab + pair_at<KB, 2 * M>(w0, lo), p1 = tab + pair_at<KB, 2 * M>(w1, lo);
-    const uint32_t p2 = tab + pair_at<KB, 2 * M + 1>(w0, lo), p3 = tab + pair_at<KB, 2 * M + 1>(w1, lo);
+// Products of two keys (rows g and g + 8) with the queries, word I of their codes and on.
+// FIRST: the sums begin here.
+template <int KB, bool KX, int NB, int I>
+__device__ __forceinline__ void key_products(float (&c)[4], float (&cl)[4], const uint32_t (&w0)[KB], const uint32_t (&w1)[KB],
+                                             uint32_t lo, const SplitArgs& p, const uint32_t (&q)[16],
+                                             const uint32_t (&ql)[NB]) {
+  using Wd = Word<KB>;
+  constexpr int n = Wd::kFields / 2;                       // products of 16 coordinates in a word
+  uint32_t o0[Wd::kFields], o1[Wd::kFields];
+  Wd::offsets(key_word<KB, I>(w0), lo, p, o0);
+  Wd::offsets(key_word<KB, I>(w1), lo, p, o1);
+#pragma unroll
+  for (int k = 0; k < n; ++k) {
+    const int m = I * n + k;
     if constexpr (KX) {
-      const uint2 a0 = lds64(p0), a1 = lds64(p1), a2 = lds64(p2), a3 = lds64(p3);
-      mma(c, a0.x, a1.x, a2.x, a3.x, q[2 * M], q[2 * M + 1]);
-      mma(cl, a0.y, a1.y, a2.y, a3.y, q[2 * M], q[2 * M + 1]);
-      if constexpr (NB == 16) mma(cl, a0.x, a1.x, a2.x, a3.x, ql[2 * M], ql[2 * M + 1]);
+      const uint2 a0 = lds64t(o0[2 * k]), a1 = lds64t(o1[2 * k]);
+      const uint2 a2 = lds64t(o0[2 * k + 1]), a3 = lds64t(o1[2 * k + 1]);
+      if (m == 0) {
+        mma0(c, a0.x, a1.x, a2.x, a3.x, q[0], q[1]);
+        mma0(cl, a0.y, a1.y, a2.y, a3.y, q[0], q[1]);
+      } else {
+        mma(c, a0.x, a1.x, a2.x, a3.x, q[2 * m], q[2 * m + 1]);
+        mma(cl, a0.y, a1.y, a2.y, a3.y, q[2 * m], q[2 * m + 1]);
+      }
+      if constexpr (NB == 16) mma(cl, a0.x, a1.x, a2.x, a3.x, ql[2 * m], ql[2 * m + 1]);
     } else {
-      mma(c, lds32(p0), lds32(p1), lds32(p2), lds32(p3), q[2 * M], q[2 * M + 1]);
+      const uint32_t a0 = lds32t(o0[2 * k]), a1 = lds32t(o1[2 * k]);
+      const uint32_t a2 = lds32t(o0[2 * k + 1]), a3 = lds32t(o1[2 * k + 1]);
+      if (m == 0) mma0(c, a0, a1, a2, a3, q[0], q[1]);
+      else mma(c, a0, a1, a2, a3, q[2 * m], q[2 * m + 1]);
     }
-    if constexpr (M < 7) KeyProducts<KB, KX, M + 1>::run(c, cl, w0, w1, tab, lo, q, ql);
   }
-};
+  if constexpr ((I + 1) * n < 8) key_products<KB, KX, NB, I + 1>(c, cl, w0, w1, lo, p, q, ql);
+}
 
-template <int VB, bool VX, int M>
-struct ValueProducts {
-  static __device__ __forceinline__ void run(float (&acc)[8][4], const uint32_t (&wa)[2], const uint32_t (&wb)[2],
-                                             const uint32_t (&wc)[2], const uint32_t (&wd)[2], uint32_t tab, uint32_t lo,
-                                             uint32_t b0, uint32_t b1) {
-    const uint32_t pa = tab + pair_at<VB, M>(wa, lo), pb = tab + pair_at<VB, M>(wb, lo);
-    const uint32_t pc = tab + pair_at<VB, M>(wc, lo), pd = tab + pair_at<VB, M>(wd, lo);
+// Fields of two keys' codes of one coordinate each: even coordinates of the word to `e`,
+// odd ones to `o`.
+template <int VB>
+__device__ __forceinline__ void interleave(uint32_t a, uint32_t b, const SplitArgs& p, uint32_t& e, uint32_t& o) {
+  constexpr uint32_t m = VB == 2 ? 0x33333333u : VB == 3 ? 0x1c71c7u : 0x0f0f0f0fu;
+  e = (a & m) | ((b * p.pow2[VB]) & ~m);
+  o = ((a >> VB) & m) | (b & ~m);
+}
+
+// Weighted sum of four keys' values (slots 2t, 2t+1, 2t+8, 2t+9 of the product), word I and on.
+template <int VB, bool VX, int I>
+__device__ __forceinline__ void value_products(float (&acc)[8][4], const uint32_t (&wa)[2], const uint32_t (&wb)[2],
+                                               const uint32_t (&wc)[2], const uint32_t (&wd)[2], 
+                                               uint32_t lo, const SplitArgs& p, uint32_t b0, uint32_t b1) {
+  using Wd = Word<VB>;
+  uint32_t e0, o0, e1, o1;
+  interleave<VB>(wa[I], wb[I], p, e0, o0);
+  interleave<VB>(wc[I], wd[I], p, e1, o1);
+  uint32_t f0[Wd::kFields], f1[Wd::kFields], f2[Wd::kFields], f3[Wd::kFields];
+  Wd::offsets(e0, lo, p, f0);
+  Wd::offsets(o0, lo, p, f1);
+  Wd::offsets(e1, lo, p, f2);
+  Wd::offsets(o1, lo, p, f3);
+#pragma unroll
+  for (int k = 0; k < Wd::kFields; ++k) {
+    const int m = I * Wd::kFields + k;
     if constexpr (VX) {
-      const uint2 a = lds64(pa), b = lds64(pb), c = lds64(pc), d = lds64(pd);
-      mma(acc[M], __byte_perm(a.x, b.x, 0x5410), __byte_perm(a.x, b.x, 0x7632), __byte_perm(c.x, d.x, 0x5410),
-          __byte_perm(c.x, d.x, 0x7632), b0, b1);
-      mma(acc[M], __byte_perm(a.y, b.y, 0x5410), __byte_perm(a.y, b.y, 0x7632), __byte_perm(c.y, d.y, 0x5410),
-          __byte_perm(c.y, d.y, 0x7632), b0, b1);
+      const uint2 a = lds64t(f0[k]), b = lds64t(f1[k]), c = lds64t(f2[k]), d = lds64t(f3[k]);
+      mma(acc[m], a.x, b.x, c.x, d.x, b0, b1);
+      mma(acc[m], a.y, b.y, c.y, d.y, b0, b1);
     } else {
-      const uint32_t a = lds32(pa), b = lds32(pb), c = lds32(pc), d = lds32(pd);
-      mma(acc[M], __byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632), __byte_perm(c, d, 0x5410),
-          __byte_perm(c, d, 0x7632), b0, b1);
+      mma(acc[m], lds32t(f0[k]), lds32t(f1[k]), lds32t(f2[k]), lds32t(f3[k]), b0, b1);
     }
-    if constexpr (M < 7) ValueProducts<VB, VX, M + 1>::run(acc, wa, wb, wc, wd, tab, lo, b0, b1);
   }
-};
+  if constexpr ((I + 1) * Wd::kFields < 8)
+    value_products<VB, VX, I + 1>(acc, wa, wb, wc, wd, lo, p, b0, b1);
+}
 
 // Largest b with tiles[b] * per <= t, by 32-way steps of the whole warp.
 __device__ __forceinline__ int find_sequence(const int* tiles, int B, int per, int t, int lane) {
@@ -265,13 +346,19 @@ __device__ __forceinline__ int find_sequence(const int* tiles, int B, int per, i
 
 template <int KB, int VB, bool KX, bool VX, bool COL>
 __global__ void __launch_bounds__(kSplitWarps * 32, 1)
-paged_split_kernel(const SplitArgs p) {
+paged_split_kernel(const __grid_constant__ SplitArgs p) {
   using L = Lay<KB, VB>;
   constexpr int QT = COL ? 4 : 8;
   constexpr int NL = (KX && !COL) ? 16 : 1;
   extern __shared__ __align__(128) char smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
+
+  const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+  const uint32_t tabs = (base + L::big - 1) & ~static_cast<uint32_t>(L::big - 1);
+  const uint32_t ktab = L::kTab == L::big ? tabs : tabs + L::vTab, vtab = L::kTab == L::big ? tabs + L::kTab : tabs;
+  const int before = (tabs - base) / L::ring;             // rings in front of the tables
+  const uint32_t ring = warp < before ? base + warp * L::ring : tabs + L::kTab + L::vTab + (warp - before) * L::ring;
 
   // tables: inputs of the call, so they may be read before the plan is there
   float kinv, vinv;
@@ -280,15 +367,14 @@ paged_split_kernel(const SplitArgs p) {
     for (int i = 0; i < 1 << KB; ++i) mk = fmaxf(mk, fabsf(p.kcb[i]));
     for (int i = 0; i < 1 << VB; ++i) mv = fmaxf(mv, fabsf(p.vcb[i]));
     const float ks = scale_to_2p7(mk, &kinv), vs = scale_to_2p7(mv, &vinv);
-    build_table<KB, KX>(smem, p.kcb, ks);
-    build_table<VB, VX>(smem + L::kTab, p.vcb, vs);
+    build_table<KB, KX>(smem + (ktab - base), p.kcb, ks);
+    build_table<VB, VX>(smem + (vtab - base), p.vcb, vs);
   }
   __syncthreads();
-  const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-  const uint32_t ktab = base, vtab = base + L::kTab;
-  const uint32_t klo = KX ? (lane & 15) * 8 : lane * 4, vlo = VX ? (lane & 15) * 8 : lane * 4;
-  const uint32_t ring = base + L::kTab + L::vTab + warp * (L::stage * L::stages);
+  const uint32_t klo = ktab | (KX ? (lane & 15) * 8 : lane * 4), vlo = vtab | (VX ? (lane & 15) * 8 : lane * 4);
+  const uint32_t sel0 = g & 1 ? 0x5432u : 0x3210u, sel1 = g & 1 ? 0x7765u : 0x6543u;
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int per = p.H * p.nqt;
   const int T = p.tiles[p.B] * per;
@@ -356,50 +442,55 @@ paged_split_kernel(const SplitArgs p) {
     float vs = 0.f, vsinv = 0.f, vtop = 0.f;               // values' lengths: scale, inverse, largest so far
     float* zrow = p.z == nullptr ? nullptr : p.z + (static_cast<size_t>(unit) * p.Sz) * QT;
 
-    // a tile is two runs of 16 rows, each on one page
+    // a tile is two runs of 16 rows, each on one page (both on one where a page holds 32)
     int pg0 = -1, pg1 = -1;
     auto look_up = [&](int tile) {
-      const int s = tile * kTile;
-      pg0 = tile < tile1 ? table[s >> p.shift] : -1;
-      pg1 = tile < tile1 && s + 16 < n ? table[(s + 16) >> p.shift] : -1;
+      const int s = min(tile, tile1 - 1) * kTile;
+      pg0 = table[s >> p.shift];
+      if (p.shift == 4) pg1 = s + 16 < n ? table[(s >> 4) + 1] : -1;
     };
     auto issue = [&](int tile, uint32_t st) {
-      if (tile < tile1) {
-        const int s = tile * kTile, in_page = s & ((1 << p.shift) - 1), in_page1 = (s + 16) & ((1 << p.shift) - 1);
-        const bool ok0 = static_cast<unsigned>(pg0) < static_cast<unsigned>(p.n_pages);
-        const bool ok1 = static_cast<unsigned>(pg1) < static_cast<unsigned>(p.n_pages);
-        const size_t r0 = ((static_cast<size_t>(ok0 ? pg0 : 0) * p.H + h) << p.shift) + in_page;
-        const size_t r1 = ((static_cast<size_t>(ok1 ? pg1 : 0) * p.H + h) << p.shift) + in_page1;
+      const int s = tile * kTile, left = n - s;
+      const bool live = tile < tile1;                      // behind the last tile nothing is read
+      const bool ok0 = live && static_cast<unsigned>(pg0) < static_cast<unsigned>(p.n_pages);
+      const uint32_t ph0 = (ok0 ? pg0 : 0) * p.H + h;
+      uint32_t there = left >= 32 ? 0xffffffffu : (1u << (left & 31)) - 1;
+      uint32_t gone = ok0 ? 0u : 0xffffu;
+      if (p.shift >= 5) {
+        const size_t r = (static_cast<size_t>(ph0) << p.shift) + (s & ((1 << p.shift) - 1));
+        const uint8_t* ks = p.kp + r * (16 * KB) + lane * 16;
+        const uint8_t* vs = p.vp + r * (16 * VB) + lane * 16;
+#pragma unroll
+        for (int i = 0; i < KB; ++i) cp16(st + lane * 16 + i * 512, ks + i * 512, ok0);
+#pragma unroll
+        for (int i = 0; i < VB; ++i) cp16(st + lane * 16 + L::kBytes + i * 512, vs + i * 512, ok0);
+        cp4(st + L::norms + lane * 4, (lane < 16 ? p.kn : p.vn - 32) + r + 2 * lane, ok0);
+        gone = ok0 ? 0u : 0xffffffffu;
+      } else {
+        const bool ok1 = live && static_cast<unsigned>(pg1) < static_cast<unsigned>(p.n_pages);
+        const uint32_t ph1 = (ok1 ? pg1 : 0) * p.H + h;
+        const size_t r0 = static_cast<size_t>(ph0) << 4, r1 = static_cast<size_t>(ph1) << 4;
 #pragma unroll
         for (int i = 0; i < KB; ++i) {
           const int c = i * 32 + lane;
           const bool second = c >= 16 * KB;
-          if (second ? ok1 : ok0)
-            cp16(st + c * 16, p.kp + (second ? r1 : r0) * (16 * KB) + (second ? c - 16 * KB : c) * 16);
+          cp16(st + c * 16, p.kp + (second ? r1 : r0) * (16 * KB) + (second ? c - 16 * KB : c) * 16, second ? ok1 : ok0);
         }
 #pragma unroll
         for (int i = 0; i < VB; ++i) {
           const int c = i * 32 + lane;
           const bool second = c >= 16 * VB;
-          if (second ? ok1 : ok0)
-            cp16(st + L::kBytes + c * 16, p.vp + (second ? r1 : r0) * (16 * VB) + (second ? c - 16 * VB : c) * 16);
+          cp16(st + L::kBytes + c * 16, p.vp + (second ? r1 : r0) * (16 * VB) + (second ? c - 16 * VB : c) * 16,
+               second ? ok1 : ok0);
         }
-        {
-          const int k = 2 * (lane & 15);
-          const bool second = k >= 16;
-          if (second ? ok1 : ok0)
-            cp4(st + L::norms + lane * 4, (lane < 16 ? p.kn : p.vn) + (second ? r1 : r0) + (k & 15));
-        }
-        if (lane == 0) {
-          const int left = n - s;
-          uint32_t there = left >= 32 ? 0xffffffffu : (1u << left) - 1;
-          if (!ok0) there &= 0xffff0000u;
-          if (!ok1) there &= 0x0000ffffu;
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(st + L::mask), "r"(there) : "memory");
-          if (!ok0 || (left > 16 && !ok1)) atomicOr(&g_wait_fault, static_cast<unsigned int>(kFaultPaged));
-        }
-        look_up(tile + 1);
+        const bool second = (lane & 15) >= 8;
+        cp4(st + L::norms + lane * 4, (lane < 16 ? p.kn : p.vn) + (second ? r1 : r0) + 2 * (lane & 7), second ? ok1 : ok0);
+        if (!ok1) gone |= 0xffff0000u;
       }
+      if (live && (there & gone) != 0 && lane == 0) atomicOr(&g_wait_fault, static_cast<unsigned int>(kFaultPaged));
+      there &= ~gone;
+      asm volatile("st.shared.b32 [%0], %1;" ::"r"(st + L::mask), "r"(there) : "memory");
+      look_up(tile + 1);
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     __syncwarp();                                          // the ring is free
@@ -417,42 +508,68 @@ paged_split_kernel(const SplitArgs p) {
 
       const uint32_t there = lds32(st + L::mask);
       const int r0 = (g >> 1) + (g & 1) * 4;               // row g of the product is this key of its 8
-      float z[2][4];
+      float z[2][4], f[2][4];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
         uint32_t w0[KB], w1[KB];
         load_words(w0, st + (16 * mt + r0) * (16 * KB) + t * 4 * KB);
         load_words(w1, st + (16 * mt + 8 + r0) * (16 * KB) + t * 4 * KB);
-        float c[4] = {0.f, 0.f, 0.f, 0.f}, cl[4] = {0.f, 0.f, 0.f, 0.f};
-        KeyProducts<KB, KX, 0>::run(c, cl, w0, w1, ktab, klo, q, ql);
+        float cl[4];
+        key_products<KB, KX, NL, 0>(z[mt], cl, w0, w1, klo, p, q, ql);
         if constexpr (KX) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) c[i] += cl[i];
+          for (int i = 0; i < 4; ++i) z[mt][i] += cl[i];
         }
         if constexpr (COL) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) c[i] += __shfl_xor_sync(0xffffffffu, c[i], 2);
+          for (int i = 0; i < 4; ++i) z[mt][i] += __shfl_xor_sync(0xffffffffu, z[mt][i], 2);
         }
         const int ka = 16 * mt + r0, kb = ka + 8;
         const float na = lds_half(st + L::norms + 2 * ka), nb = lds_half(st + L::norms + 2 * kb);
-        const bool ha = (there >> ka) & 1, hb = (there >> kb) & 1;
-        z[mt][0] = ha ? c[0] * na * f0 : -INFINITY;
-        z[mt][1] = ha ? c[1] * na * f1 : -INFINITY;
-        z[mt][2] = hb ? c[2] * nb * f0 : -INFINITY;
-        z[mt][3] = hb ? c[3] * nb * f1 : -INFINITY;
+        f[mt][0] = na * f0;
+        f[mt][1] = na * f1;
+        f[mt][2] = nb * f0;
+        f[mt][3] = nb * f1;
         if (zrow != nullptr && (!COL || t < 2)) {
           float* zt = zrow + static_cast<size_t>(tile * kTile) * QT + c0;
-          if (tile * kTile + ka < n) *reinterpret_cast<float2*>(zt + ka * QT) = make_float2(z[mt][0], z[mt][1]);
-          if (tile * kTile + kb < n) *reinterpret_cast<float2*>(zt + kb * QT) = make_float2(z[mt][2], z[mt][3]);
+          const bool ha = (there >> ka) & 1, hb = (there >> kb) & 1;
+          if (tile * kTile + ka < n)
+            *reinterpret_cast<float2*>(zt + ka * QT) = ha ? make_float2(z[mt][0] * f[mt][0], z[mt][1] * f[mt][1])
+                                                          : make_float2(-INFINITY, -INFINITY);
+          if (tile * kTile + kb < n)
+            *reinterpret_cast<float2*>(zt + kb * QT) = hb ? make_float2(z[mt][2] * f[mt][2], z[mt][3] * f[mt][3])
+                                                          : make_float2(-INFINITY, -INFINITY);
         }
       }
-      // The running maximum moves only when a logit passes it by 2^8 (so weights stay below
-      // 2^8 and their fp16 form below 2^16), which is rare after the first tiles.
-      const float nv = ((there >> lane) & 1) ? lds_half(st + L::norms + 64 + 2 * lane) : 0.f;
-      const float z0 = fmaxf(fmaxf(z[0][0], z[0][2]), fmaxf(z[1][0], z[1][2]));
-      const float z1 = fmaxf(fmaxf(z[0][1], z[0][3]), fmaxf(z[1][1], z[1][3]));
-      if (__any_sync(0xffffffffu, z0 > m0 + 8.f || z1 > m1 + 8.f || nv > vtop)) {
-        float a = z0, c = z1, v = nv;
+      float nv = lds_half(st + L::norms + 64 + 2 * lane);
+      const bool part_tile = there != 0xffffffffu;
+      if (part_tile) {                                     // absent slots: a factor that leaves no weight whatever z is
+        if (!((there >> lane) & 1)) nv = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          if (!((there >> (16 * mt + r0)) & 1)) z[mt][0] = z[mt][1] = -INFINITY, f[mt][0] = f[mt][1] = 1.f;
+          if (!((there >> (16 * mt + r0 + 8)) & 1)) z[mt][2] = z[mt][3] = -INFINITY, f[mt][2] = f[mt][3] = 1.f;
+        }
+      }
+      // Logits relative to the running maximum.  It moves only when one passes it by 2^8 (so
+      // weights stay below 2^8 and their fp16 form below 2^16), which is rare after the first
+      // tile; before there is one, everything passes it.
+      float x[2][4], top = -INFINITY;
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        x[mt][0] = fmaf(z[mt][0], f[mt][0], -m0);
+        x[mt][1] = fmaf(z[mt][1], f[mt][1], -m1);
+        x[mt][2] = fmaf(z[mt][2], f[mt][2], -m0);
+        x[mt][3] = fmaf(z[mt][3], f[mt][3], -m1);
+        top = fmaxf(top, fmaxf(fmaxf(x[mt][0], x[mt][1]), fmaxf(x[mt][2], x[mt][3])));
+      }
+      if (__any_sync(0xffffffffu, top > 8.f || m0 == -INFINITY || m1 == -INFINITY || nv > vtop)) {
+        float a = -INFINITY, c = -INFINITY, v = nv;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          a = fmaxf(a, fmaxf(z[mt][0] * f[mt][0], z[mt][2] * f[mt][2]));
+          c = fmaxf(c, fmaxf(z[mt][1] * f[mt][1], z[mt][3] * f[mt][3]));
+        }
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
           a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
@@ -484,13 +601,22 @@ paged_split_kernel(const SplitArgs p) {
           acc[m][2] *= x0;
           acc[m][3] *= x1;
         }
+        // no slot yet: every logit here is -inf, and stays so
+        const float s0 = m0 > -INFINITY ? m0 : 0.f, s1 = m1 > -INFINITY ? m1 : 0.f;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          x[mt][0] = fmaf(z[mt][0], f[mt][0], -s0);
+          x[mt][1] = fmaf(z[mt][1], f[mt][1], -s1);
+          x[mt][2] = fmaf(z[mt][2], f[mt][2], -s0);
+          x[mt][3] = fmaf(z[mt][3], f[mt][3], -s1);
+        }
       }
-      const float s0 = m0 > -INFINITY ? m0 : 0.f, s1 = m1 > -INFINITY ? m1 : 0.f;
+      nv *= vs;
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
         const int ka = 16 * mt + r0, kb = ka + 8;
-        const float va = __shfl_sync(0xffffffffu, nv, ka) * vs, vb = __shfl_sync(0xffffffffu, nv, kb) * vs;
-        const float p0 = ex2(z[mt][0] - s0), p1 = ex2(z[mt][1] - s1), p2 = ex2(z[mt][2] - s0), p3 = ex2(z[mt][3] - s1);
+        const float va = __shfl_sync(0xffffffffu, nv, ka), vb = __shfl_sync(0xffffffffu, nv, kb);
+        const float p0 = ex2(x[mt][0]), p1 = ex2(x[mt][1]), p2 = ex2(x[mt][2]), p3 = ex2(x[mt][3]);
         l0 += p0 + p2;
         l1 += p1 + p3;
         float w0 = p0 * va, w1 = p1 * va, w2 = p2 * vb, w3 = p3 * vb;
@@ -506,11 +632,11 @@ paged_split_kernel(const SplitArgs p) {
         // slots 2t and 2t + 1 of the product are keys t and t + 4 of their 8
         const uint32_t row = st + L::kBytes + (16 * mt + t) * (16 * VB);
         uint32_t wa[2], wb[2], wc[2], wd[2];
-        load_value<VB>(wa, row, g);
-        load_value<VB>(wb, row + 4 * 16 * VB, g);
-        load_value<VB>(wc, row + 8 * 16 * VB, g);
-        load_value<VB>(wd, row + 12 * 16 * VB, g);
-        ValueProducts<VB, VX, 0>::run(acc, wa, wb, wc, wd, vtab, vlo, b0, b1);
+        load_value<VB>(wa, row, g, sel0, sel1);
+        load_value<VB>(wb, row + 4 * 16 * VB, g, sel0, sel1);
+        load_value<VB>(wc, row + 8 * 16 * VB, g, sel0, sel1);
+        load_value<VB>(wd, row + 12 * 16 * VB, g, sel0, sel1);
+        value_products<VB, VX, 0>(acc, wa, wb, wc, wd, vlo, p, b0, b1);
       }
     }
 
