@@ -2,16 +2,16 @@
 // one token per sequence, read straight from the packed codes of the pages.
 //
 // Work: the cache of every unit (sequence, KV head, query tile) in tiles of 32 slots, all
-// units end to end; every warp of the grid (one CTA of 16 warps per SM) takes an equal run of
+// units end to end; every warp of the grid (one CTA of 12 warps per SM) takes an equal run of
 // that line (the tiles are counted on the device: lengths are not known to the host) and
 // leaves one partial (maximum, sum, weighted value sum) for each unit it touched.  No two
 // warps ever wait for each other.
 //
 // Products: mma.m16n8k16 (fp16 operands, fp32 sums) with the keys or values as the 16-row
 // operand and up to 8 queries as its 8 columns, so grouped heads cost what one head costs.
-// The 16-row operand is made in registers: two neighbouring codes select a pair of centroids
-// from a table in shared memory.  Every lane (every 16th with 8-byte entries) has a copy of the
-// table in its own banks, so a look-up never conflicts.  tcgen05 would need that operand
+// The 16-row operand is made in registers: neighbouring codes select fp16 pairs of centroids
+// from tables in shared memory, where every lane that a load serves has a copy in its own banks,
+// so that a look-up never conflicts.  tcgen05 would need that operand
 // written to shared memory and read back (512 bytes a slot instead of none); at 4 to 8 queries
 // the tensor work is a small part either way.
 //
@@ -29,7 +29,7 @@
 
 namespace tq {
 
-constexpr int kSplitWarps = 16;
+constexpr int kSplitWarps = 12;
 constexpr int kTile = 32;            // slots a warp takes at a time
 constexpr int kPartF = 132;          // partial of a query: 128 sums, maximum, sum, 2 unused
 constexpr int kMaxCtas = 192;        // partials are laid out for at most this many CTAs
@@ -71,23 +71,36 @@ enum { kVarFast = 0, kVarMass4 = 1, kVarMass8 = 2, kVarF32 = 3 };
 #ifdef TQ_SPLIT_KERNEL
 namespace {
 
-// Shared memory: the two tables, each at an address that is a multiple of its size (so that an
-// entry's address is made by one AND-OR), the larger one first; the warps' rings of stages in
-// what is left before and behind them.
+// Tables of centroids, 256 entries of 128 bytes each: an entry is picked by a byte of the code
+// stream, so that its address (table | byte << 8 | lane's copy) is one byte permute.  The
+// entry holds copies of what the byte's codes stand for, one for each lane that a load serves
+// at a time, each in banks of its own.
+//   4 bits: the byte's two codes.        2 bits: its four codes.
+//   3 bits: two codes in its low six bits (LOW) or in its high six bits (HIGH); the other two
+//           bits are whatever lies there in the stream.
+// Two tables interleave in a block of 64 KB (the halves of 256-byte rows); blocks lie at shared
+// addresses that are multiples of 64 KB.
+constexpr int kBlock = 65536;
+constexpr int kSmem = 232448;          // all a CTA can have
+
+template <int BITS>
+constexpr int tables_of() { return BITS == 3 ? 2 : 1; }
+
 template <int KB, int VB>
 struct Lay {
-  static constexpr int kTab = (1 << (2 * KB)) * 128, vTab = (1 << (2 * VB)) * 128;
-  static constexpr int big = kTab > vTab ? kTab : vTab;
+  static constexpr int blocks = (tables_of<KB>() + tables_of<VB>() + 1) / 2;
   static constexpr int kBytes = kTile * 16 * KB, vBytes = kTile * 16 * VB;
   static constexpr int norms = kBytes + vBytes;          // 32 fp16 of keys, 32 of values
   static constexpr int mask = norms + 4 * kTile;         // which slots of the tile are there
   static constexpr int stage = mask + 16;
-  static constexpr int bytes = 232448;                   // all a CTA can have
-  // 17 rings: the room before the tables may be cut short of one
-  static constexpr int fit = (bytes - kTab - vTab) / ((kSplitWarps + 1) * stage);
-  static constexpr int stages = fit > 4 ? 4 : fit;       // tiles in flight or in use, per warp
+  // The warps' rings of stages lie before and behind the blocks; the dynamic shared memory
+  // begins somewhere in the first 4 KB.
+  static constexpr int room0 = kBlock - 4096, room1 = kSmem - (1 + blocks) * kBlock;
+  static constexpr int rings(int stages) { return room0 / (stage * stages) + room1 / (stage * stages); }
+  static constexpr int stages = rings(4) >= kSplitWarps ? 4 : rings(3) >= kSplitWarps ? 3 : 2;   // a warp's tiles in flight or in use
   static constexpr int ring = stage * stages;
-  static_assert(stages >= 2, "two stages have to fit");
+  static constexpr int before = room0 / ring;            // rings before the blocks
+  static_assert(rings(stages) >= kSplitWarps, "two stages have to fit");
 };
 
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
@@ -109,6 +122,11 @@ __device__ __forceinline__ uint32_t lds32t(uint32_t a) {
 __device__ __forceinline__ uint2 lds64t(uint32_t a) {
   uint2 v;
   asm("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint4 lds128t(uint32_t a) {
+  uint4 v;
+  asm("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -169,60 +187,110 @@ __device__ __forceinline__ float scale_to_2p7(float m, float* inv) {
   return __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
 }
 
-// Table of centroid pairs: entry e = (c[e % 2^bits], c[e / 2^bits]) times `s`, 128 bytes of
-// copies each: 32 of the fp16 pair, or 16 of (pair of hi parts, pair of lo parts).
+// Fills table `id` (half id % 2 of block id / 2) from the centroids times s.  X: the fp16 pairs
+// of hi parts are followed by those of lo parts.  shift: where the byte's codes begin.
 template <int BITS, bool X>
-__device__ __forceinline__ void build_table(char* tab, const float* cb, float s) {
-  constexpr int n = 1 << (2 * BITS);
-  for (int e = threadIdx.x; e < n * 8; e += blockDim.x) {
-    const int i = e >> 3;
-    const float a = cb[i & ((1 << BITS) - 1)] * s, b = cb[i >> BITS] * s;
+__device__ __forceinline__ void build_table(char* blocks, int id, const float* cb, float s, int shift) {
+  constexpr uint32_t m = (1u << BITS) - 1;
+  char* tab = blocks + (id >> 1) * kBlock + (id & 1) * 128;
+  for (int e = threadIdx.x; e < 256 * 8; e += blockDim.x) {
+    const int i = (e >> 3) >> shift;
+    const float a = cb[i & m] * s, b = cb[(i >> BITS) & m] * s;
     const uint32_t hi = pack2(a, b);
     const uint32_t lo = X ? pack2(a - half_round(a), b - half_round(b)) : hi;
-    reinterpret_cast<uint4*>(tab)[e] = make_uint4(hi, lo, hi, lo);
+    uint4 v = make_uint4(hi, lo, hi, lo);
+    if constexpr (BITS == 2) {
+      const float c = cb[(i >> 4) & m] * s, d = cb[(i >> 6) & m] * s;
+      const uint32_t hi2 = pack2(c, d);
+      const uint32_t lo2 = X ? pack2(c - half_round(c), d - half_round(d)) : hi2;
+      v = X ? make_uint4(hi, hi2, lo, lo2) : make_uint4(hi, hi2, hi, hi2);
+    }
+    *reinterpret_cast<uint4*>(tab + (e >> 3) * 256 + (e & 7) * 16) = v;
   }
 }
+template <int BITS, bool X>
+__device__ __forceinline__ void build_tables(char* blocks, int id, const float* cb, float s) {
+  build_table<BITS, X>(blocks, id, cb, s, 0);
+  if constexpr (BITS == 3) build_table<BITS, X>(blocks, id + 1, cb, s, 2);
+}
 
-// Codes are read in words of `kCodes`: 16 two-bit codes or 8 wider ones (24 bits of 3-bit
-// codes), of which two neighbouring ones make a field, the number of an entry of the table.
-template <int BITS>
-struct Word {
-  static constexpr int kCodes = BITS == 2 ? 16 : 8;
-  static constexpr int kFields = kCodes / 2;
-  static constexpr int kWidth = 2 * BITS;
-  static constexpr uint32_t kMask = ((1u << kWidth) - 1) << 7;
+// A lane's copy within an entry: 4 bytes of a pair, 8 of a pair in two parts or of two
+// pairs, 16 of two pairs in two parts.
+template <int BITS, bool X>
+__device__ __forceinline__ uint32_t copy_of(int lane) {
+  constexpr int n = 4 * (X ? 2 : 1) * (BITS == 2 ? 2 : 1);
+  return (lane * n) & 127;
+}
 
-  // Addresses of the fields' entries: field i moved to bits 7 and up, the table's address and
-  // the lane's bank offset around it.  Shifts to the left are products with a number the compiler does not know,
-  // which run on the FMA pipe: the kernel is bound by the ALU pipe, which would take them all
-  // (131072 slots, 3-bit: see the kernel).
-  static __device__ __forceinline__ void offsets(uint32_t w, uint32_t lane_off, const SplitArgs& p, uint32_t (&o)[kFields]) {
-#pragma unroll
-    for (int i = kFields - 1; i >= 0; --i) {
-      const int at = kWidth * i;
-      uint32_t x;
-      if (at < 7) {
-        x = w * p.pow2[7 - at];
-      } else if (kWidth < 7 && (i & 1) == 0) {            // the next field's shift, and back by one field
-        x = (w >> (at + kWidth - 7)) * p.pow2[kWidth];
-      } else {
-        x = w >> (at - 7);
-      }
-      o[i] = (x & kMask) | lane_off;
+// Address of the entry that byte I of w names; tab: the table's address and the lane's copy.
+template <int I>
+__device__ __forceinline__ uint32_t entry(uint32_t w, uint32_t tab) {
+  return __byte_perm(w, tab, 0x7604 | I << 4);
+}
+
+// The fp16 pairs (X: and their lo parts) of the four pairs of neighbouring codes of one word
+// of the stream: 8 codes of 3 or 4 bits.  For 3 bits u is the word moved up by four bits, so that
+// its second and third pair lie in one byte each.  2-bit words hold eight pairs.
+template <int BITS, bool X>
+struct Pairs {
+  static constexpr int n = BITS == 2 ? 8 : 4;
+  uint32_t hi[n], lo[X ? n : 1];
+  template <int K>
+  __device__ __forceinline__ void one(uint32_t at) {
+    if constexpr (X) {
+      const uint2 v = lds64t(at);
+      hi[K] = v.x;
+      lo[K] = v.y;
+    } else {
+      hi[K] = lds32t(at);
+    }
+  }
+  template <int K>
+  __device__ __forceinline__ void two(uint32_t at) {
+    if constexpr (X) {
+      const uint4 v = lds128t(at);
+      hi[2 * K] = v.x;
+      hi[2 * K + 1] = v.y;
+      lo[2 * K] = v.z;
+      lo[2 * K + 1] = v.w;
+    } else {
+      const uint2 v = lds64t(at);
+      hi[2 * K] = v.x;
+      hi[2 * K + 1] = v.y;
+    }
+  }
+  // B0, B1: the bytes of the first pair in w0 and of the last one in w1
+  template <int B0, int B1>
+  __device__ __forceinline__ void look_up3(uint32_t w0, uint32_t w1, uint32_t u, uint32_t low, uint32_t high) {
+    one<0>(entry<B0>(w0, low));
+    one<1>(entry<1>(u, high));
+    one<2>(entry<2>(u, low));
+    one<3>(entry<B1>(w1, high));
+  }
+  __device__ __forceinline__ void look_up(uint32_t w, uint32_t tab) {
+    if constexpr (BITS == 2) {
+      two<0>(entry<0>(w, tab));
+      two<1>(entry<1>(w, tab));
+      two<2>(entry<2>(w, tab));
+      two<3>(entry<3>(w, tab));
+    } else {
+      one<0>(entry<0>(w, tab));
+      one<1>(entry<1>(w, tab));
+      one<2>(entry<2>(w, tab));
+      one<3>(entry<3>(w, tab));
     }
   }
 };
 
-// Word I of the 32 codes of a key row that a lane takes (BITS raw words of the row).
-template <int KB, int I>
-__device__ __forceinline__ uint32_t key_word(const uint32_t (&w)[KB]) {
-  if constexpr (KB == 3) {
-    if constexpr (I == 0) return w[0];
-    else if constexpr (I == 3) return w[2] >> 8;
-    else return __funnelshift_r(w[I - 1], w[I], 32 - 8 * I);
-  } else {
-    return w[I];
-  }
+// Word I of the 32 codes of a key row that a lane takes.
+template <int KB, bool X, int I>
+__device__ __forceinline__ void key_pairs(Pairs<KB, X>& r, const uint32_t (&w)[KB], uint32_t low, uint32_t high,
+                                          const SplitArgs& p) {
+  if constexpr (KB != 3) r.look_up(w[I], low);
+  else if constexpr (I == 0) r.template look_up3<0, 2>(w[0], w[0], w[0] * p.pow2[4], low, high);
+  else if constexpr (I == 1) r.template look_up3<3, 1>(w[0], w[1], __funnelshift_r(w[0], w[1], 20), low, high);
+  else if constexpr (I == 2) r.template look_up3<2, 0>(w[1], w[2], __funnelshift_r(w[1], w[2], 12), low, high);
+  else r.template look_up3<1, 3>(w[2], w[2], w[2] >> 4, low, high);
 }
 
 template <int N>
@@ -258,42 +326,32 @@ __device__ __forceinline__ void load_value(uint32_t (&w)[2], uint32_t row, int g
 }
 
 // Products of two keys (rows g and g + 8) with the queries, word I of their codes and on.
-// FIRST: the sums begin here.
 template <int KB, bool KX, int NB, int I>
 __device__ __forceinline__ void key_products(float (&c)[4], float (&cl)[4], const uint32_t (&w0)[KB], const uint32_t (&w1)[KB],
-                                             uint32_t lo, const SplitArgs& p, const uint32_t (&q)[16],
+                                             uint32_t low, uint32_t high, const SplitArgs& p, const uint32_t (&q)[16],
                                              const uint32_t (&ql)[NB]) {
-  using Wd = Word<KB>;
-  constexpr int n = Wd::kFields / 2;                       // products of 16 coordinates in a word
-  uint32_t o0[Wd::kFields], o1[Wd::kFields];
-  Wd::offsets(key_word<KB, I>(w0), lo, p, o0);
-  Wd::offsets(key_word<KB, I>(w1), lo, p, o1);
+  using Pr = Pairs<KB, KX>;
+  constexpr int n = Pr::n / 2;                             // products of 16 coordinates in a word
+  Pr a, b;
+  key_pairs<KB, KX, I>(a, w0, low, high, p);
+  key_pairs<KB, KX, I>(b, w1, low, high, p);
 #pragma unroll
   for (int k = 0; k < n; ++k) {
     const int m = I * n + k;
+    if (m == 0) mma0(c, a.hi[0], b.hi[0], a.hi[1], b.hi[1], q[0], q[1]);
+    else mma(c, a.hi[2 * k], b.hi[2 * k], a.hi[2 * k + 1], b.hi[2 * k + 1], q[2 * m], q[2 * m + 1]);
     if constexpr (KX) {
-      const uint2 a0 = lds64t(o0[2 * k]), a1 = lds64t(o1[2 * k]);
-      const uint2 a2 = lds64t(o0[2 * k + 1]), a3 = lds64t(o1[2 * k + 1]);
-      if (m == 0) {
-        mma0(c, a0.x, a1.x, a2.x, a3.x, q[0], q[1]);
-        mma0(cl, a0.y, a1.y, a2.y, a3.y, q[0], q[1]);
-      } else {
-        mma(c, a0.x, a1.x, a2.x, a3.x, q[2 * m], q[2 * m + 1]);
-        mma(cl, a0.y, a1.y, a2.y, a3.y, q[2 * m], q[2 * m + 1]);
-      }
-      if constexpr (NB == 16) mma(cl, a0.x, a1.x, a2.x, a3.x, ql[2 * m], ql[2 * m + 1]);
-    } else {
-      const uint32_t a0 = lds32t(o0[2 * k]), a1 = lds32t(o1[2 * k]);
-      const uint32_t a2 = lds32t(o0[2 * k + 1]), a3 = lds32t(o1[2 * k + 1]);
-      if (m == 0) mma0(c, a0, a1, a2, a3, q[0], q[1]);
-      else mma(c, a0, a1, a2, a3, q[2 * m], q[2 * m + 1]);
+      if (m == 0) mma0(cl, a.lo[0], b.lo[0], a.lo[1], b.lo[1], q[0], q[1]);
+      else mma(cl, a.lo[2 * k], b.lo[2 * k], a.lo[2 * k + 1], b.lo[2 * k + 1], q[2 * m], q[2 * m + 1]);
     }
+    if constexpr (NB == 16) mma(cl, a.hi[2 * k], b.hi[2 * k], a.hi[2 * k + 1], b.hi[2 * k + 1], ql[2 * m], ql[2 * m + 1]);
   }
-  if constexpr ((I + 1) * n < 8) key_products<KB, KX, NB, I + 1>(c, cl, w0, w1, lo, p, q, ql);
+  if constexpr ((I + 1) * n < 8) key_products<KB, KX, NB, I + 1>(c, cl, w0, w1, low, high, p, q, ql);
 }
 
-// Fields of two keys' codes of one coordinate each: even coordinates of the word to `e`,
-// odd ones to `o`.
+// Two keys' codes of one coordinate side by side: even coordinates of the word to `e`, odd
+// ones to `o` (shifts to the left are products: they run on the FMA pipe, the ALU pipe being
+// the busier one).
 template <int VB>
 __device__ __forceinline__ void interleave(uint32_t a, uint32_t b, const SplitArgs& p, uint32_t& e, uint32_t& o) {
   constexpr uint32_t m = VB == 2 ? 0x33333333u : VB == 3 ? 0x1c71c7u : 0x0f0f0f0fu;
@@ -301,33 +359,34 @@ __device__ __forceinline__ void interleave(uint32_t a, uint32_t b, const SplitAr
   o = ((a >> VB) & m) | (b & ~m);
 }
 
+template <int VB, bool VX>
+__device__ __forceinline__ void value_pairs(Pairs<VB, VX>& r, uint32_t w, uint32_t low, uint32_t high, const SplitArgs& p) {
+  if constexpr (VB == 3) r.template look_up3<0, 2>(w, w, w * p.pow2[4], low, high);
+  else r.look_up(w, low);
+}
+
 // Weighted sum of four keys' values (slots 2t, 2t+1, 2t+8, 2t+9 of the product), word I and on.
 template <int VB, bool VX, int I>
 __device__ __forceinline__ void value_products(float (&acc)[8][4], const uint32_t (&wa)[2], const uint32_t (&wb)[2],
-                                               const uint32_t (&wc)[2], const uint32_t (&wd)[2], 
-                                               uint32_t lo, const SplitArgs& p, uint32_t b0, uint32_t b1) {
-  using Wd = Word<VB>;
+                                               const uint32_t (&wc)[2], const uint32_t (&wd)[2], uint32_t low,
+                                               uint32_t high, const SplitArgs& p, uint32_t b0, uint32_t b1) {
+  using Pr = Pairs<VB, VX>;
   uint32_t e0, o0, e1, o1;
   interleave<VB>(wa[I], wb[I], p, e0, o0);
   interleave<VB>(wc[I], wd[I], p, e1, o1);
-  uint32_t f0[Wd::kFields], f1[Wd::kFields], f2[Wd::kFields], f3[Wd::kFields];
-  Wd::offsets(e0, lo, p, f0);
-  Wd::offsets(o0, lo, p, f1);
-  Wd::offsets(e1, lo, p, f2);
-  Wd::offsets(o1, lo, p, f3);
+  Pr f0, f1, f2, f3;
+  value_pairs<VB, VX>(f0, e0, low, high, p);
+  value_pairs<VB, VX>(f1, o0, low, high, p);
+  value_pairs<VB, VX>(f2, e1, low, high, p);
+  value_pairs<VB, VX>(f3, o1, low, high, p);
 #pragma unroll
-  for (int k = 0; k < Wd::kFields; ++k) {
-    const int m = I * Wd::kFields + k;
-    if constexpr (VX) {
-      const uint2 a = lds64t(f0[k]), b = lds64t(f1[k]), c = lds64t(f2[k]), d = lds64t(f3[k]);
-      mma(acc[m], a.x, b.x, c.x, d.x, b0, b1);
-      mma(acc[m], a.y, b.y, c.y, d.y, b0, b1);
-    } else {
-      mma(acc[m], lds32t(f0[k]), lds32t(f1[k]), lds32t(f2[k]), lds32t(f3[k]), b0, b1);
-    }
+  for (int k = 0; k < Pr::n; ++k) {
+    const int m = I * Pr::n + k;
+    mma(acc[m], f0.hi[k], f1.hi[k], f2.hi[k], f3.hi[k], b0, b1);
+    if constexpr (VX) mma(acc[m], f0.lo[k], f1.lo[k], f2.lo[k], f3.lo[k], b0, b1);
   }
-  if constexpr ((I + 1) * Wd::kFields < 8)
-    value_products<VB, VX, I + 1>(acc, wa, wb, wc, wd, lo, p, b0, b1);
+  if constexpr ((I + 1) * Pr::n < 8)
+    value_products<VB, VX, I + 1>(acc, wa, wb, wc, wd, low, high, p, b0, b1);
 }
 
 // Largest b with tiles[b] * per <= t, by 32-way steps of the whole warp.
@@ -355,23 +414,28 @@ paged_split_kernel(const __grid_constant__ SplitArgs p) {
   const int g = lane >> 2, t = lane & 3;
 
   const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-  const uint32_t tabs = (base + L::big - 1) & ~static_cast<uint32_t>(L::big - 1);
-  const uint32_t ktab = L::kTab == L::big ? tabs : tabs + L::vTab, vtab = L::kTab == L::big ? tabs + L::kTab : tabs;
-  const int before = (tabs - base) / L::ring;             // rings in front of the tables
-  const uint32_t ring = warp < before ? base + warp * L::ring : tabs + L::kTab + L::vTab + (warp - before) * L::ring;
+  if (base > 4096) {                                       // not the layout the rings are cut for
+    atomicOr(&g_wait_fault, static_cast<unsigned int>(kFaultPaged));
+    return;
+  }
+  const uint32_t ring = warp < L::before ? base + warp * L::ring
+                                         : (1 + L::blocks) * kBlock + (warp - L::before) * L::ring;
 
   // tables: inputs of the call, so they may be read before the plan is there
+  constexpr int vid = tables_of<KB>();                     // numbers of the values' tables
   float kinv, vinv;
   {
     float mk = 0.f, mv = 0.f;
     for (int i = 0; i < 1 << KB; ++i) mk = fmaxf(mk, fabsf(p.kcb[i]));
     for (int i = 0; i < 1 << VB; ++i) mv = fmaxf(mv, fabsf(p.vcb[i]));
     const float ks = scale_to_2p7(mk, &kinv), vs = scale_to_2p7(mv, &vinv);
-    build_table<KB, KX>(smem + (ktab - base), p.kcb, ks);
-    build_table<VB, VX>(smem + (vtab - base), p.vcb, vs);
+    build_tables<KB, KX>(smem + (kBlock - base), 0, p.kcb, ks);
+    build_tables<VB, VX>(smem + (kBlock - base), vid, p.vcb, vs);
   }
   __syncthreads();
-  const uint32_t klo = ktab | (KX ? (lane & 15) * 8 : lane * 4), vlo = vtab | (VX ? (lane & 15) * 8 : lane * 4);
+  const uint32_t klow = kBlock + copy_of<KB, KX>(lane), khigh = klow + 128;
+  const uint32_t vlow = (1 + vid / 2) * kBlock + (vid & 1) * 128 + copy_of<VB, VX>(lane);
+  const uint32_t vhigh = (1 + (vid + 1) / 2) * kBlock + ((vid + 1) & 1) * 128 + copy_of<VB, VX>(lane);
   const uint32_t sel0 = g & 1 ? 0x5432u : 0x3210u, sel1 = g & 1 ? 0x7765u : 0x6543u;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -515,7 +579,7 @@ paged_split_kernel(const __grid_constant__ SplitArgs p) {
         load_words(w0, st + (16 * mt + r0) * (16 * KB) + t * 4 * KB);
         load_words(w1, st + (16 * mt + 8 + r0) * (16 * KB) + t * 4 * KB);
         float cl[4];
-        key_products<KB, KX, NL, 0>(z[mt], cl, w0, w1, klo, p, q, ql);
+        key_products<KB, KX, NL, 0>(z[mt], cl, w0, w1, klow, khigh, p, q, ql);
         if constexpr (KX) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) z[mt][i] += cl[i];
@@ -636,7 +700,7 @@ paged_split_kernel(const __grid_constant__ SplitArgs p) {
         load_value<VB>(wb, row + 4 * 16 * VB, g, sel0, sel1);
         load_value<VB>(wc, row + 8 * 16 * VB, g, sel0, sel1);
         load_value<VB>(wd, row + 12 * 16 * VB, g, sel0, sel1);
-        value_products<VB, VX, 0>(acc, wa, wb, wc, wd, vlo, p, b0, b1);
+        value_products<VB, VX, 0>(acc, wa, wb, wc, wd, vlow, vhigh, p, b0, b1);
       }
     }
 
@@ -681,14 +745,14 @@ cudaError_t launch_one(const SplitArgs& a, int ctas, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(configured.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<KB, VB>::bytes);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_acq_rel);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kSplitWarps * 32);
-  cfg.dynamicSmemBytes = Lay<KB, VB>::bytes;
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
