@@ -8,10 +8,10 @@
 // searches and packs its coordinates in registers.
 //
 // The codes are those of a 64-bit product: a coordinate within kNear of a midpoint (in units of
-// the row's length) is summed again in 64 bits from the inputs.  kNear = 2^-16 covers the
-// operands' 2^-21 and, at 2^-23 of the row's length each, the roundings of the up to 24 fp32
-// sums of 16 products with room for a tensor core that cuts off instead of rounding; it meets
-// about 1 coordinate in 1300 (3 bits).
+// the row's length) is summed again in 64 bits from the inputs.  kNear = 2^-17 covers the
+// operands' 2^-21 and the up to 24 fp32 sums of 16 products, each of which is at most the
+// row's length and is off by at most 2^-23 of it even where bits are cut off instead of rounded
+// (2^-18.4 together); it meets about 1 coordinate in 2600 (3 bits).
 //
 // N is 128 (the rotation of a head stays in shared memory from tile to tile) or, where that
 // leaves SMs without a tile, 32: a decode step of 64 tokens then runs on four times the SMs.
@@ -22,8 +22,7 @@ namespace {
 
 constexpr int kRows = 128;             // rows of a tile
 constexpr int kThreads = 256;
-constexpr float kNear = 1.f / 65536.f;
-constexpr int kListed = 1024;          // near coordinates a tile can list; with more, all are summed again
+constexpr float kNear = 1.f / 131072.f;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
@@ -42,19 +41,16 @@ __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint
       "r"(static_cast<uint32_t>(add))
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
-  uint32_t r[32];
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&v)[16]) {
+  uint32_t r[16];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(addr));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
@@ -103,186 +99,234 @@ struct AppendArgs {
   int items;                 // (head, keys or values, part of the rotation, tile)
 };
 
-// The cell of v among the midpoints m (ascending): binary search, and whether one of the
-// midpoints it met (both neighbours of v are among them) is near.
-template <int BITS>
-__device__ __forceinline__ uint32_t cell(float v, const float (&m)[15], bool& near) {
-  float t = m[(1 << (BITS - 1)) - 1];
-  bool p = v > t;
-  near = fabsf(v - t) < kNear;
-  uint32_t c = p ? 1u << (BITS - 1) : 0u;
+// One coordinate v, number J of 32: its cell among the midpoints m (ascending) by binary search.
+// Each step's bit is the sign of v - midpoint, moved into the packed word from below by one
+// funnel shift (so coordinates come from the last to the first, and the words hold the bits'
+// complement).  Returns the least distance to a midpoint it met; both neighbours of v are
+// among them.
+template <int BITS, int J>
+__device__ __forceinline__ float put_cell(float v, const float (&m)[15], uint32_t (&w)[BITS]) {
+  auto push = [&](float d, int bit) {
+    uint32_t& x = w[(BITS * J + bit) / 32];
+    x = __funnelshift_l(__float_as_uint(d), x, 1);
+  };
+  constexpr int n = 1 << BITS;
+  const float d0 = v - m[n / 2 - 1];
+  push(d0, BITS - 1);
+  const bool p = d0 > 0.f;
   if constexpr (BITS == 2) {
-    t = p ? m[2] : m[0];
-    c |= v > t ? 1u : 0u;
-    near |= fabsf(v - t) < kNear;
+    const float d1 = v - (p ? m[2] : m[0]);
+    push(d1, 0);
+    return fminf(fabsf(d0), fabsf(d1));
   } else if constexpr (BITS == 3) {
-    t = p ? m[5] : m[1];
-    const float x = p ? m[4] : m[0], y = p ? m[6] : m[2];
-    p = v > t;
-    near |= fabsf(v - t) < kNear;
-    c |= p ? 2u : 0u;
-    t = p ? y : x;
-    c |= v > t ? 1u : 0u;
-    near |= fabsf(v - t) < kNear;
+    const float d1 = v - (p ? m[5] : m[1]);
+    const float a = p ? m[4] : m[0], b = p ? m[6] : m[2];
+    push(d1, 1);
+    const float d2 = v - (d1 > 0.f ? b : a);
+    push(d2, 0);
+    return fminf(fminf(fabsf(d0), fabsf(d1)), fabsf(d2));
   } else {
-    t = p ? m[11] : m[3];
-    float x[4];
-    float u0 = p ? m[9] : m[1], u1 = p ? m[13] : m[5];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = p ? m[8 + 2 * i] : m[2 * i];
-    p = v > t;
-    near |= fabsf(v - t) < kNear;
-    c |= p ? 4u : 0u;
-    t = p ? u1 : u0;
-    const float y0 = p ? x[2] : x[0], y1 = p ? x[3] : x[1];
-    p = v > t;
-    near |= fabsf(v - t) < kNear;
-    c |= p ? 2u : 0u;
-    t = p ? y1 : y0;
-    c |= v > t ? 1u : 0u;
-    near |= fabsf(v - t) < kNear;
+    const float d1 = v - (p ? m[11] : m[3]);
+    const float a0 = p ? m[8] : m[0], a1 = p ? m[9] : m[1], a2 = p ? m[10] : m[2];
+    const float b0 = p ? m[12] : m[4], b1 = p ? m[13] : m[5], b2 = p ? m[14] : m[6];
+    push(d1, 2);
+    const bool q = d1 > 0.f;
+    const float c0 = q ? b0 : a0, c1 = q ? b1 : a1, c2 = q ? b2 : a2;
+    const float d2 = v - c1;
+    push(d2, 1);
+    const float d3 = v - (d2 > 0.f ? c2 : c0);
+    push(d3, 0);
+    return fminf(fminf(fabsf(d0), fabsf(d1)), fminf(fabsf(d2), fabsf(d3)));
   }
-  return c;
 }
 
-// 32 coordinates of a row: packed codes to w, near ones to the returned mask.
-template <int BITS>
-__device__ __forceinline__ uint32_t search32(const float (&y)[32], float inv, const float (&m)[15], uint32_t (&w)[BITS]) {
-  uint32_t mask = 0;
-#pragma unroll
-  for (int i = 0; i < BITS; ++i) w[i] = 0;
-#pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    bool near;
-    const uint32_t c = cell<BITS>(y[j] * inv, m, near);
-    const int at = BITS * j;
-    w[at / 32] |= c << (at % 32);
-    if (at % 32 + BITS > 32) w[at / 32 + 1] |= c >> (32 - at % 32);
-    if (near) mask |= 1u << j;
-  }
-  return mask;
+// Coordinates J .. J - 15 of 32: packed codes to w, near ones to the mask.
+template <int BITS, int J, int LEFT>
+__device__ __forceinline__ void search16(const float (&y)[16], float inv, const float (&m)[15], uint32_t (&w)[BITS], uint32_t& mask) {
+  if (put_cell<BITS, J>(y[J & 15] * inv, m, w) < kNear) mask |= 1u << J;
+  if constexpr (LEFT > 1) search16<BITS, J - 1, LEFT - 1>(y, inv, m, w, mask);
+}
+
+// s + x rounded to s; returns the rounding error, exactly.
+__device__ __forceinline__ float add_exact(float& s, float x) {
+  const float t = s + x, b = t - s;
+  const float e = (s - (t - b)) + (x - b);
+  s = t;
+  return e;
 }
 
 // What the threads of a tile know of its rows.
 struct RowInfo {
   float inv;         // 1 / (length * scales): turns a sum into a unit coordinate; 0 where there is none
+  float scale;       // the power of two that takes the row to 2^7 (in two factors for tiny rows)
   int kind;          // 0: no row, 1: an ordinary one, 2: zero, 3: NaN or infinity within
   uint32_t norm;     // fp16 length
+  int tiny;          // the other factor is 2^64
   int code;          // kinds 2 and 3: the code of every coordinate
   long long at;      // row on the cache's planes
 };
 
+// The code of coordinate c of a row, as 64 bits decide it.  Eight lanes (j = 0 .. 7) with 16
+// coordinates each: sums of products as pairs of fp32 (each product and each addition with its
+// rounding error, 2^-45 of the row's length); where they cannot tell (an exact tie, say), the
+// sums in 64 bits.  P, x: the rows, widened on the way.
 template <typename T, int BITS>
-__device__ __forceinline__ void search_tile(const AppendArgs& a, int kv, int h, int part, int tile, uint32_t tmem,
-                                            RowInfo* info, uint32_t* codes, uint16_t* list, int* listed) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int chunks = a.N / 32, words = chunks * BITS;      // words of a row in this tile
-  float m[15];
+__device__ __forceinline__ uint32_t exact_cell(const float* P, const T* x, const RowInfo& ri, const float* cb, const float* mids, bool live, int j) {
+  const float s0 = ri.tiny ? 18446744073709551616.f : 1.f, s1 = ri.scale;
+  float s = 0.f, se = 0.f, q = 0.f, qe = 0.f;
+  if (live) {
+    const float4* P4 = reinterpret_cast<const float4*>(P + 16 * j);
+    const uint4* x4 = reinterpret_cast<const uint4*>(x + 16 * j);
 #pragma unroll
-  for (int i = 0; i + 1 < (1 << BITS); ++i)
-    m[i] = static_cast<float>(0.5 * (static_cast<double>(a.cb[kv][i]) + static_cast<double>(a.cb[kv][i + 1])));
-  {
-    const int r = 32 * (warp & 3) + lane;
-    const RowInfo ri = info[r];
-    const int c0 = chunks == 4 ? 2 * (warp >> 2) : (warp >> 2), c1 = chunks == 4 ? c0 + 2 : (warp < 4 ? 1 : c0);
-    for (int c = c0; c < c1; ++c) {
-      float y[32];
-      tmem_ld32(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 32 * c, y);
-      uint32_t w[BITS], mask = search32<BITS>(y, ri.inv, m, w);
-      if (ri.kind != 1) {
-        mask = 0;
+    for (int k = 0; k < 2; ++k) {
+      uint4 raw[sizeof(T) / 2];
 #pragma unroll
-        for (int i = 0; i < BITS; ++i) {                   // one code throughout
-          uint32_t x = 0;
-          for (int j = 0; j < 32; ++j) x |= ((static_cast<uint32_t>(ri.code) >> ((32 * i + j) % BITS)) & 1u) << j;
-          w[i] = x;
+      for (int v = 0; v < static_cast<int>(sizeof(T) / 2); ++v) raw[v] = __ldg(x4 + k * (sizeof(T) / 2) + v);
+      float xv[8];
+      widen(raw, xv);
+      const float4 u = __ldg(P4 + 2 * k), v = __ldg(P4 + 2 * k + 1);
+      const float pv[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float xs = xv[i] * s0 * s1;
+        const float d = __fmul_rn(xs, pv[i]), d2 = __fmul_rn(xs, xs);   // never fused with the additions
+        se += fmaf(xs, pv[i], -d) + add_exact(s, d);
+        qe += fmaf(xs, xs, -d2) + add_exact(q, d2);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    const float so = __shfl_xor_sync(0xffffffffu, s, o), qo = __shfl_xor_sync(0xffffffffu, q, o);
+    const float seo = __shfl_xor_sync(0xffffffffu, se, o), qeo = __shfl_xor_sync(0xffffffffu, qe, o);
+    se += seo + add_exact(s, so);
+    qe += qeo + add_exact(q, qo);
+  }
+  uint32_t code = 0;
+  if (live && j == 0) {
+    const float len = sqrtf(q);                            // len + le: the length to 2^-45
+    const float le = (fmaf(-len, len, q) + qe) / (2.f * len);
+    const float y = s / len;
+    for (int i = 0; i + 1 < (1 << BITS); ++i) {
+      bool above = y > mids[i];
+      if (fabsf(y - mids[i]) < 4.f * kNear) {
+        float mid = 0.5f * cb[i];                          // mid + me, exactly
+        const float me = add_exact(mid, 0.5f * cb[i + 1]);
+        const float at = __fmul_rn(mid, len);
+        const float ae = fmaf(mid, len, -at) + fmaf(mid, le, me * len);
+        const float diff = (s - at) + (se - ae);           // s - at is exact so near the midpoint
+        if (fabsf(diff) > 1e-11f * len) {
+          above = diff > 0.f;
+        } else {
+          const double sc = static_cast<double>(s1) * static_cast<double>(s0);
+          double q64 = 0.0, s64 = 0.0;
+          for (int k = 0; k < kPD; ++k) {
+            const double xv = static_cast<double>(static_cast<float>(x[k])) * sc;
+            s64 += xv * static_cast<double>(P[k]);
+            q64 += xv * xv;
+          }
+          above = s64 > 0.5 * (static_cast<double>(cb[i]) + static_cast<double>(cb[i + 1])) * sqrt(q64);
         }
       }
-#pragma unroll
-      for (int i = 0; i < BITS; ++i) codes[r * words + c * BITS + i] = w[i];
-      while (mask != 0) {
-        const int j = __ffs(mask) - 1;
-        mask &= mask - 1;
-        const int at = atomicAdd(listed, 1);
-        if (at < kListed) list[at] = static_cast<uint16_t>(r << 7 | (32 * c + j));
-      }
+      code += above ? 1u : 0u;
     }
   }
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  __syncthreads();
-  // near coordinates again, in 64 bits: eight lanes each
-  const int total = *listed;
-  const bool all = total > kListed;
-  const int count = all ? kRows * a.N : total;
+  return code;
+}
+
+// A warp's share of a tile: 32 rows, 64 coordinates each (32 where N is 32, on the first four
+// warps), from tensor memory to the planes.
+template <typename T, int BITS>
+__device__ __forceinline__ void search_tile(const AppendArgs& a, int kv, int h, int part, int tile, uint32_t tmem,
+                                            const RowInfo* info, const float* mids) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool whole = a.N == kPD;
+  if (!whole && warp >= 4) return;
+  float m[15];
+#pragma unroll
+  for (int i = 0; i + 1 < (1 << BITS); ++i) m[i] = mids[i];
+  const int r0 = 32 * (warp & 3), r = r0 + lane;
+  RowInfo ri = info[r];
+  if (ri.at < 0) ri.kind = 0;
   const T* X = static_cast<const T*>(a.X[kv]);
-  for (int e0 = warp * 4; e0 < count; e0 += (kThreads / 32) * 4) {
-    const int e = e0 + (lane >> 3), j = lane & 7;
-    int r = 0, c = 0;
-    bool live = e < count;
-    if (live) {
-      const int v = all ? e : list[e];
-      r = all ? e / a.N : v >> 7;
-      c = all ? e - r * a.N : v & 127;
-      live = info[r].kind == 1;
-    }
-    double s = 0.0, q = 0.0;
-    if (live) {
-      const T* x = X + (static_cast<size_t>(tile * kRows + r) * a.pg.H + h) * kPD + j;
-      const float* P = a.Pi[kv] + (static_cast<size_t>(h % a.rot) * kPD + part * a.N + c) * kPD + j;
+  const float* P = a.Pi[kv] + (static_cast<size_t>(h % a.rot) * kPD + part * a.N) * kPD;
+  uint32_t* dst = reinterpret_cast<uint32_t*>((kv ? a.pg.vp : a.pg.kp) + ri.at * (16 * BITS)) + part * (whole ? 0 : BITS);
+  const int c0 = whole ? 2 * (warp >> 2) : 0;
+  uint32_t w[2 * BITS];
+  uint64_t mask = 0;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const double xv = static_cast<double>(static_cast<float>(x[8 * i]));
-        s += static_cast<double>(P[8 * i]) * xv;
-        q += xv * xv;
-      }
-    }
+  for (int i = 0; i < 2 * BITS; ++i) w[i] = 0;
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
-      s += __shfl_xor_sync(0xffffffffu, s, o);
-      q += __shfl_xor_sync(0xffffffffu, q, o);
+  for (int c = 0; c < 2; ++c) {
+    if (c == 1 && !whole) break;
+    uint32_t v[BITS], near = 0;
+#pragma unroll
+    for (int i = 0; i < BITS; ++i) v[i] = 0;
+    const uint32_t from = tmem + (static_cast<uint32_t>(r0) << 16) + 32 * (c0 + c);
+    float y[16];
+    tmem_ld16(from + 16, y);
+    search16<BITS, 31, 16>(y, ri.inv, m, v, near);
+    tmem_ld16(from, y);
+    search16<BITS, 15, 16>(y, ri.inv, m, v, near);
+#pragma unroll
+    for (int i = 0; i < BITS; ++i) w[c * BITS + i] = ~v[i];
+    mask |= static_cast<uint64_t>(near) << (32 * c);
+  }
+  if (ri.kind != 1) {
+    mask = 0;
+#pragma unroll
+    for (int i = 0; i < BITS; ++i) {                       // one code throughout
+      uint32_t x = 0;
+      for (int j = 0; j < 32; ++j) x |= ((static_cast<uint32_t>(ri.code) >> ((32 * i + j) % BITS)) & 1u) << j;
+      w[i] = w[BITS + i] = x;
     }
-    if (live && j == 0) {
-      const double len = sqrt(q);
-      uint32_t code = 0;
-      for (int i = 0; i + 1 < (1 << BITS); ++i)
-        code += s > 0.5 * (static_cast<double>(a.cb[kv][i]) + static_cast<double>(a.cb[kv][i + 1])) * len ? 1u : 0u;
-      uint32_t* w = codes + r * words + (BITS * c) / 32;
-      const int sh = (BITS * c) % 32;
-      const bool over = sh + BITS > 32;
-      // other lanes and warps may change neighbouring codes of the same words
-      uint32_t old = w[0] >> sh;
-      if (over) old |= w[1] << (32 - sh);
-      const uint32_t flip = (old ^ code) & ((1u << BITS) - 1);
-      if (flip != 0) {
-        atomicXor(w, flip << sh);
-        if (over) atomicXor(w + 1, flip >> (32 - sh));
+  }
+  // near coordinates, four lanes' at a time
+  for (uint32_t waiting = __ballot_sync(0xffffffffu, mask != 0); waiting != 0; waiting = __ballot_sync(0xffffffffu, mask != 0)) {
+    uint32_t left = waiting;
+    for (int k = 0; k < (lane >> 3); ++k) left &= left - 1;
+    const bool live = left != 0;
+    const int owner = live ? __ffs(left) - 1 : 0;
+    const int mine = __ffsll(static_cast<long long>(mask)) - 1;
+    const int at = __shfl_sync(0xffffffffu, mine, owner);
+    const uint32_t code = exact_cell<T, BITS>(P + (32 * c0 + (live ? at : 0)) * kPD,
+                                              X + (static_cast<size_t>(tile * kRows + r0 + owner) * a.pg.H + h) * kPD,
+                                              info[r0 + owner], a.cb[kv], mids, live, lane & 7);
+    const int rank = __popc(waiting & ((1u << lane) - 1));
+    const uint32_t exact = __shfl_sync(0xffffffffu, code, 8 * (rank & 3));
+    if (mask != 0 && rank < 4) {
+      mask &= mask - 1;
+      constexpr uint32_t ones = (1u << BITS) - 1;
+#pragma unroll
+      for (int i = 0; i < 2 * BITS; ++i) {
+        const int sh = BITS * mine - 32 * i;               // where the code begins in this word
+        if (sh > -BITS && sh < 32) {
+          const uint32_t on = sh >= 0 ? ones << sh : ones >> -sh, v = sh >= 0 ? exact << sh : exact >> -sh;
+          w[i] = (w[i] & ~on) | v;
+        }
       }
     }
   }
-  __syncthreads();
-  // to the planes
-  const uint32_t bytes = 16 * BITS, off = part * words;
-  uint8_t* plane = kv ? a.pg.vp : a.pg.kp;
-  if (chunks == 4) {
-    for (int e = tid; e < kRows * BITS; e += kThreads) {
-      const int r = e / BITS, i = e - r * BITS;
-      if (info[r].kind != 0)
-        *reinterpret_cast<uint4*>(plane + info[r].at * bytes + 16 * i) = *reinterpret_cast<const uint4*>(codes + r * words + 4 * i);
-    }
-  } else {
-    for (int e = tid; e < kRows * words; e += kThreads) {
-      const int r = e / words, i = e - r * words;
-      if (info[r].kind != 0) *reinterpret_cast<uint32_t*>(plane + info[r].at * bytes + 4 * (off + i)) = codes[e];
+  if (ri.kind != 0) {
+    uint32_t* o = dst + BITS * c0;
+    if (!whole) {
+#pragma unroll
+      for (int i = 0; i < BITS; ++i) o[i] = w[i];
+    } else if constexpr (BITS == 3) {                      // 24 bytes, from a multiple of 8
+#pragma unroll
+      for (int i = 0; i < 3; ++i) reinterpret_cast<uint2*>(o)[i] = make_uint2(w[2 * i], w[2 * i + 1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < BITS / 2; ++i)
+        reinterpret_cast<uint4*>(o)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     }
   }
-  if (part == 0 && tid < kRows && info[tid].kind != 0)
-    (kv ? a.pg.vn : a.pg.kn)[info[tid].at] = static_cast<uint16_t>(info[tid].norm);
+  if (part == 0 && warp < 4 && ri.kind != 0) (kv ? a.pg.vn : a.pg.kn)[ri.at] = static_cast<uint16_t>(ri.norm);
 }
 
 template <typename T>
 constexpr int append_smem(int N) {
-  return kRows * 256 * (sizeof(T) == 4 ? 2 : 1) + N * 256 * 2 + kRows * 64 + kRows * static_cast<int>(sizeof(RowInfo)) +
-         kListed * 2 + 64;
+  return kRows * 256 * (sizeof(T) == 4 ? 2 : 1) + N * 256 * 2 + 2 * kRows * static_cast<int>(sizeof(RowInfo)) + 64 + 64;
 }
 
 template <typename T>
@@ -294,12 +338,10 @@ append_kernel(const __grid_constant__ AppendArgs a) {
   const int N = a.N;
   char* sA = smem;                                         // hi, then lo of the rows
   char* sB = sA + kRows * 256 * (XLO ? 2 : 1);             // hi, then lo of the rotation
-  uint32_t* codes = reinterpret_cast<uint32_t*>(sB + N * 512);
-  RowInfo* info = reinterpret_cast<RowInfo*>(codes + kRows * 16);
-  uint16_t* list = reinterpret_cast<uint16_t*>(info + kRows);
-  uint64_t* bar = reinterpret_cast<uint64_t*>(list + kListed);
+  RowInfo* infos = reinterpret_cast<RowInfo*>(sB + N * 512);   // of this tile and of the one before, in turn
+  float* mids = reinterpret_cast<float*>(infos + 2 * kRows);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(mids + 16);
   uint32_t* slot = reinterpret_cast<uint32_t*>(bar + 1);
-  int* listed = reinterpret_cast<int*>(slot + 1);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   if (tid == 0) {
@@ -323,7 +365,7 @@ append_kernel(const __grid_constant__ AppendArgs a) {
   // Loads of an item, in registers while the tile before is searched.  Lane 8g + j of warp w
   // holds chunks g, g + 4, g + 8, g + 12 (eight values) of rows 8w + j and 64 + 8w + j.
   uint4 raw[2][4][V];
-  int seq = -1, slt = -1, pos = 0;
+  int seq = -1, slt = -1, pos = 0, page = -1;
   auto request = [&](int item) {
     const int tile = item % a.tiles, hk = item / a.tiles / parts;
     const T* X = static_cast<const T*>(a.X[hk & 1]) + static_cast<size_t>(hk >> 1) * kPD;
@@ -345,15 +387,26 @@ append_kernel(const __grid_constant__ AppendArgs a) {
       pos = r[2];
     }
   };
-  if (first < last) request(first);
+  // The page of this thread's row: its number is wanted a tile later.
+  auto find_page = [&]() {
+    const bool in = seq >= 0 && slt >= 0 && seq < a.B && slt < a.cap;
+    page = in ? a.pg.table[static_cast<size_t>(seq) * a.pg.max_pages + (slt >> a.pg.shift)] : -1;
+  };
+  if (first < last) {
+    request(first);
+    find_page();
+  }
 
   int loaded = -1;
   uint32_t phase = 0;
-  bool ok = true;
-  for (int item = first; item < last && ok; ++item) {
+  bool lost = false;
+  for (int item = first; item < last; ++item) {
     const int tile = item % a.tiles, hkp = item / a.tiles, part = hkp % parts, hk = hkp / parts, kv = hk & 1, h = hk >> 1;
     if (hkp != loaded) {                                   // rows part * N .. of the head's rotation, times 2^7
       loaded = hkp;
+      // the warps are past the tile before this one's products, but not past its midpoints
+      __syncthreads();
+      if (tid + 1 < (1 << a.bits[kv])) mids[tid] = 0.5f * (a.cb[kv][tid] + a.cb[kv][tid + 1]);   // within 2^-24: kNear has room
       const float* P = a.Pi[kv] + (static_cast<size_t>(h % a.rot) * kPD + part * N) * kPD;
       for (int e = tid; e < N * 16; e += kThreads) {
         const int d = (e >> 5) / 4 * 8 + (e & 7), c = (e >> 5) % 4 * 4 + ((e >> 3) & 3);   // as the rows: 8 rows x 4 chunks a warp
@@ -365,25 +418,24 @@ append_kernel(const __grid_constant__ AppendArgs a) {
         *reinterpret_cast<uint4*>(sB + N * 256 + at) = lo_chunk(x);
       }
     }
+    RowInfo* info = infos + (item & 1) * kRows;
     // where each row goes
     if (tid < kRows) {
       long long at = -1;
       if (seq >= 0 && slt >= 0) {
-        if (seq < a.B && slt < a.cap) {
-          const int page = a.pg.page(seq, slt);
-          if (page >= 0) at = static_cast<long long>(a.pg.row(page, h, slt));
-        } else {
+        if (static_cast<unsigned>(page) < static_cast<unsigned>(a.pg.n_pages)) {
+          at = static_cast<long long>(a.pg.row(page, h, slt));
+          if (kv == 0 && part == 0) {
+            const size_t m = (static_cast<size_t>(seq) * a.pg.H + h) * a.S + slt;
+            if (a.mass != nullptr) a.mass[m] = 0.f;
+            if (a.positions != nullptr) a.positions[m] = pos;
+          }
+        } else {                                           // a sequence, slot or page out of range
           atomicOr(&g_wait_fault, static_cast<unsigned int>(kFaultPaged));
-        }
-        if (at >= 0 && kv == 0 && part == 0) {
-          const size_t m = (static_cast<size_t>(seq) * a.pg.H + h) * a.S + slt;
-          if (a.mass != nullptr) a.mass[m] = 0.f;
-          if (a.positions != nullptr) a.positions[m] = pos;
         }
       }
       info[tid].at = at;
     }
-    if (tid == 0) *listed = 0;
     // rows to fp16, scaled to 2^7
 #pragma unroll
     for (int rg = 0; rg < 2; ++rg) {
@@ -404,12 +456,18 @@ append_kernel(const __grid_constant__ AppendArgs a) {
       const int e = static_cast<int>(__float_as_uint(t) >> 23);                   // 1 .. 254 for a row that is neither zero nor infinite
       const int k2 = 134 - e;                                                     // -120 .. 126
       const float s1 = finite && top != 0 ? __uint_as_float(static_cast<uint32_t>(127 + (k2 > 126 ? 126 : k2)) << 23) : 0.f;
+      if (s0 != 1.f) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[k][i] *= s0;
+      }
       float sum = 0.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[k][i] = finite ? x[k][i] * s0 * s1 : 0.f;
+        for (int i = 0; i < 8; ++i) {                      // NaN and infinity stay within their row, which takes no codes from it
+          x[k][i] *= s1;
           sum = fmaf(x[k][i], x[k][i], sum);
         }
         const int r = 64 * rg + 8 * warp + (lane & 7), c = (lane >> 3) + 4 * k;
@@ -424,6 +482,8 @@ append_kernel(const __grid_constant__ AppendArgs a) {
         const float len = sqrtf(sum);
         const int kind = !finite ? 3 : top == 0 ? 2 : 1;
         ri.kind = kind;
+        ri.scale = s1;
+        ri.tiny = s0 != 1.f;
         ri.inv = kind == 1 ? 1.f / (128.f * len) : 0.f;
         // the length: powers of two taken back, one rounding in fp32 and one to fp16
         const float n = kind == 1 ? len / s1 / s0 : kind == 2 ? 0.f : __uint_as_float(top > 0x7f800000u ? 0x7fc00000u : 0x7f800000u);
@@ -439,7 +499,6 @@ append_kernel(const __grid_constant__ AppendArgs a) {
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    if (tid < kRows && info[tid].at < 0) info[tid].kind = 0;
     if (tid == 0) {
       const uint32_t A = smem_u32(sA), Bm = smem_u32(sB);
       const uint32_t la = kRows * 16, lb = N * 16;
@@ -454,17 +513,17 @@ append_kernel(const __grid_constant__ AppendArgs a) {
       asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
     }
     if (item + 1 < last) request(item + 1);
-    ok = wait_parity_bounded(smem_u32(bar), phase, kFaultPaged) && ok;
+    if (!lost && !wait_parity_bounded(smem_u32(bar), phase, kFaultPaged)) lost = true;
     phase ^= 1;
-    ok = __syncthreads_and(ok) != 0;
-    if (!ok) break;                                        // the product never came: nothing is written
+    find_page();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    switch (a.bits[kv]) {
-      case 2: search_tile<T, 2>(a, kv, h, part, tile, tmem, info, codes, list, listed); break;
-      case 3: search_tile<T, 3>(a, kv, h, part, tile, tmem, info, codes, list, listed); break;
-      default: search_tile<T, 4>(a, kv, h, part, tile, tmem, info, codes, list, listed); break;
+    if (!__any_sync(0xffffffffu, lost)) {                  // else the product never came: nothing is written
+      switch (a.bits[kv]) {
+        case 2: search_tile<T, 2>(a, kv, h, part, tile, tmem, info, mids); break;
+        case 3: search_tile<T, 3>(a, kv, h, part, tile, tmem, info, mids); break;
+        default: search_tile<T, 4>(a, kv, h, part, tile, tmem, info, mids); break;
+      }
     }
-    __syncthreads();
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
