@@ -1,10 +1,33 @@
-// Eviction from the paged cache by accumulated attention weight (tq_evict_paged).
+// Eviction from the paged cache by accumulated attention weight (tq_evict_paged): two
+// launches.
+//
+// select: a cluster of up to 8 CTAs per (sequence, head).  Each CTA keeps the keys (the order of
+// preference as unsigned numbers) of its share of the slots in shared memory; the keep-th
+// largest key is found by its digits from the top (11, 11 and 10 bits), the counts of a
+// digit added up over the cluster through distributed shared memory.  The slots given up below
+// `keep` and the kept ones behind it are then numbered in slot order and listed, and the
+// weights of the slots that stay are copied.  mass and positions are read once in order, and once
+// more, for the kept slots, from L2.
+//
+// move: the i-th listed row behind `keep` goes to the i-th listed slot below it.  Sources and
+// targets are disjoint, so the rows move in any order; a thread moves 16 bytes.
+//
+// Bound by memory latency for the bounded cache's steady state, by the moved rows (read and
+// written once) after a long prompt.
+#include <cooperative_groups.h>
+
 #include "tq_paged.cuh"
 
 namespace tq {
 namespace {
 
-constexpr int kSel = 1024;
+namespace cg = cooperative_groups;
+
+constexpr int kSel = 1024;              // threads of a CTA of select
+constexpr int kDigit = 2048;            // counts of the widest digit
+constexpr int kCached = 48 * 1024;      // keys a CTA can keep in shared memory
+constexpr int kCluster = 8;
+constexpr int kMoves = 64;              // rows a CTA of move takes
 
 // Order of preference as an unsigned number: protected slots above every weight, then the
 // weight (its bits made monotone; -0 as 0, NaN as -inf).
@@ -26,110 +49,223 @@ __device__ __forceinline__ int block_scan(int v, int* red, int* total) {
   __syncthreads();
   if (lane == 31) red[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    int t = lane < kSel / 32 ? red[lane] : 0;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, t, o);
-      if (lane >= o) t += u;
-    }
-    red[lane] = t;
+  int t = red[lane];                                       // every warp adds up the warps' totals
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, t, o);
+    if (lane >= o) t += u;
   }
-  __syncthreads();
-  *total = red[kSel / 32 - 1];
-  return x - v + (warp > 0 ? red[warp - 1] : 0);
+  *total = __shfl_sync(0xffffffffu, t, 31);
+  const int before = __shfl_sync(0xffffffffu, t, warp > 0 ? warp - 1 : 0);
+  return x - v + (warp > 0 ? before : 0);
 }
 
-// One block per (sequence, head).  The keep-th largest key is found by its digits from the
-// top (256 counts a pass); then one pass in slot order lists the slots that are given up
-// below `keep` and the kept ones behind it.
+// This CTA's sum over the CTAs of lower rank of *mine, and the sum over all.
+__device__ __forceinline__ int cluster_before(cg::cluster_group& cl, int* mine) {
+  const int rank = cl.block_rank();
+  int sum = 0;
+  for (int r = 0; r < rank; ++r) sum += *cl.map_shared_rank(mine, r);
+  return sum;
+}
+
+struct SelectArgs {
+  const int* lengths;
+  const int* seen;
+  const float* mass;
+  const int* positions;
+  float* mass_out;
+  int* pos_out;
+  int* counts;                          // [B*H] moves
+  int* lists;                           // [B*H][2][most] slots to fill, slots to take
+  uint32_t* keys;                       // [B*H][S] where they do not fit shared memory
+  int H, S, cap, budget, recent, most;
+};
+
+template <bool CACHED>
 __global__ void __launch_bounds__(kSel)
-evict_select_kernel(Paged pg, const int* __restrict__ lengths, const int* __restrict__ seen,
-                    const float* __restrict__ mass, const int* __restrict__ positions, int S, int cap,
-                    int budget, int recent, float* __restrict__ mass_out, int* __restrict__ pos_out,
-                    int* __restrict__ counts, int* __restrict__ lists, int most) {
-  __shared__ int hist[256];
+evict_select_kernel(const SelectArgs a) {
+  extern __shared__ uint32_t cache[];
+  __shared__ int hist[2][kDigit];
   __shared__ int red[32];
   __shared__ int pick[2];
-  const int b = blockIdx.x, h = blockIdx.y, t = threadIdx.x;
-  const int n = pg.length(lengths, b, cap);
-  const int keep = min(n, budget);
-  const size_t unit = static_cast<size_t>(b) * pg.H + h;
-  const float* m = mass + unit * S;
-  const int* ps = positions + unit * S;
-  const long long oldest = static_cast<long long>(seen[b]) - recent;
+  __shared__ int part[3];
+  cg::cluster_group cl = cg::this_cluster();
+  const int C = cl.num_blocks(), rank = cl.block_rank(), t = threadIdx.x;
+  const int unit = blockIdx.x / C, b = unit / a.H;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int n = a.lengths[b];
+  if (n < 0 || n > a.cap) {
+    if (t == 0) atomicOr(&g_wait_fault, static_cast<unsigned int>(kFaultPaged));
+    n = n < 0 ? 0 : a.cap;
+  }
+  const int keep = min(n, a.budget);
+  const int per = (n + C - 1) / C, first = min(n, rank * per), mine = min(n, first + per) - first;
+  const size_t base = static_cast<size_t>(unit) * a.S + first;
+  const float* m = a.mass + base;
+  const int* ps = a.positions + base;
+  float* mo = a.mass_out + base;
+  int* po = a.pos_out + base;
+  if (keep == n) {                                         // nothing to give up
+    for (int s = t; s < mine; s += kSel) {
+      mo[s] = m[s];
+      po[s] = ps[s];
+    }
+    if (t == 0 && rank == 0) a.counts[unit] = 0;
+    return;
+  }
+  uint32_t* key = CACHED ? cache : a.keys + base;
+  const long long oldest = static_cast<long long>(a.seen[b]) - a.recent;
+  for (int i = t; i < kDigit; i += kSel) hist[0][i] = 0;
+  for (int s0 = 0; s0 < mine; s0 += 4 * kSel) {
+    float x[4];
+    int y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int s = s0 + i * kSel + t;
+      x[i] = s < mine ? m[s] : 0.f;
+      y[i] = s < mine ? ps[s] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int s = s0 + i * kSel + t;
+      if (s < mine) key[s] = rank_key(x[i], y[i], oldest);
+    }
+  }
+  __syncthreads();
+
+  // the keep-th largest key
   uint32_t prefix = 0;
   int want = keep;
-  if (keep < n) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (t < 256) hist[t] = 0;
-      __syncthreads();
-      for (int s = t; s < n; s += kSel) {
-        const uint32_t k = rank_key(m[s], ps[s], oldest);
-        if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255], 1);
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
+    int* hs = hist[pass & 1];
+    for (int s = t; s < mine; s += kSel) {
+      const uint32_t k = key[s];
+      if (pass == 0 || (k >> (shift + width)) == (prefix >> (shift + width))) atomicAdd(&hs[(k >> shift) & ((1u << width) - 1)], 1);
+    }
+    cl.sync();
+    for (int i = t; i < kDigit; i += kSel) hist[(pass + 1) & 1][i] = 0;   // its readers are done: they have come to this sync
+    // two digits a thread, the largest first
+    const int hi = (1 << width) - 1 - 2 * t;
+    int2 v = make_int2(0, 0);
+    if (hi > 0) {
+      for (int r = 0; r < C; ++r) {
+        const int2 x = *reinterpret_cast<const int2*>(cl.map_shared_rank(hs, r) + hi - 1);
+        v.x += x.x;
+        v.y += x.y;
       }
-      __syncthreads();
-      if (t == 0) {
-        int left = want, v = 255;
-        while (v > 0 && hist[v] < left) left -= hist[v--];
-        pick[0] = v;
-        pick[1] = left;
-      }
-      __syncthreads();
-      prefix |= static_cast<uint32_t>(pick[0]) << shift;
-      want = pick[1];
-      __syncthreads();
+    }
+    int total;
+    const int above = block_scan(v.x + v.y, red, &total);
+    if (above < want && want <= above + v.x + v.y) {
+      const bool upper = want <= above + v.y;
+      pick[0] = upper ? hi : hi - 1;
+      pick[1] = want - above - (upper ? 0 : v.y);
+    }
+    __syncthreads();
+    prefix |= static_cast<uint32_t>(pick[0]) << shift;
+    want = pick[1];
+    __syncthreads();
+  }
+
+  // Slots in order, a run of them per thread (an odd number: no bank conflicts): of the
+  // keys equal to the last one kept, the first `want` are.
+  const int run = ((mine + kSel - 1) / kSel) | 1;
+  const int r0 = min(mine, t * run), r1 = min(mine, r0 + run);
+  int eq = 0, total;
+  for (int s = r0; s < r1; ++s) eq += key[s] == prefix;
+  int e = block_scan(eq, red, &total);
+  if (t == 0) part[0] = total;
+  cl.sync();
+  e += cluster_before(cl, &part[0]);
+  int holes = 0, extra = 0;
+  {
+    int x = e;
+    for (int s = r0; s < r1; ++s) {
+      const uint32_t k = key[s];
+      const bool kept = k > prefix || (k == prefix && x++ < want);
+      const bool low = first + s < keep;
+      holes += low && !kept;
+      extra += !low && kept;
     }
   }
-  int* hole = lists + unit * 2 * most;
-  int* sur = hole + most;
-  int eq0 = 0, h0 = 0, s0 = 0, tot;
-  for (int base = 0; base < n; base += kSel) {
-    const int s = base + t;
-    const uint32_t k = s < n ? rank_key(m[s], ps[s], oldest) : 0;
-    const bool eq = s < n && keep < n && k == prefix;
-    const int e = eq0 + block_scan(eq, red, &tot);
-    eq0 += tot;
-    const bool kept = s < n && (keep == n || k > prefix || (eq && e < want));
-    const bool is_hole = s < keep && !kept, is_sur = s >= keep && kept;
-    const int hi = h0 + block_scan(is_hole, red, &tot);
-    h0 += tot;
-    const int si = s0 + block_scan(is_sur, red, &tot);
-    s0 += tot;
-    if (is_hole) hole[hi] = s;
-    if (is_sur) sur[si] = s;
-    if (s < keep && kept) {
-      mass_out[unit * S + s] = m[s];
-      pos_out[unit * S + s] = ps[s];
+  int hi = block_scan(holes, red, &total);
+  if (t == 0) part[1] = total;
+  int xi = block_scan(extra, red, &total);
+  if (t == 0) part[2] = total;
+  cl.sync();
+  hi += cluster_before(cl, &part[1]);
+  xi += cluster_before(cl, &part[2]);
+  if (rank == C - 1 && t == kSel - 1) a.counts[unit] = hi + holes;
+  // what becomes of each slot, in place of its key: its number in a list, or all ones
+  constexpr uint32_t kStays = 0xffffffffu, kGone = 0xfffffffeu;
+  for (int s = r0; s < r1; ++s) {
+    const uint32_t k = key[s];
+    const bool kept = k > prefix || (k == prefix && e++ < want);
+    const bool low = first + s < keep;
+    key[s] = low ? (kept ? kStays : static_cast<uint32_t>(hi++)) : (kept ? static_cast<uint32_t>(xi++) : kGone);
+  }
+  __syncthreads();
+  int* to = a.lists + static_cast<size_t>(unit) * 2 * a.most;
+  int* from = to + a.most;
+  for (int s = t; s < mine; s += kSel) {
+    const uint32_t k = key[s];
+    if (first + s < keep) {
+      if (k == kStays) {
+        mo[s] = m[s];
+        po[s] = ps[s];
+      } else {
+        to[k] = first + s;
+      }
+    } else if (k != kGone) {
+      from[k] = first + s;
     }
   }
-  if (t == 0) counts[unit] = h0;
+  cl.sync();                                               // no CTA leaves while its counts may be read
 }
 
-__global__ void evict_move_kernel(Paged pg, const float* __restrict__ mass, const int* __restrict__ positions,
-                                  int S, float* __restrict__ mass_out, int* __restrict__ pos_out,
-                                  const int* __restrict__ counts, const int* __restrict__ lists, int most,
-                                  int kbits, int vbits) {
-  const int b = blockIdx.x, h = blockIdx.y;
-  const size_t unit = static_cast<size_t>(b) * pg.H + h;
-  const int* hole = lists + unit * 2 * most;
-  const int* sur = hole + most;
-  const int cnt = counts[unit], parts = kbits + vbits + 1;
-  for (int e = threadIdx.x; e < cnt * parts; e += blockDim.x) {
-    const int i = e / parts, c = e % parts;
-    const int to = hole[i], from = sur[i];
-    const int pt = pg.page(b, to), pf = pg.page(b, from);
-    if (pt < 0 || pf < 0) continue;
-    const size_t rt = pg.row(pt, h, to), rf = pg.row(pf, h, from);
+// A thread of move takes 16 bytes of a key or value row, or a row's two lengths, weight and
+// position.
+__global__ void __launch_bounds__(256)
+evict_move_kernel(Paged pg, const float* __restrict__ mass, const int* __restrict__ positions, int S,
+                  float* __restrict__ mass_out, int* __restrict__ pos_out, const int* __restrict__ counts,
+                  const int* __restrict__ lists, int most, int chunks, int kbits, int vbits) {
+  __shared__ long long rows[2][kMoves];
+  const int unit = blockIdx.x / chunks, i0 = (blockIdx.x - unit * chunks) * kMoves;
+  const int b = unit / pg.H, h = unit - b * pg.H;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int cnt = min(kMoves, counts[unit] - i0);
+  if (cnt <= 0) return;
+  const int* to = lists + static_cast<size_t>(unit) * 2 * most + i0;
+  const int* from = to + most;
+  if (threadIdx.x < 2 * kMoves) {
+    const int i = threadIdx.x & (kMoves - 1), side = threadIdx.x / kMoves;
+    long long at = -1;
+    if (i < cnt) {
+      const int s = side ? from[i] : to[i];
+      const int page = pg.page(b, s);
+      if (page >= 0) at = static_cast<long long>(pg.row(page, h, s));
+      if (!side) {                                         // weights follow whether or not the rows can
+        const int f = from[i];
+        mass_out[static_cast<size_t>(unit) * S + s] = mass[static_cast<size_t>(unit) * S + f];
+        pos_out[static_cast<size_t>(unit) * S + s] = positions[static_cast<size_t>(unit) * S + f];
+      }
+    }
+    rows[side][i] = at;
+  }
+  __syncthreads();
+  const int parts = kbits + vbits + 1;
+  for (int e = threadIdx.x; e < cnt * parts; e += 256) {
+    const int i = e / parts, c = e - i * parts;
+    const long long rt = rows[0][i], rf = rows[1][i];
+    if (rt < 0 || rf < 0) continue;
     if (c < kbits) {
       reinterpret_cast<uint4*>(pg.kp)[rt * kbits + c] = reinterpret_cast<const uint4*>(pg.kp)[rf * kbits + c];
     } else if (c < kbits + vbits) {
-      reinterpret_cast<uint4*>(pg.vp)[rt * vbits + c - kbits] =
-          reinterpret_cast<const uint4*>(pg.vp)[rf * vbits + c - kbits];
+      reinterpret_cast<uint4*>(pg.vp)[rt * vbits + c - kbits] = reinterpret_cast<const uint4*>(pg.vp)[rf * vbits + c - kbits];
     } else {
       pg.kn[rt] = pg.kn[rf];
       pg.vn[rt] = pg.vn[rf];
-      mass_out[unit * S + to] = mass[unit * S + from];
-      pos_out[unit * S + to] = positions[unit * S + from];
     }
   }
 }
@@ -137,29 +273,83 @@ __global__ void evict_move_kernel(Paged pg, const float* __restrict__ mass, cons
 // Rows one (sequence, head) can move.
 int most_moves(int S, int budget) { return budget >= S ? 0 : (budget < S - budget ? budget : S - budget); }
 
+// CTAs of a cluster: enough to fill the device from few rows, at least 2048 slots each, and as
+// many as it takes to keep the keys in shared memory (where 8 do).
+int cluster_size(int S, int64_t units, int sms) {
+  int C = 1;
+  while (C < kCluster && ((units * C * 2 <= 2 * sms && S / (2 * C) >= 2048) || S > C * kCached)) C *= 2;
+  return C;
+}
+bool keys_fit(int S) { return S <= kCluster * kCached; }
+
 }  // namespace
 
 size_t evict_paged_bytes(int B, int H, int S, int budget) {
   const size_t units = static_cast<size_t>(B) * H;
-  return paged_round(units * 4) + paged_round(units * 2 * most_moves(S, budget) * 4);
+  return paged_round(units * 4) + paged_round(units * 2 * most_moves(S, budget) * 4) + (keys_fit(S) ? 0 : paged_round(units * S * 4));
 }
 
 cudaError_t launch_evict_paged(const tq_paged_cache& c, const int* table, const int* lengths, const int* seen,
                                int B, int max_pages, const float* mass, const int* positions, int S, int budget,
                                int recent, float* mass_out, int* positions_out, void* ws, cudaStream_t st) {
+  static std::atomic<int> sms_cache[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int sms = sms_cache[dev & 63].load(std::memory_order_acquire);
+  if (sms == 0) {
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCached * 4);
+    if (e != cudaSuccess) return e;
+    sms_cache[dev & 63].store(sms, std::memory_order_release);
+  }
   const int pages = max_pages * c.page_size;
-  const int cap = S < pages ? S : pages;
-  int* counts = static_cast<int*>(ws);
-  int* lists = reinterpret_cast<int*>(static_cast<char*>(ws) + paged_round(static_cast<size_t>(B) * c.H * 4));
-  const Paged pg = paged_view(c, table, max_pages);
+  const int64_t units = static_cast<int64_t>(B) * c.H;
   const int most = most_moves(S, budget);
-  evict_select_kernel<<<dim3(B, c.H), kSel, 0, st>>>(pg, lengths, seen, mass, positions, S, cap, budget, recent,
-                                                    mass_out, positions_out, counts, lists, most);
-  cudaError_t e = cudaGetLastError();
+  SelectArgs a;
+  a.lengths = lengths;
+  a.seen = seen;
+  a.mass = mass;
+  a.positions = positions;
+  a.mass_out = mass_out;
+  a.pos_out = positions_out;
+  a.counts = static_cast<int*>(ws);
+  a.lists = reinterpret_cast<int*>(static_cast<char*>(ws) + paged_round(units * 4));
+  a.keys = reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(a.lists) + paged_round(units * 2 * most * 4));
+  a.H = c.H;
+  a.S = S;
+  a.cap = S < pages ? S : pages;
+  a.budget = budget;
+  a.recent = recent;
+  a.most = most;
+  const int C = cluster_size(a.cap, units, sms);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(units * C));
+  cfg.blockDim = dim3(kSel);
+  cfg.dynamicSmemBytes = keys_fit(S) ? (static_cast<size_t>(ceil_div(a.cap, C)) * 4 + 15) / 16 * 16 : 0;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = keys_fit(S) ? cudaLaunchKernelEx(&cfg, evict_select_kernel<true>, a) : cudaLaunchKernelEx(&cfg, evict_select_kernel<false>, a);
   if (e != cudaSuccess || most == 0) return e;
-  evict_move_kernel<<<dim3(B, c.H), 256, 0, st>>>(pg, mass, positions, S, mass_out, positions_out, counts, lists,
-                                                 most, c.k_bits, c.v_bits);
-  return cudaGetLastError();
+  const int chunks = ceil_div(most, kMoves);
+  if (units * chunks > INT32_MAX) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t mv = {};
+  mv.gridDim = dim3(static_cast<unsigned>(units * chunks));
+  mv.blockDim = dim3(256);
+  mv.stream = st;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  mv.attrs = attr;
+  mv.numAttrs = 1;
+  return cudaLaunchKernelEx(&mv, evict_move_kernel, paged_view(c, table, max_pages), mass, positions, S, mass_out,
+                            positions_out, static_cast<const int*>(a.counts), static_cast<const int*>(a.lists), most,
+                            chunks, c.k_bits, c.v_bits);
 }
 
 cudaError_t take_faults_evict(unsigned int* bits) { return take_unit_faults(bits); }
