@@ -26,8 +26,9 @@ namespace cg = cooperative_groups;
 constexpr int kSel = 1024;              // threads of a CTA of select
 constexpr int kDigit = 2048;            // counts of the widest digit
 constexpr int kCached = 48 * 1024;      // keys a CTA can keep in shared memory
+constexpr int kListed = 3072;           // of them that share the first digit, listed for the last pass
 constexpr int kCluster = 8;
-constexpr int kMoves = 64;              // rows a CTA of move takes
+constexpr int kMoves = 256;             // rows a CTA of move takes
 
 // Order of preference as an unsigned number: protected slots above every weight, then the
 // weight (its bits made monotone; -0 as 0, NaN as -inf).
@@ -86,8 +87,10 @@ evict_select_kernel(const SelectArgs a) {
   extern __shared__ uint32_t cache[];
   __shared__ int hist[2][kDigit];
   __shared__ int red[32];
-  __shared__ int pick[2];
+  __shared__ int pick[3];
   __shared__ int part[3];
+  __shared__ int listed;
+  __shared__ uint32_t list[kListed];
   cg::cluster_group cl = cg::this_cluster();
   const int C = cl.num_blocks(), rank = cl.block_rank(), t = threadIdx.x;
   const int unit = blockIdx.x / C, b = unit / a.H;
@@ -115,33 +118,51 @@ evict_select_kernel(const SelectArgs a) {
   uint32_t* key = CACHED ? cache : a.keys + base;
   const long long oldest = static_cast<long long>(a.seen[b]) - a.recent;
   for (int i = t; i < kDigit; i += kSel) hist[0][i] = 0;
-  for (int s0 = 0; s0 < mine; s0 += 4 * kSel) {
-    float x[4];
-    int y[4];
+  if (t == 0) listed = 0;
+  __syncthreads();
+  constexpr int U = 8;                                     // loads of each array in flight, a thread
+  for (int s0 = t; s0 < mine; s0 += U * kSel) {
+    float x[U];
+    int y[U];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int s = s0 + i * kSel + t;
-      x[i] = s < mine ? m[s] : 0.f;
-      y[i] = s < mine ? ps[s] : 0;
+    for (int i = 0; i < U; ++i) {
+      const int s = min(s0 + i * kSel, mine - 1);
+      x[i] = m[s];
+      y[i] = ps[s];
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int s = s0 + i * kSel + t;
-      if (s < mine) key[s] = rank_key(x[i], y[i], oldest);
+    for (int i = 0; i < U; ++i) {
+      const int s = s0 + i * kSel;
+      if (s < mine) {
+        const uint32_t k = rank_key(x[i], y[i], oldest);
+        key[s] = k;
+        atomicAdd(&hist[0][k >> 21], 1);
+      }
     }
   }
-  __syncthreads();
 
-  // the keep-th largest key
+  // the keep-th largest key; what shares its first digit is listed for the last pass
   uint32_t prefix = 0;
-  int want = keep;
+  int want = keep, equal = 0;
 #pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
     int* hs = hist[pass & 1];
-    for (int s = t; s < mine; s += kSel) {
-      const uint32_t k = key[s];
-      if (pass == 0 || (k >> (shift + width)) == (prefix >> (shift + width))) atomicAdd(&hs[(k >> shift) & ((1u << width) - 1)], 1);
+    if (pass == 1) {
+#pragma unroll 4
+      for (int s = t; s < mine; s += kSel) {
+        const uint32_t k = key[s];
+        if ((k >> 21) == (prefix >> 21)) {
+          atomicAdd(&hs[(k >> 10) & 2047u], 1);
+          const int i = atomicAdd(&listed, 1);
+          if (i < kListed) list[i] = k;
+        }
+      }
+    } else if (pass == 2) {
+      const bool all = listed > kListed;                   // more than the list holds: through all of them
+      const uint32_t* from = all ? key : list;
+      for (int s = t, e = all ? mine : listed; s < e; s += kSel)
+        if ((from[s] >> 10) == (prefix >> 10)) atomicAdd(&hs[from[s] & 1023u], 1);
     }
     cl.sync();
     for (int i = t; i < kDigit; i += kSel) hist[(pass + 1) & 1][i] = 0;   // its readers are done: they have come to this sync
@@ -161,113 +182,135 @@ evict_select_kernel(const SelectArgs a) {
       const bool upper = want <= above + v.y;
       pick[0] = upper ? hi : hi - 1;
       pick[1] = want - above - (upper ? 0 : v.y);
+      pick[2] = upper ? v.y : v.x;
     }
     __syncthreads();
     prefix |= static_cast<uint32_t>(pick[0]) << shift;
     want = pick[1];
+    equal = pick[2];
     __syncthreads();
   }
 
-  // Slots in order, a run of them per thread (an odd number: no bank conflicts): of the
-  // keys equal to the last one kept, the first `want` are.
-  const int run = ((mine + kSel - 1) / kSel) | 1;
-  const int r0 = min(mine, t * run), r1 = min(mine, r0 + run);
-  int eq = 0, total;
-  for (int s = r0; s < r1; ++s) eq += key[s] == prefix;
-  int e = block_scan(eq, red, &total);
-  if (t == 0) part[0] = total;
-  cl.sync();
-  e += cluster_before(cl, &part[0]);
+  // Slots in order: a warp takes a run of them, 32 at a time.  Of the keys equal to the last one
+  // kept (one, unless weights are the same) the first `want` are kept.
+  const int lane = t & 31, warp = t >> 5;
+  const uint32_t below = (1u << lane) - 1;
+  const int run = ((mine + kSel - 1) / kSel) * 32;
+  const int r0 = min(mine, warp * run), r1 = min(mine, r0 + run);
+  int e0 = 0;                                              // equal keys before the run
+  const bool ties = equal > want;
+  if (ties) {
+    int eq = 0, total;
+    for (int s = r0 + lane; s < r1; s += 32) eq += key[s] == prefix;
+    const int before = block_scan(eq, red, &total);
+    e0 = __shfl_sync(0xffffffffu, before, 0);
+    if (t == 0) part[0] = total;
+    cl.sync();
+    e0 += cluster_before(cl, &part[0]);
+  }
+  auto kept_now = [&](int s, int& e) {                     // is the slot kept; e: equal keys so far
+    const uint32_t k = s < r1 ? key[s] : 0;
+    bool kept = s < r1 && k >= prefix;
+    if (ties) {
+      const uint32_t same = __ballot_sync(0xffffffffu, s < r1 && k == prefix);
+      if (k == prefix) kept = kept && e + __popc(same & below) < want;
+      e += __popc(same);
+    }
+    return kept;
+  };
   int holes = 0, extra = 0;
   {
-    int x = e;
-    for (int s = r0; s < r1; ++s) {
-      const uint32_t k = key[s];
-      const bool kept = k > prefix || (k == prefix && x++ < want);
-      const bool low = first + s < keep;
-      holes += low && !kept;
+    int e = e0;
+#pragma unroll 4
+    for (int s0 = r0; s0 < r1; s0 += 32) {
+      const int s = s0 + lane;
+      const bool kept = kept_now(s, e), low = first + s < keep;
+      holes += s < r1 && low && !kept;
       extra += !low && kept;
     }
   }
+  int total;
   int hi = block_scan(holes, red, &total);
+  hi = __shfl_sync(0xffffffffu, hi, 0);
   if (t == 0) part[1] = total;
   int xi = block_scan(extra, red, &total);
+  xi = __shfl_sync(0xffffffffu, xi, 0);
   if (t == 0) part[2] = total;
   cl.sync();
   hi += cluster_before(cl, &part[1]);
   xi += cluster_before(cl, &part[2]);
-  if (rank == C - 1 && t == kSel - 1) a.counts[unit] = hi + holes;
-  // what becomes of each slot, in place of its key: its number in a list, or all ones
-  constexpr uint32_t kStays = 0xffffffffu, kGone = 0xfffffffeu;
-  for (int s = r0; s < r1; ++s) {
-    const uint32_t k = key[s];
-    const bool kept = k > prefix || (k == prefix && e++ < want);
-    const bool low = first + s < keep;
-    key[s] = low ? (kept ? kStays : static_cast<uint32_t>(hi++)) : (kept ? static_cast<uint32_t>(xi++) : kGone);
-  }
-  __syncthreads();
+  if (rank == C - 1 && t == 0) a.counts[unit] = hi + part[1];   // thread 0: what the CTAs before have
   int* to = a.lists + static_cast<size_t>(unit) * 2 * a.most;
   int* from = to + a.most;
-  for (int s = t; s < mine; s += kSel) {
-    const uint32_t k = key[s];
-    if (first + s < keep) {
-      if (k == kStays) {
+  {
+    int e = e0;
+#pragma unroll 2
+    for (int s0 = r0; s0 < r1; s0 += 32) {
+      const int s = s0 + lane;
+      const bool kept = kept_now(s, e), low = first + s < keep;
+      const uint32_t hb = __ballot_sync(0xffffffffu, s < r1 && low && !kept), xb = __ballot_sync(0xffffffffu, !low && kept);
+      if (kept && low) {
         mo[s] = m[s];
         po[s] = ps[s];
-      } else {
-        to[k] = first + s;
       }
-    } else if (k != kGone) {
-      from[k] = first + s;
+      if (hb >> lane & 1) to[hi + __popc(hb & below)] = first + s;
+      if (xb >> lane & 1) from[xi + __popc(xb & below)] = first + s;
+      hi += __popc(hb);
+      xi += __popc(xb);
     }
   }
   cl.sync();                                               // no CTA leaves while its counts may be read
 }
 
-// A thread of move takes 16 bytes of a key or value row, or a row's two lengths, weight and
-// position.
+// Eight threads of move take a row's 16-byte pieces (up to four of the key, up to four of the
+// value), eight rows each with all their loads in flight; a thread a row its two lengths, its
+// weight and its position.
 __global__ void __launch_bounds__(256)
 evict_move_kernel(Paged pg, const float* __restrict__ mass, const int* __restrict__ positions, int S,
                   float* __restrict__ mass_out, int* __restrict__ pos_out, const int* __restrict__ counts,
                   const int* __restrict__ lists, int most, int chunks, int kbits, int vbits) {
   __shared__ long long rows[2][kMoves];
   const int unit = blockIdx.x / chunks, i0 = (blockIdx.x - unit * chunks) * kMoves;
-  const int b = unit / pg.H, h = unit - b * pg.H;
+  const int b = unit / pg.H, h = unit - b * pg.H, t = threadIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int cnt = min(kMoves, counts[unit] - i0);
   if (cnt <= 0) return;
-  const int* to = lists + static_cast<size_t>(unit) * 2 * most + i0;
-  const int* from = to + most;
-  if (threadIdx.x < 2 * kMoves) {
-    const int i = threadIdx.x & (kMoves - 1), side = threadIdx.x / kMoves;
-    long long at = -1;
-    if (i < cnt) {
-      const int s = side ? from[i] : to[i];
-      const int page = pg.page(b, s);
-      if (page >= 0) at = static_cast<long long>(pg.row(page, h, s));
-      if (!side) {                                         // weights follow whether or not the rows can
-        const int f = from[i];
-        mass_out[static_cast<size_t>(unit) * S + s] = mass[static_cast<size_t>(unit) * S + f];
-        pos_out[static_cast<size_t>(unit) * S + s] = positions[static_cast<size_t>(unit) * S + f];
-      }
+  if (t < cnt) {
+    const int* to = lists + static_cast<size_t>(unit) * 2 * most + i0;
+    const int s = to[t], f = to[most + t];
+    const int ps = pg.page(b, s), pf = pg.page(b, f);
+    const size_t at = static_cast<size_t>(unit) * S;
+    const float w = mass[at + f];                          // weights follow whether or not the rows can
+    const int p = positions[at + f];
+    const bool ok = ps >= 0 && pf >= 0;
+    const size_t rt = ok ? pg.row(ps, h, s) : 0, rf = ok ? pg.row(pf, h, f) : 0;
+    const uint16_t kn = pg.kn[rf], vn = pg.vn[rf];
+    mass_out[at + s] = w;
+    pos_out[at + s] = p;
+    if (ok) {
+      pg.kn[rt] = kn;
+      pg.vn[rt] = vn;
     }
-    rows[side][i] = at;
+    rows[0][t] = ok ? static_cast<long long>(rt) : -1;
+    rows[1][t] = static_cast<long long>(rf);
   }
   __syncthreads();
-  const int parts = kbits + vbits + 1;
-  for (int e = threadIdx.x; e < cnt * parts; e += 256) {
-    const int i = e / parts, c = e - i * parts;
-    const long long rt = rows[0][i], rf = rows[1][i];
-    if (rt < 0 || rf < 0) continue;
-    if (c < kbits) {
-      reinterpret_cast<uint4*>(pg.kp)[rt * kbits + c] = reinterpret_cast<const uint4*>(pg.kp)[rf * kbits + c];
-    } else if (c < kbits + vbits) {
-      reinterpret_cast<uint4*>(pg.vp)[rt * vbits + c - kbits] = reinterpret_cast<const uint4*>(pg.vp)[rf * vbits + c - kbits];
-    } else {
-      pg.kn[rt] = pg.kn[rf];
-      pg.vn[rt] = pg.vn[rf];
-    }
+  const int c = t & 7;
+  if (c >= kbits + vbits) return;
+  const bool key = c < kbits;
+  uint4* plane = reinterpret_cast<uint4*>(key ? pg.kp : pg.vp) + (key ? c : c - kbits);
+  const int bits = key ? kbits : vbits;
+  uint4 v[kMoves / 32];
+  long long to[kMoves / 32];
+#pragma unroll
+  for (int k = 0; k < kMoves / 32; ++k) {
+    const int i = k * 32 + (t >> 3);
+    to[k] = i < cnt ? rows[0][i] : -1;
+    if (to[k] >= 0) v[k] = plane[rows[1][i] * bits];
   }
+#pragma unroll
+  for (int k = 0; k < kMoves / 32; ++k)
+    if (to[k] >= 0) plane[to[k] * bits] = v[k];
 }
 
 // Rows one (sequence, head) can move.
