@@ -23,11 +23,11 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSel = 1024;              // threads of a CTA of select
+constexpr int kCluster = 8;             // CTAs of a cluster, at most
+constexpr int kSel = 512;               // threads of a CTA of select (two or more CTAs an SM)
 constexpr int kDigit = 2048;            // counts of the widest digit
 constexpr int kCached = 48 * 1024;      // keys a CTA can keep in shared memory
 constexpr int kListed = 3072;           // of them that share the first digit, listed for the last pass
-constexpr int kCluster = 8;
 constexpr int kMoves = 256;             // rows a CTA of move takes
 
 // Order of preference as an unsigned number: protected slots above every weight, then the
@@ -50,7 +50,7 @@ __device__ __forceinline__ int block_scan(int v, int* red, int* total) {
   __syncthreads();
   if (lane == 31) red[warp] = x;
   __syncthreads();
-  int t = red[lane];                                       // every warp adds up the warps' totals
+  int t = lane < kSel / 32 ? red[lane] : 0;                // every warp adds up the warps' totals
   for (int o = 1; o < 32; o <<= 1) {
     const int u = __shfl_up_sync(0xffffffffu, t, o);
     if (lane >= o) t += u;
@@ -64,7 +64,9 @@ __device__ __forceinline__ int block_scan(int v, int* red, int* total) {
 __device__ __forceinline__ int cluster_before(cg::cluster_group& cl, int* mine) {
   const int rank = cl.block_rank();
   int sum = 0;
-  for (int r = 0; r < rank; ++r) sum += *cl.map_shared_rank(mine, r);
+#pragma unroll
+  for (int r = 0; r < kCluster - 1; ++r)
+    if (r < rank) sum += *cl.map_shared_rank(mine, r);
   return sum;
 }
 
@@ -85,7 +87,7 @@ template <bool CACHED>
 __global__ void __launch_bounds__(kSel)
 evict_select_kernel(const SelectArgs a) {
   extern __shared__ uint32_t cache[];
-  __shared__ int hist[2][kDigit];
+  __shared__ __align__(16) int hist[2][kDigit];
   __shared__ int red[32];
   __shared__ int pick[3];
   __shared__ int part[3];
@@ -149,7 +151,7 @@ evict_select_kernel(const SelectArgs a) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
     int* hs = hist[pass & 1];
     if (pass == 1) {
-#pragma unroll 4
+#pragma unroll 8
       for (int s = t; s < mine; s += kSel) {
         const uint32_t k = key[s];
         if ((k >> 21) == (prefix >> 21)) {
@@ -166,23 +168,29 @@ evict_select_kernel(const SelectArgs a) {
     }
     cl.sync();
     for (int i = t; i < kDigit; i += kSel) hist[(pass + 1) & 1][i] = 0;   // its readers are done: they have come to this sync
-    // two digits a thread, the largest first
-    const int hi = (1 << width) - 1 - 2 * t;
-    int2 v = make_int2(0, 0);
+    // four digits a thread, the largest first
+    const int hi = (1 << width) - 1 - 4 * t;
+    int4 v = make_int4(0, 0, 0, 0);
     if (hi > 0) {
-      for (int r = 0; r < C; ++r) {
-        const int2 x = *reinterpret_cast<const int2*>(cl.map_shared_rank(hs, r) + hi - 1);
-        v.x += x.x;
-        v.y += x.y;
-      }
+      int4 x[kCluster];
+#pragma unroll
+      for (int r = 0; r < kCluster; ++r)                   // all ranks' counts in flight
+        if (r < C) x[r] = *reinterpret_cast<const int4*>(cl.map_shared_rank(hs, r) + hi - 3);
+#pragma unroll
+      for (int r = 0; r < kCluster; ++r)
+        if (r < C) v = make_int4(v.x + x[r].x, v.y + x[r].y, v.z + x[r].z, v.w + x[r].w);
     }
     int total;
-    const int above = block_scan(v.x + v.y, red, &total);
-    if (above < want && want <= above + v.x + v.y) {
-      const bool upper = want <= above + v.y;
-      pick[0] = upper ? hi : hi - 1;
-      pick[1] = want - above - (upper ? 0 : v.y);
-      pick[2] = upper ? v.y : v.x;
+    int above = block_scan(v.x + v.y + v.z + v.w, red, &total);
+    const int at[4] = {v.w, v.z, v.y, v.x};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (above < want && want <= above + at[i]) {
+        pick[0] = hi - i;
+        pick[1] = want - above;
+        pick[2] = at[i];
+      }
+      above += at[i];
     }
     __syncthreads();
     prefix |= static_cast<uint32_t>(pick[0]) << shift;
@@ -221,7 +229,7 @@ evict_select_kernel(const SelectArgs a) {
   int holes = 0, extra = 0;
   {
     int e = e0;
-#pragma unroll 4
+#pragma unroll 8
     for (int s0 = r0; s0 < r1; s0 += 32) {
       const int s = s0 + lane;
       const bool kept = kept_now(s, e), low = first + s < keep;
@@ -244,19 +252,33 @@ evict_select_kernel(const SelectArgs a) {
   int* from = to + a.most;
   {
     int e = e0;
-#pragma unroll 2
-    for (int s0 = r0; s0 < r1; s0 += 32) {
-      const int s = s0 + lane;
-      const bool kept = kept_now(s, e), low = first + s < keep;
-      const uint32_t hb = __ballot_sync(0xffffffffu, s < r1 && low && !kept), xb = __ballot_sync(0xffffffffu, !low && kept);
-      if (kept && low) {
-        mo[s] = m[s];
-        po[s] = ps[s];
+    constexpr int V = 8;                                   // weights of slots that may stay: loads in flight
+    for (int s0 = r0; s0 < r1; s0 += 32 * V) {
+      float x[V];
+      int y[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int s = s0 + 32 * i + lane;
+        if (s < r1 && first + s < keep) {
+          x[i] = m[s];
+          y[i] = ps[s];
+        }
       }
-      if (hb >> lane & 1) to[hi + __popc(hb & below)] = first + s;
-      if (xb >> lane & 1) from[xi + __popc(xb & below)] = first + s;
-      hi += __popc(hb);
-      xi += __popc(xb);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (s0 + 32 * i >= r1) break;
+        const int s = s0 + 32 * i + lane;
+        const bool kept = kept_now(s, e), low = first + s < keep;
+        const uint32_t hb = __ballot_sync(0xffffffffu, s < r1 && low && !kept), xb = __ballot_sync(0xffffffffu, !low && kept);
+        if (kept && low) {
+          mo[s] = x[i];
+          po[s] = y[i];
+        }
+        if (hb >> lane & 1) to[hi + __popc(hb & below)] = first + s;
+        if (xb >> lane & 1) from[xi + __popc(xb & below)] = first + s;
+        hi += __popc(hb);
+        xi += __popc(xb);
+      }
     }
   }
   cl.sync();                                               // no CTA leaves while its counts may be read
