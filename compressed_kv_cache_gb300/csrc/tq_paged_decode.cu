@@ -93,9 +93,10 @@ constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kJoinQ = 8;
 constexpr int kJoinSlots = 8;        // partials a warp has in flight
 
-// Block (sequence and head, group of up to 8 queries).  Thread (r, d) of 4 x 128 holds rows
-// 32r .. 32r+31 of column d of Pi_v, requested before the wait for the split.  The partials
-// of each query are read by all warps, eight in flight a warp, four coordinates a lane.
+// Block (sequence and head, group of 1, 2, 4 or 8 of its queries).  Thread (r, d) of 4 x 128 holds
+// rows 32r .. 32r+31 of column d of Pi_v, requested before the wait for the split.  The warps
+// are shared out among the queries; a warp takes every (16 / group)-th partial of its query,
+// eight in flight, four coordinates a lane.
 template <typename T>
 __global__ void __launch_bounds__(kJoinThreads)
 join_kernel(const float* __restrict__ part, const int* __restrict__ tiles, const float* __restrict__ Piv, int B, int H,
@@ -103,7 +104,8 @@ join_kernel(const float* __restrict__ part, const int* __restrict__ tiles, const
   constexpr int kRows = kPD * kPD / kJoinThreads;
   __shared__ float wm[kJoinWarps], wl[kJoinWarps];
   __shared__ __align__(16) float wacc[kJoinWarps][kPD];
-  __shared__ __align__(16) float norm[kPD];
+  __shared__ __align__(16) float norm[kJoinQ][kPD];
+  __shared__ float sums[kJoinQ][kPD * kPD / (kPD * kRows)][kPD];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int bh = blockIdx.x, b = bh / H, h = bh - b * H, q0 = blockIdx.y * group;
@@ -116,19 +118,20 @@ join_kernel(const float* __restrict__ part, const int* __restrict__ tiles, const
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int per = H * nqt, T0 = tiles[b], nt = tiles[b + 1] - T0, total = tiles[B] * per;
   const int rq = total / W, rr = total - rq * W;
-  for (int i = 0; i < nq; ++i) {
-    const int qi = q0 + i, j = qi / QT, c = qi - j * QT;
+  const int mine = warp & (group - 1), each = kJoinWarps / group;   // this warp's query, and its warps
+  {
+    const int qi = min(q0 + mine, G - 1), j = qi / QT, c = qi - j * QT;
     const int unit = b * per + h * nqt + j, t0 = T0 * per + (h * nqt + j) * nt;
     float M = -INFINITY, Ls = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     if (nt > 0) {
       const int first = run_of(t0, rq, rr), last = run_of(t0 + nt - 1, rq, rr);
-      for (int w = first + warp; w <= last; w += kJoinWarps * kJoinSlots) {
+      for (int w = first + warp / group; w <= last; w += each * kJoinSlots) {
         float2 ml[kJoinSlots];
         float4 x[kJoinSlots];
 #pragma unroll
         for (int k = 0; k < kJoinSlots; ++k) {
-          const int wk = w + k * kJoinWarps;
+          const int wk = w + k * each;
           if (wk <= last) {
             const float* pp = part + (static_cast<size_t>(wk + unit) * QT + c) * kPartF;
             ml[k] = *reinterpret_cast<const float2*>(pp + kPD);
@@ -162,65 +165,78 @@ join_kernel(const float* __restrict__ part, const int* __restrict__ tiles, const
       wl[warp] = Ls;
     }
     *reinterpret_cast<float4*>(&wacc[warp][4 * lane]) = a;
-    __syncthreads();
-    if (tid < kPD) {
-      float m = wm[0];
-#pragma unroll
-      for (int w = 1; w < kJoinWarps; ++w) m = fmaxf(m, wm[w]);
-      const float ref = m > -INFINITY ? m : 0.f;
-      float s = 0.f, l = 0.f;
-#pragma unroll
-      for (int w = 0; w < kJoinWarps; ++w) {
-        const float e = exp2f(wm[w] - ref);
-        s = fmaf(wacc[w][tid], e, s);
-        l = fmaf(wl[w], e, l);
-      }
-      norm[tid] = l != 0.f ? s / l : 0.f;                  // no slot at all: zeros
-      if (fin != nullptr && tid == 0)
-        *reinterpret_cast<float2*>(fin + 2 * (static_cast<size_t>(bh) * G + qi)) = make_float2(ref, l != 0.f ? 1.f / l : 0.f);
+  }
+  __syncthreads();
+  for (int i = r; i < nq; i += kJoinThreads / kPD) {       // a query for each 128 threads
+    float m = -INFINITY;
+    for (int w = i; w < kJoinWarps; w += group) m = fmaxf(m, wm[w]);
+    const float ref = m > -INFINITY ? m : 0.f;
+    float s = 0.f, l = 0.f;
+    for (int w = i; w < kJoinWarps; w += group) {
+      const float e = exp2f(wm[w] - ref);
+      s = fmaf(wacc[w][d], e, s);
+      l = fmaf(wl[w], e, l);
     }
-    __syncthreads();
+    norm[i][d] = l != 0.f ? s / l : 0.f;                   // no slot at all: zeros
+    if (fin != nullptr && d == 0)
+      *reinterpret_cast<float2*>(fin + 2 * (static_cast<size_t>(bh) * G + q0 + i)) = make_float2(ref, l != 0.f ? 1.f / l : 0.f);
+  }
+  __syncthreads();
+  for (int i = 0; i < nq; ++i) {
     float o = 0.f;
 #pragma unroll
     for (int k = 0; k < kRows; k += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(&norm[r * kRows + k]);
+      const float4 v = *reinterpret_cast<const float4*>(&norm[i][r * kRows + k]);
       o = fmaf(v.x, pv[k], o);
       o = fmaf(v.y, pv[k + 1], o);
       o = fmaf(v.z, pv[k + 2], o);
       o = fmaf(v.w, pv[k + 3], o);
     }
-    wacc[r][d] = o;
-    __syncthreads();
-    if (r == 0) store_o(out, (static_cast<size_t>(bh) * G + qi) * kPD + d, wacc[0][d] + wacc[1][d] + wacc[2][d] + wacc[3][d]);
-    __syncthreads();
+    sums[i][r][d] = o;
   }
+  __syncthreads();
+  for (int i = r; i < nq; i += kJoinThreads / kPD)
+    store_o(out, (static_cast<size_t>(bh) * G + q0 + i) * kPD + d, sums[i][0][d] + sums[i][1][d] + sums[i][2][d] + sums[i][3][d]);
 }
 
-// mass[b,h,s] += sum over the group's queries of 2^(z - M) / L.  One thread a slot.
+// mass[b,h,s] += sum over the group's queries of 2^(z - M) / L.  Four slots a thread.
+constexpr int kMassSlots = 1024;
+
 __global__ void __launch_bounds__(256)
 mass_kernel(const float* __restrict__ z, const float* __restrict__ fin, const int* __restrict__ cut, int H, int G,
             int QT, int nqt, int cap, int S, float* __restrict__ mass) {
-  const int chunks = (cap + 255) / 256;
-  const int bh = blockIdx.x / chunks, s = (blockIdx.x - bh * chunks) * 256 + threadIdx.x;
+  const int chunks = (cap + kMassSlots - 1) / kMassSlots;
+  const int bh = blockIdx.x / chunks, s0 = (blockIdx.x - bh * chunks) * kMassSlots + threadIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (s >= cut[bh / H]) return;
-  float sum = 0.f;
+  const int n = cut[bh / H];
+  if (s0 - static_cast<int>(threadIdx.x) >= n) return;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f}, old[4];
+  float* to = mass + static_cast<size_t>(bh) * S;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) old[k] = s0 + 256 * k < n ? to[s0 + 256 * k] : 0.f;
   for (int j = 0; j < nqt; ++j) {
-    const float* zs = z + (static_cast<size_t>(bh * nqt + j) * S + s) * QT;
+    const float* zj = z + static_cast<size_t>(bh * nqt + j) * S * QT;
     for (int c0 = 0; c0 < QT; c0 += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(zs + c0);
-      const float x[4] = {v.x, v.y, v.z, v.w};
+      if (j * QT + c0 >= G) break;
+      float4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        v[k] = s0 + 256 * k < n ? *reinterpret_cast<const float4*>(zj + static_cast<size_t>(s0 + 256 * k) * QT + c0)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const int qi = j * QT + c0 + c;
         if (qi < G) {
           const float2 f = *reinterpret_cast<const float2*>(fin + 2 * (static_cast<size_t>(bh) * G + qi));
-          sum = fmaf(exp2f(x[c] - f.x), f.y, sum);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sum[k] = fmaf(exp2f((c == 0 ? v[k].x : c == 1 ? v[k].y : c == 2 ? v[k].z : v[k].w) - f.x), f.y, sum[k]);
         }
       }
     }
   }
-  mass[static_cast<size_t>(bh) * S + s] += sum;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (s0 + 256 * k < n) to[s0 + 256 * k] = old[k] + sum[k];
 }
 
 // Workspace: rotated queries, tiles, cut lengths, maxima and sums, partials, logits.
@@ -288,17 +304,16 @@ cudaError_t launch(const tq_paged_cache& c, const T* Q, const int* table, const 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // one query a block while that leaves SMs idle, up to 8 (Pi_v is then read once for them)
+  // one query a block while that does not fill the SMs, up to 8 (Pi_v is then read once for them)
   const int64_t queries = static_cast<int64_t>(B) * c.H * G;
-  int group = static_cast<int>(queries / (2 * sms));
-  group = group < 1 ? 1 : (group > kJoinQ ? kJoinQ : group);
-  group = group > G ? G : group;
+  int group = 1;
+  while (group < kJoinQ && group < G && queries > static_cast<int64_t>(sms) * group) group *= 2;
   cfg.gridDim = dim3(B * c.H, (G + group - 1) / group);
   cfg.blockDim = dim3(kJoinThreads);
   e = cudaLaunchKernelEx(&cfg, join_kernel<T>, static_cast<const float*>(part), static_cast<const int*>(tiles), c.Pi_v,
                          B, c.H, G, c.rot_heads, QT, nqt, ctas * kSplitWarps, group, out, fin);
   if (e != cudaSuccess || mass == nullptr) return e;
-  cfg.gridDim = dim3((cap + 255) / 256 * B * c.H);
+  cfg.gridDim = dim3((cap + kMassSlots - 1) / kMassSlots * B * c.H);
   cfg.blockDim = dim3(256);
   return cudaLaunchKernelEx(&cfg, mass_kernel, static_cast<const float*>(z), static_cast<const float*>(fin),
                             static_cast<const int*>(cut), c.H, G, QT, nqt, cap, S, mass);

@@ -187,31 +187,36 @@ __device__ __forceinline__ float scale_to_2p7(float m, float* inv) {
   return __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
 }
 
-// Fills table `id` (half id % 2 of block id / 2) from the centroids times s.  X: the fp16 pairs
-// of hi parts are followed by those of lo parts.  shift: where the byte's codes begin.
-template <int BITS, bool X>
-__device__ __forceinline__ void build_table(char* blocks, int id, const float* cb, float s, int shift) {
-  constexpr uint32_t m = (1u << BITS) - 1;
+// Fills table `id` (half id % 2 of block id / 2) from the scaled centroids, one a lane.  X: the
+// fp16 pairs of hi parts are followed by those of lo parts.  SHIFT: where the byte's codes
+// begin.  A thread writes an entry's eight 16-byte pieces, beginning at its own.
+template <int BITS, bool X, int SHIFT>
+__device__ __forceinline__ void build_table(char* blocks, int id, float cb) {
+  constexpr int m = (1 << BITS) - 1;
   char* tab = blocks + (id >> 1) * kBlock + (id & 1) * 128;
-  for (int e = threadIdx.x; e < 256 * 8; e += blockDim.x) {
-    const int i = (e >> 3) >> shift;
-    const float a = cb[i & m] * s, b = cb[(i >> BITS) & m] * s;
+  for (int e0 = 0; e0 < 256; e0 += kSplitWarps * 32) {     // whole warps: the centroids come from lanes
+    const int e = e0 + static_cast<int>(threadIdx.x);
+    const int i = (e & 255) >> SHIFT;
+    const float a = __shfl_sync(0xffffffffu, cb, i & m), b = __shfl_sync(0xffffffffu, cb, (i >> BITS) & m);
     const uint32_t hi = pack2(a, b);
     const uint32_t lo = X ? pack2(a - half_round(a), b - half_round(b)) : hi;
     uint4 v = make_uint4(hi, lo, hi, lo);
     if constexpr (BITS == 2) {
-      const float c = cb[(i >> 4) & m] * s, d = cb[(i >> 6) & m] * s;
+      const float c = __shfl_sync(0xffffffffu, cb, (i >> 4) & m), d = __shfl_sync(0xffffffffu, cb, (i >> 6) & m);
       const uint32_t hi2 = pack2(c, d);
       const uint32_t lo2 = X ? pack2(c - half_round(c), d - half_round(d)) : hi2;
       v = X ? make_uint4(hi, hi2, lo, lo2) : make_uint4(hi, hi2, hi, hi2);
     }
-    *reinterpret_cast<uint4*>(tab + (e >> 3) * 256 + (e & 7) * 16) = v;
+    if (e < 256) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(tab + e * 256 + ((k + e) & 7) * 16) = v;
+    }
   }
 }
 template <int BITS, bool X>
-__device__ __forceinline__ void build_tables(char* blocks, int id, const float* cb, float s) {
-  build_table<BITS, X>(blocks, id, cb, s, 0);
-  if constexpr (BITS == 3) build_table<BITS, X>(blocks, id + 1, cb, s, 2);
+__device__ __forceinline__ void build_tables(char* blocks, int id, float cb) {
+  build_table<BITS, X, 0>(blocks, id, cb);
+  if constexpr (BITS == 3) build_table<BITS, X, 2>(blocks, id + 1, cb);
 }
 
 // A lane's copy within an entry: 4 bytes of a pair, 8 of a pair in two parts or of two
@@ -425,12 +430,16 @@ paged_split_kernel(const __grid_constant__ SplitArgs p) {
   constexpr int vid = tables_of<KB>();                     // numbers of the values' tables
   float kinv, vinv;
   {
-    float mk = 0.f, mv = 0.f;
-    for (int i = 0; i < 1 << KB; ++i) mk = fmaxf(mk, fabsf(p.kcb[i]));
-    for (int i = 0; i < 1 << VB; ++i) mv = fmaxf(mv, fabsf(p.vcb[i]));
+    const float kc = lane < 1 << KB ? p.kcb[lane] : 0.f, vc = lane < 1 << VB ? p.vcb[lane] : 0.f;
+    float mk = fabsf(kc), mv = fabsf(vc);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+      mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+    }
     const float ks = scale_to_2p7(mk, &kinv), vs = scale_to_2p7(mv, &vinv);
-    build_tables<KB, KX>(smem + (kBlock - base), 0, p.kcb, ks);
-    build_tables<VB, VX>(smem + (kBlock - base), vid, p.vcb, vs);
+    build_tables<KB, KX>(smem + (kBlock - base), 0, kc * ks);
+    build_tables<VB, VX>(smem + (kBlock - base), vid, vc * vs);
   }
   __syncthreads();
   const uint32_t klow = kBlock + copy_of<KB, KX>(lane), khigh = klow + 128;
@@ -441,70 +450,34 @@ paged_split_kernel(const __grid_constant__ SplitArgs p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int per = p.H * p.nqt;
+  const bool few = p.B <= 32;                              // then lane b knows sequence b
+  const int mine = few ? p.tiles[min(lane, p.B)] : 0, mylen = few ? p.lengths[min(lane, p.B - 1)] : 0;
   const int T = p.tiles[p.B] * per;
   const int W = gridDim.x * kSplitWarps;
-  const int run = warp * gridDim.x + blockIdx.x;          // short lines reach every SM
+  const int run = warp * gridDim.x + blockIdx.x;           // short lines reach every SM
   const int rq = T / W, rr = T % W;
   const int end = run_start(run + 1, rq, rr);
   for (int at = run_start(run, rq, rr); at < end;) {
-    const int b = find_sequence(p.tiles, p.B, per, at, lane);
-    const int first = p.tiles[b], nt = p.tiles[b + 1] - first;
+    int b, first, nt, n;
+    if (few) {
+      b = 31 - __clz(__ballot_sync(0xffffffffu, lane < p.B && mine * per <= at));
+      first = __shfl_sync(0xffffffffu, mine, b);
+      nt = (b + 1 < 32 ? __shfl_sync(0xffffffffu, mine, (b + 1) & 31) : T / per) - first;
+      n = __shfl_sync(0xffffffffu, mylen, b);
+    } else {
+      b = find_sequence(p.tiles, p.B, per, at, lane);
+      first = p.tiles[b];
+      nt = p.tiles[b + 1] - first;
+      n = p.lengths[b];
+    }
     const int in = at - first * per;
     const int u = in / nt;                                 // (head, query tile) of the sequence
     const int tile0 = in - u * nt;
     const int tile1 = min(nt, tile0 + (end - at));
     at += tile1 - tile0;
     const int h = u / p.nqt, j = u - h * p.nqt;
-    const int n = p.lengths[b];
     const int unit = b * per + u;
     const int* table = p.table + static_cast<size_t>(b) * p.max_pages;
-
-    // queries: column g is query g (COL: g % 4; its hi part for g < 4, its lo part above)
-    uint32_t q[16], ql[NL];
-    float qinv;
-    {
-      const int qi = j * QT + (COL ? (g & 3) : g);
-      const float4* src = reinterpret_cast<const float4*>(
-          p.A + (static_cast<size_t>(b * p.H + h) * p.G + min(qi, p.G - 1)) * kPD + 32 * t);
-      float x[32], m = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 v = src[i];
-        x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
-      }
-#pragma unroll
-      for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(x[i]));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      float s = scale_to_2p7(m, &qinv);
-      if (qi >= p.G) s = 0.f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float a = x[2 * i] * s, c = x[2 * i + 1] * s;
-        const float al = a - half_round(a), cl = c - half_round(c);
-        if constexpr (COL) q[i] = g < 4 ? pack2(a, c) : pack2(al, cl);
-        else q[i] = pack2(a, c);
-        if constexpr (NL == 16) ql[i] = pack2(al, cl);
-      }
-      if (qi >= p.G) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          q[i] = 0;
-          if constexpr (NL == 16) ql[i] = 0;
-        }
-      }
-    }
-    // logit factors of columns 2t and 2t + 1 (COL: of their queries)
-    const int c0 = COL ? 2 * (t & 1) : 2 * t;
-    const float f0 = __shfl_sync(0xffffffffu, qinv, 4 * c0) * kinv * p.scale2;
-    const float f1 = __shfl_sync(0xffffffffu, qinv, 4 * (c0 + 1)) * kinv * p.scale2;
-
-    float acc[8][4];
-#pragma unroll
-    for (int m = 0; m < 8; ++m) acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-    float vs = 0.f, vsinv = 0.f, vtop = 0.f;               // values' lengths: scale, inverse, largest so far
-    float* zrow = p.z == nullptr ? nullptr : p.z + (static_cast<size_t>(unit) * p.Sz) * QT;
 
     // a tile is two runs of 16 rows, each on one page (both on one where a page holds 32)
     int pg0 = -1, pg1 = -1;
@@ -557,10 +530,63 @@ paged_split_kernel(const __grid_constant__ SplitArgs p) {
       look_up(tile + 1);
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    __syncwarp();                                          // the ring is free
     look_up(tile0);
+    // queries: column g is query g (COL: g % 4; its hi part for g < 4, its lo part above); they
+    // are asked for with the first pages, and made ready while the first tiles come
+    const int qi = j * QT + (COL ? (g & 3) : g);
+    float4 qraw[8];
+    {
+      const float4* src = reinterpret_cast<const float4*>(
+          p.A + (static_cast<size_t>(b * p.H + h) * p.G + min(qi, p.G - 1)) * kPD + 32 * t);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) qraw[i] = src[i];
+    }
+    __syncwarp();                                          // the ring is free
 #pragma unroll
     for (int i = 0; i < L::stages - 1; ++i) issue(tile0 + i, ring + i * L::stage);
+    uint32_t q[16], ql[NL];
+    float qinv;
+    {
+      float x[32], m = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 v = qraw[i];
+        x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(x[i]));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      float s = scale_to_2p7(m, &qinv);
+      if (qi >= p.G) s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float a = x[2 * i] * s, c = x[2 * i + 1] * s;
+        const float al = a - half_round(a), cl = c - half_round(c);
+        if constexpr (COL) q[i] = g < 4 ? pack2(a, c) : pack2(al, cl);
+        else q[i] = pack2(a, c);
+        if constexpr (NL == 16) ql[i] = pack2(al, cl);
+      }
+      if (qi >= p.G) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          q[i] = 0;
+          if constexpr (NL == 16) ql[i] = 0;
+        }
+      }
+    }
+    // logit factors of columns 2t and 2t + 1 (COL: of their queries)
+    const int c0 = COL ? 2 * (t & 1) : 2 * t;
+    const float f0 = __shfl_sync(0xffffffffu, qinv, 4 * c0) * kinv * p.scale2;
+    const float f1 = __shfl_sync(0xffffffffu, qinv, 4 * (c0 + 1)) * kinv * p.scale2;
+
+    float acc[8][4];
+#pragma unroll
+    for (int m = 0; m < 8; ++m) acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float vs = 0.f, vsinv = 0.f, vtop = 0.f;               // values' lengths: scale, inverse, largest so far
+    float* zrow = p.z == nullptr ? nullptr : p.z + (static_cast<size_t>(unit) * p.Sz) * QT;
+
     int rs = 0, ws = L::stages - 1;
     for (int tile = tile0; tile < tile1; ++tile) {
       asm volatile("cp.async.wait_group %0;" ::"n"(L::stages - 2) : "memory");
