@@ -515,7 +515,7 @@ class PagedCache:
     calls, not resized); all are on one device, and the calls run there."""
 
     __slots__ = ("k_plane", "k_norm", "v_plane", "v_norm", "Pi_k", "k_codebook", "Pi_v", "v_codebook", "device",
-                 "H", "page_size", "D", "k_bits", "v_bits", "_struct", "_ref")
+                 "H", "page_size", "D", "k_bits", "v_bits", "_struct", "_ref", "_index")
 
     def __init__(self, k_plane, k_norm, v_plane, v_norm, Pi_k, k_codebook, Pi_v, v_codebook):
         names = ("k_plane", "k_norm", "v_plane", "v_norm", "Pi_k", "Pi_v", "k_codebook", "v_codebook")
@@ -541,17 +541,17 @@ class PagedCache:
         self.Pi_k, self.k_codebook, self.Pi_v, self.v_codebook = Pi_k, k_codebook, Pi_v, v_codebook
         self.device, self.H, self.page_size, self.D, self.k_bits, self.v_bits = k_plane.device, H, page, D, kb, vb
         self._struct = _PagedCacheStruct(*ptrs, N, H, page, D, kb, vb, 1 if Pi_k.dim() == 2 else Pi_k.shape[0])
-        self._ref = ctypes.addressof(self._struct)
+        self._ref, self._index = ctypes.addressof(self._struct), k_plane.get_device()
 
 
-def _on(cache: PagedCache, t: torch.Tensor, name: str, dtype, shape) -> int:
+def _on(index: int, t: torch.Tensor, name: str, dtype, shape) -> int:
     """Pointer of a tensor of a paged call: its type, device, shape and contiguity are checked."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.device != cache.device:
-        raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{index}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
@@ -559,29 +559,38 @@ def _on(cache: PagedCache, t: torch.Tensor, name: str, dtype, shape) -> int:
     return t.data_ptr()
 
 
-def _paged_call(name: str, cache: PagedCache, *args) -> None:
-    """Calls `name` on the cache's device and that device's current stream."""
-    dev = cache.device.index
-    if dev == torch.cuda.current_device():
-        status = getattr(_lib or lib(), name)(cache._ref, *args, torch.cuda.current_stream(dev).cuda_stream)
+def _paged_call(name: str, index: int, *args) -> None:
+    """Calls `name` on device `index` and that device's current stream."""
+    fn = getattr(_lib or lib(), name)
+    if index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(dev):
-            status = getattr(_lib or lib(), name)(cache._ref, *args, torch.cuda.current_stream(dev).cuda_stream)
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
     if status != TQ_OK:
         raise TQError(name, status)
 
 
-def _table(cache: PagedCache, page_table: torch.Tensor) -> tuple[int, int, int]:
+def _raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):         # the same handle, without a Stream object around it
+    _raw_stream = torch._C._cuda_getCurrentRawStream       # noqa: F811
+
+
+def _table(index: int, page_table: torch.Tensor) -> tuple[int, int, int]:
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be a [B, max_pages] tensor")
     B, M = page_table.shape
-    return _on(cache, page_table, "page_table", torch.int32, (B, M)), B, M
+    return _on(index, page_table, "page_table", torch.int32, (B, M)), B, M
 
 
-def _workspace_of(cache: PagedCache, workspace, need: int) -> tuple[torch.Tensor, int]:
+def _workspace_of(index: int, workspace, need: int) -> tuple[int, int]:
     if workspace is None:
-        workspace = torch.empty(need, device=cache.device, dtype=torch.uint8)
-    return workspace, _on(cache, workspace, "workspace", torch.uint8, (workspace.numel(),))
+        workspace = torch.empty(need, device=torch.device("cuda", index), dtype=torch.uint8)
+    n = workspace.numel()
+    return _on(index, workspace, "workspace", torch.uint8, (n,)), n
 
 
 def append_paged(K, V, rows, cache: PagedCache, page_table, mass=None, positions=None) -> None:
@@ -591,19 +600,19 @@ def append_paged(K, V, rows, cache: PagedCache, page_table, mass=None, positions
     (optional) get 0 and the position at the slots written.  No two rows may name one slot."""
     if not isinstance(K, torch.Tensor) or K.dim() != 3 or K.dtype not in QTYPE:
         raise ValueError("K must be a [n, H, D] fp32 or bf16 tensor")
-    n = K.shape[0]
-    shape = (n, cache.H, cache.D)
-    tp, B, M = _table(cache, page_table)
+    n, dev, H = K.shape[0], cache._index, cache.H
+    shape = (n, H, cache.D)
+    tp, B, M = _table(dev, page_table)
     S = 0
     for t in (mass, positions):
         if t is not None:
             S = t.shape[-1] if t.dim() == 3 else 0
             if S < 1:
                 raise ValueError("mass and positions must be [B, H, S] tensors with S >= 1")
-    _paged_call("tq_append_paged", cache, _on(cache, K, "K", K.dtype, shape), _on(cache, V, "V", K.dtype, shape),
-                QTYPE[K.dtype], _on(cache, rows, "rows", torch.int32, (n, 3)), n, tp, B, M,
-                None if mass is None else _on(cache, mass, "mass", torch.float32, (B, cache.H, S)),
-                None if positions is None else _on(cache, positions, "positions", torch.int32, (B, cache.H, S)), S)
+    _paged_call("tq_append_paged", dev, cache._ref, _on(dev, K, "K", K.dtype, shape), _on(dev, V, "V", K.dtype, shape),
+                QTYPE[K.dtype], _on(dev, rows, "rows", torch.int32, (n, 3)), n, tp, B, M,
+                None if mass is None else _on(dev, mass, "mass", torch.float32, (B, H, S)),
+                None if positions is None else _on(dev, positions, "positions", torch.int32, (B, H, S)), S)
 
 
 def decode_paged_workspace_bytes(B: int, H: int, G: int, S: int, with_mass: bool) -> int:
@@ -618,26 +627,26 @@ def decode_paged(Q, cache: PagedCache, page_table, lengths, mass=None, scale=Non
     type; zeros for a sequence of length 0."""
     if not isinstance(Q, torch.Tensor) or Q.dim() != 3 or Q.dtype not in QTYPE:
         raise ValueError("Q must be a [B, heads, D] fp32 or bf16 tensor")
-    tp, B, M = _table(cache, page_table)
-    H, D = cache.H, cache.D
+    dev, H, D = cache._index, cache.H, cache.D
+    tp, B, M = _table(dev, page_table)
     heads = Q.shape[1]
     if heads < H or heads % H:
         raise ValueError(f"{heads} query heads over {H} KV heads")
     G = heads // H
-    qp = _on(cache, Q, "Q", Q.dtype, (B, heads, D))
+    shape, dtype = (B, heads, D), Q.dtype
+    qp = _on(dev, Q, "Q", dtype, shape)
     S, mp = 0, None
     if mass is not None:
         S = mass.shape[-1] if mass.dim() == 3 else 0
         if S < 1:
             raise ValueError("mass must be a [B, H, S] tensor with S >= 1")
-        mp = _on(cache, mass, "mass", torch.float32, (B, H, S))
-    ws, wp = _workspace_of(cache, workspace, 0 if workspace is not None else
+        mp = _on(dev, mass, "mass", torch.float32, (B, H, S))
+    wp, wn = _workspace_of(dev, workspace, 0 if workspace is not None else
                            decode_paged_workspace_bytes(B, H, G, S, mass is not None))
     if out is None:
         out = torch.empty_like(Q)
-    _paged_call("tq_decode_paged", cache, qp, QTYPE[Q.dtype], tp, _on(cache, lengths, "lengths", torch.int32, (B,)),
-                B, G, M, 1.0 / D ** 0.5 if scale is None else float(scale), mp, S,
-                _on(cache, out, "out", Q.dtype, (B, heads, D)), wp, ws.numel())
+    _paged_call("tq_decode_paged", dev, cache._ref, qp, QTYPE[dtype], tp, _on(dev, lengths, "lengths", torch.int32, (B,)),
+                B, G, M, 1.0 / D ** 0.5 if scale is None else float(scale), mp, S, _on(dev, out, "out", dtype, shape), wp, wn)
     return out
 
 
@@ -652,19 +661,20 @@ def evict_paged(cache: PagedCache, page_table, lengths, seen, mass, positions, b
     budget move to the slots given up.  lengths, seen int32 [B]; mass fp32, positions int32
     [B,H,S].  Returns (mass, positions) of the slots as they are now (`out`, or new tensors of
     0 and -1 behind the kept slots); `lengths` is the caller's to cut once all layers are done."""
-    tp, B, M = _table(cache, page_table)
+    dev = cache._index
+    tp, B, M = _table(dev, page_table)
     if not isinstance(mass, torch.Tensor) or mass.dim() != 3:
         raise ValueError("mass must be a [B, H, S] tensor")
     shape = (B, cache.H, mass.shape[-1])
     S = shape[2]
-    mp, pp = _on(cache, mass, "mass", torch.float32, shape), _on(cache, positions, "positions", torch.int32, shape)
+    mp, pp = _on(dev, mass, "mass", torch.float32, shape), _on(dev, positions, "positions", torch.int32, shape)
     budget, recent = max(-1, min(int(budget), S)), max(-1, min(int(recent), 2 ** 31 - 1))   # both fit an int
     if out is None:
         out = torch.zeros_like(mass), torch.full_like(positions, -1)
-    ws, wp = _workspace_of(cache, workspace, 0 if workspace is not None else
+    wp, wn = _workspace_of(dev, workspace, 0 if workspace is not None else
                            evict_paged_workspace_bytes(B, cache.H, S, budget))
-    _paged_call("tq_evict_paged", cache, tp, _on(cache, lengths, "lengths", torch.int32, (B,)),
-                _on(cache, seen, "seen", torch.int32, (B,)), B, M, mp, pp, S, budget, recent,
-                _on(cache, out[0], "mass_out", torch.float32, shape),
-                _on(cache, out[1], "positions_out", torch.int32, shape), wp, ws.numel())
+    _paged_call("tq_evict_paged", dev, cache._ref, tp, _on(dev, lengths, "lengths", torch.int32, (B,)),
+                _on(dev, seen, "seen", torch.int32, (B,)), B, M, mp, pp, S, budget, recent,
+                _on(dev, out[0], "mass_out", torch.float32, shape),
+                _on(dev, out[1], "positions_out", torch.int32, shape), wp, wn)
     return out
