@@ -21,9 +21,15 @@ namespace tq {
 namespace {
 
 constexpr int kRows = 128;             // rows of a tile
-constexpr int kThreads = 256;
+constexpr int kCells = 128;            // cells of the search table
+constexpr int kCopies = 4;             // of each, for every fourth lane
 constexpr float kNear = 1.f / 131072.f;
 
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
 // Shared-memory matrix descriptor, K-major, no swizzle: core matrices of 8 rows x 16 bytes,
@@ -96,6 +102,7 @@ struct AppendArgs {
   float* mass;
   int* positions;
   int n, B, rot, S, cap, N, tiles, bits[2];
+  uint32_t step;             // bytes from cell to cell
   int items;                 // (head, keys or values, part of the rotation, tile)
 };
 
@@ -145,6 +152,67 @@ template <int BITS, int J, int LEFT>
 __device__ __forceinline__ void search16(const float (&y)[16], float inv, const float (&m)[15], uint32_t (&w)[BITS], uint32_t& mask) {
   if (put_cell<BITS, J>(y[J & 15] * inv, m, w) < kNear) mask |= 1u << J;
   if constexpr (LEFT > 1) search16<BITS, J - 1, LEFT - 1>(y, inv, m, w, mask);
+}
+
+// Search table: the midpoints' range in cells, each with the midpoint k nearest to it; the code
+// of a v in the cell is k + (v > midpoint k).  The cells are a 62nd of the range or less
+// apart from every other midpoint (or the table is not used: search16), so that no v has
+// another midpoint nearer by.  The cell of v is a saturating FMA and a rounding.
+struct Cell {
+  float mid;
+  int above;       // k + 1
+};
+struct Grid {
+  float scale, shift;                                      // v * scale + shift in [0, 1] over the cells
+  int ok;
+};
+
+__device__ __forceinline__ float cell_u(float y, float scale, float shift) {   // 2^23 + cell
+  return fmaf(__saturatef(fmaf(y, scale, shift)), static_cast<float>(kCells - 1), 8388608.f);
+}
+
+// One warp: the grid of n ascending midpoints.
+__device__ __forceinline__ Grid make_grid(const float* mids, int n, int lane) {
+  const float lo = mids[0], hi = mids[n - 1], w = (hi - lo) / static_cast<float>(kCells - 4);
+  const bool close = lane + 1 < n && !(mids[min(lane + 1, n - 1)] - mids[min(lane, n - 1)] >= 2.f * w);
+  Grid g;
+  g.ok = !__any_sync(0xffffffffu, close) && w > 1e-30f && w < 1e30f;
+  g.scale = 1.f / (w * static_cast<float>(kCells - 1));
+  g.shift = (1.5f * w - lo) * g.scale;
+  return g;
+}
+// Entry i, by the cell's centre.
+__device__ __forceinline__ Cell make_cell(const float* mids, int n, const Grid& g, int i) {
+  const float c = (static_cast<float>(i) / static_cast<float>(kCells - 1) - g.shift) / g.scale;
+  int k = 0;
+  for (int j = 1; j < n; ++j)
+    if (fabsf(mids[j] - c) < fabsf(mids[k] - c)) k = j;
+  return {mids[k], k + 1};
+}
+
+// Coordinates J .. J + 15 of 32 (J 0 or 16): packed codes to w, near ones to the mask.  at:
+// what takes the bits of cell_u to the address of the lane's copy.
+template <int BITS, int J>
+__device__ __forceinline__ void look_up16(const float (&y)[16], float inv, float scale, float shift, uint32_t at, uint32_t step,
+                                          uint32_t (&w)[BITS], uint32_t& mask) {
+  float least = 1.f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const uint2 e = lds64(__float_as_uint(cell_u(y[j], scale, shift)) * step + at);
+    const float d = fmaf(y[j], inv, -__uint_as_float(e.x));
+    const uint32_t code = e.y + static_cast<uint32_t>(static_cast<int>(__float_as_uint(d)) >> 31);
+    least = fminf(least, fabsf(d));
+    const int bit = BITS * (J + j);
+    w[bit / 32] += code << (bit % 32);
+    if (bit % 32 + BITS > 32) w[bit / 32 + 1] += code >> (32 - bit % 32);
+  }
+  if (least < kNear) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const uint2 e = lds64(__float_as_uint(cell_u(y[j], scale, shift)) * step + at);
+      if (fabsf(fmaf(y[j], inv, -__uint_as_float(e.x))) < kNear) mask |= 1u << (J + j);
+    }
+  }
 }
 
 // s + x rounded to s; returns the rounding error, exactly.
@@ -234,42 +302,54 @@ __device__ __forceinline__ uint32_t exact_cell(const float* P, const T* x, const
   return code;
 }
 
-// A warp's share of a tile: 32 rows, 64 coordinates each (32 where N is 32, on the first four
-// warps), from tensor memory to the planes.
-template <typename T, int BITS>
+// A warp's share of a tile: 32 rows, CH times 32 coordinates each (where N is 32: 32, on the
+// first four warps), from tensor memory to the planes.
+template <typename T, int BITS, int CH>
 __device__ __forceinline__ void search_tile(const AppendArgs& a, int kv, int h, int part, int tile, uint32_t tmem,
-                                            const RowInfo* info, const float* mids) {
+                                            const RowInfo* info, const float* mids, const Grid* grid, uint32_t cells) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool whole = a.N == kPD;
   if (!whole && warp >= 4) return;
-  float m[15];
-#pragma unroll
-  for (int i = 0; i + 1 < (1 << BITS); ++i) m[i] = mids[i];
+  const Grid g = *grid;
+  const uint32_t step = a.step, at = cells + (lane & (kCopies - 1)) * 8 - 0x4b000000u * step;
   const int r0 = 32 * (warp & 3), r = r0 + lane;
   RowInfo ri = info[r];
   if (ri.at < 0) ri.kind = 0;
   const T* X = static_cast<const T*>(a.X[kv]);
   const float* P = a.Pi[kv] + (static_cast<size_t>(h % a.rot) * kPD + part * a.N) * kPD;
   uint32_t* dst = reinterpret_cast<uint32_t*>((kv ? a.pg.vp : a.pg.kp) + ri.at * (16 * BITS)) + part * (whole ? 0 : BITS);
-  const int c0 = whole ? 2 * (warp >> 2) : 0;
-  uint32_t w[2 * BITS];
+  const int c0 = whole ? CH * (warp >> 2) : 0;
+  uint32_t w[CH * BITS];
   uint64_t mask = 0;
 #pragma unroll
-  for (int i = 0; i < 2 * BITS; ++i) w[i] = 0;
+  for (int i = 0; i < CH * BITS; ++i) w[i] = 0;
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
+  for (int c = 0; c < CH; ++c) {
     if (c == 1 && !whole) break;
     uint32_t v[BITS], near = 0;
 #pragma unroll
     for (int i = 0; i < BITS; ++i) v[i] = 0;
     const uint32_t from = tmem + (static_cast<uint32_t>(r0) << 16) + 32 * (c0 + c);
     float y[16];
-    tmem_ld16(from + 16, y);
-    search16<BITS, 31, 16>(y, ri.inv, m, v, near);
-    tmem_ld16(from, y);
-    search16<BITS, 15, 16>(y, ri.inv, m, v, near);
+    if (g.ok) {
+      const float scale = ri.inv * g.scale;
+      tmem_ld16(from, y);
+      look_up16<BITS, 0>(y, ri.inv, scale, g.shift, at, step, v, near);
+      tmem_ld16(from + 16, y);
+      look_up16<BITS, 16>(y, ri.inv, scale, g.shift, at, step, v, near);
+    } else {
+      float m[15];
 #pragma unroll
-    for (int i = 0; i < BITS; ++i) w[c * BITS + i] = ~v[i];
+      for (int i = 0; i + 1 < (1 << BITS); ++i) m[i] = mids[i];
+      tmem_ld16(from + 16, y);
+      search16<BITS, 31, 16>(y, ri.inv, m, v, near);
+      tmem_ld16(from, y);
+      search16<BITS, 15, 16>(y, ri.inv, m, v, near);
+#pragma unroll
+      for (int i = 0; i < BITS; ++i) v[i] = ~v[i];
+    }
+#pragma unroll
+    for (int i = 0; i < BITS; ++i) w[c * BITS + i] = v[i];
     mask |= static_cast<uint64_t>(near) << (32 * c);
   }
   if (ri.kind != 1) {
@@ -278,7 +358,8 @@ __device__ __forceinline__ void search_tile(const AppendArgs& a, int kv, int h, 
     for (int i = 0; i < BITS; ++i) {                       // one code throughout
       uint32_t x = 0;
       for (int j = 0; j < 32; ++j) x |= ((static_cast<uint32_t>(ri.code) >> ((32 * i + j) % BITS)) & 1u) << j;
-      w[i] = w[BITS + i] = x;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) w[c * BITS + i] = x;
     }
   }
   // near coordinates, four lanes' at a time
@@ -298,7 +379,7 @@ __device__ __forceinline__ void search_tile(const AppendArgs& a, int kv, int h, 
       mask &= mask - 1;
       constexpr uint32_t ones = (1u << BITS) - 1;
 #pragma unroll
-      for (int i = 0; i < 2 * BITS; ++i) {
+      for (int i = 0; i < CH * BITS; ++i) {
         const int sh = BITS * mine - 32 * i;               // where the code begins in this word
         if (sh > -BITS && sh < 32) {
           const uint32_t on = sh >= 0 ? ones << sh : ones >> -sh, v = sh >= 0 ? exact << sh : exact >> -sh;
@@ -309,16 +390,16 @@ __device__ __forceinline__ void search_tile(const AppendArgs& a, int kv, int h, 
   }
   if (ri.kind != 0) {
     uint32_t* o = dst + BITS * c0;
-    if (!whole) {
+    if (!whole || (CH == 1 && BITS == 3)) {                // 4 * BITS bytes
 #pragma unroll
       for (int i = 0; i < BITS; ++i) o[i] = w[i];
-    } else if constexpr (BITS == 3) {                      // 24 bytes, from a multiple of 8
+    } else if constexpr ((CH * BITS) % 4 == 0) {
 #pragma unroll
-      for (int i = 0; i < 3; ++i) reinterpret_cast<uint2*>(o)[i] = make_uint2(w[2 * i], w[2 * i + 1]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < BITS / 2; ++i)
+      for (int i = 0; i < CH * BITS / 4; ++i)
         reinterpret_cast<uint4*>(o)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    } else if constexpr ((CH * BITS) % 2 == 0) {           // 8 or 24 bytes, from a multiple of 8
+#pragma unroll
+      for (int i = 0; i < CH * BITS / 2; ++i) reinterpret_cast<uint2*>(o)[i] = make_uint2(w[2 * i], w[2 * i + 1]);
     }
   }
   if (part == 0 && warp < 4 && ri.kind != 0) (kv ? a.pg.vn : a.pg.kn)[ri.at] = static_cast<uint16_t>(ri.norm);
@@ -326,22 +407,31 @@ __device__ __forceinline__ void search_tile(const AppendArgs& a, int kv, int h, 
 
 template <typename T>
 constexpr int append_smem(int N) {
-  return kRows * 256 * (sizeof(T) == 4 ? 2 : 1) + N * 256 * 2 + 2 * kRows * static_cast<int>(sizeof(RowInfo)) + 64 + 64;
+  return kRows * 256 * (sizeof(T) == 4 ? 2 : 1) + N * 256 * 2 + 2 * kRows * static_cast<int>(sizeof(RowInfo)) +
+         kCells * kCopies * 8 + 64 + 64;
 }
 
+// fp32 rows take twice the shared memory: one CTA of 16 warps an SM instead of two of 8.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 1 : 2)
+constexpr int threads_of() { return sizeof(T) == 4 ? 512 : 256; }
+
+template <typename T>
+__global__ void __launch_bounds__(threads_of<T>(), sizeof(T) == 4 ? 1 : 2)
 append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr bool XLO = sizeof(T) == 4;                     // rows need a lo part
   constexpr int V = sizeof(T) / 2;                         // 16-byte loads of 8 values
+  constexpr int kThreads = threads_of<T>();
+  constexpr int RG = 512 / kThreads;                       // groups of 8 rows a warp takes, and chunks of 32 coordinates it searches
   extern __shared__ __align__(128) char smem[];
   const int N = a.N;
   char* sA = smem;                                         // hi, then lo of the rows
   char* sB = sA + kRows * 256 * (XLO ? 2 : 1);             // hi, then lo of the rotation
   RowInfo* infos = reinterpret_cast<RowInfo*>(sB + N * 512);   // of this tile and of the one before, in turn
-  float* mids = reinterpret_cast<float*>(infos + 2 * kRows);
+  Cell* cells = reinterpret_cast<Cell*>(infos + 2 * kRows);
+  float* mids = reinterpret_cast<float*>(cells + kCells * kCopies);
   uint64_t* bar = reinterpret_cast<uint64_t*>(mids + 16);
   uint32_t* slot = reinterpret_cast<uint32_t*>(bar + 1);
+  Grid* grid = reinterpret_cast<Grid*>(slot + 1);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   if (tid == 0) {
@@ -363,14 +453,14 @@ append_kernel(const __grid_constant__ AppendArgs a) {
   const int first = cta * per + min(cta, more), last = first + per + (cta < more ? 1 : 0);
 
   // Loads of an item, in registers while the tile before is searched.  Lane 8g + j of warp w
-  // holds chunks g, g + 4, g + 8, g + 12 (eight values) of rows 8w + j and 64 + 8w + j.
-  uint4 raw[2][4][V];
+  // holds chunks g, g + 4, g + 8, g + 12 (eight values) of rows 8w + j (and 64 + 8w + j).
+  uint4 raw[RG][4][V];
   int seq = -1, slt = -1, pos = 0, page = -1;
   auto request = [&](int item) {
     const int tile = item % a.tiles, hk = item / a.tiles / parts;
     const T* X = static_cast<const T*>(a.X[hk & 1]) + static_cast<size_t>(hk >> 1) * kPD;
 #pragma unroll
-    for (int rg = 0; rg < 2; ++rg) {
+    for (int rg = 0; rg < RG; ++rg) {
       const int i = tile * kRows + 64 * rg + 8 * warp + (lane & 7);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -406,7 +496,13 @@ append_kernel(const __grid_constant__ AppendArgs a) {
       loaded = hkp;
       // the warps are past the tile before this one's products, but not past its midpoints
       __syncthreads();
-      if (tid + 1 < (1 << a.bits[kv])) mids[tid] = 0.5f * (a.cb[kv][tid] + a.cb[kv][tid + 1]);   // within 2^-24: kNear has room
+      const int n = (1 << a.bits[kv]) - 1;
+      if (tid < n) mids[tid] = 0.5f * (a.cb[kv][tid] + a.cb[kv][tid + 1]);   // within 2^-24: kNear has room
+      __syncthreads();
+      const Grid g = make_grid(mids, n, lane);
+      if (tid == 0) *grid = g;
+      if (g.ok)
+        for (int e = tid; e < kCells * kCopies; e += kThreads) cells[e] = make_cell(mids, n, g, e / kCopies);
       const float* P = a.Pi[kv] + (static_cast<size_t>(h % a.rot) * kPD + part * N) * kPD;
       for (int e = tid; e < N * 16; e += kThreads) {
         const int d = (e >> 5) / 4 * 8 + (e & 7), c = (e >> 5) % 4 * 4 + ((e >> 3) & 3);   // as the rows: 8 rows x 4 chunks a warp
@@ -438,7 +534,7 @@ append_kernel(const __grid_constant__ AppendArgs a) {
     }
     // rows to fp16, scaled to 2^7
 #pragma unroll
-    for (int rg = 0; rg < 2; ++rg) {
+    for (int rg = 0; rg < RG; ++rg) {
       uint32_t top = 0;
       float x[4][8];
 #pragma unroll
@@ -519,9 +615,9 @@ append_kernel(const __grid_constant__ AppendArgs a) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     if (!__any_sync(0xffffffffu, lost)) {                  // else the product never came: nothing is written
       switch (a.bits[kv]) {
-        case 2: search_tile<T, 2>(a, kv, h, part, tile, tmem, info, mids); break;
-        case 3: search_tile<T, 3>(a, kv, h, part, tile, tmem, info, mids); break;
-        default: search_tile<T, 4>(a, kv, h, part, tile, tmem, info, mids); break;
+        case 2: search_tile<T, 2, RG>(a, kv, h, part, tile, tmem, info, mids, grid, smem_u32(cells)); break;
+        case 3: search_tile<T, 3, RG>(a, kv, h, part, tile, tmem, info, mids, grid, smem_u32(cells)); break;
+        default: search_tile<T, 4, RG>(a, kv, h, part, tile, tmem, info, mids, grid, smem_u32(cells)); break;
       }
     }
   }
@@ -558,6 +654,7 @@ cudaError_t launch(const tq_paged_cache& c, const T* K, const T* V, const int* r
   a.mass = mass;
   a.positions = positions;
   a.n = n;
+  a.step = kCopies * 8;
   a.B = B;
   a.rot = c.rot_heads;
   a.S = S;
@@ -572,7 +669,7 @@ cudaError_t launch(const tq_paged_cache& c, const T* K, const T* V, const int* r
   if (items > INT32_MAX) return cudaErrorInvalidValue;
   a.items = static_cast<int>(items);
   const int64_t most = static_cast<int64_t>(sms) * (sizeof(T) == 4 ? 1 : 2);
-  append_kernel<T><<<static_cast<int>(items < most ? items : most), kThreads, append_smem<T>(a.N), st>>>(a);
+  append_kernel<T><<<static_cast<int>(items < most ? items : most), threads_of<T>(), append_smem<T>(a.N), st>>>(a);
   return cudaGetLastError();
 }
 

@@ -343,6 +343,29 @@ def test_append(tq, kb, vb, bf16, n):
     assert np.array_equal(m.cpu().numpy(), mass) and np.array_equal(q.cpu().numpy(), pos)
 
 
+@pytest.mark.parametrize("kind", ["tight", "wide", "uneven", "same", "zero"])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_append_codebooks(tq, kind, bf16):
+    """Codebooks whose midpoints lie together, outside the coordinates' range, at very uneven
+    distances, on one another, or all at 0."""
+    for kb, vb in ((2, 3), (3, 4), (4, 2)):
+        p = Pages(tq, 1, 2, 160, 16, kb, vb, seed=7 * kb)
+        for name, b in (("kc", kb), ("vc", vb)):
+            c = getattr(p, name).astype(np.float64)
+            c = {"tight": 1e-3 * c, "wide": 8 * c, "uneven": np.sign(c) * (np.abs(c) + 0.02) ** 3 * 30, "same": np.full(c.size, 0.03),
+                 "zero": np.zeros(c.size)}[kind]
+            setattr(p, name, np.sort(c).astype(np.float32))
+        p.upload(tq)
+        rng = np.random.default_rng(kb)
+        K, V = (dev(rng.standard_normal((150, 2, D)).astype(np.float32)) for _ in range(2))
+        if bf16:
+            K, V = K.bfloat16(), V.bfloat16()
+        rows = np.stack([np.zeros(150), np.arange(150), np.arange(150)], 1).astype(np.int32)
+        before = p.host()
+        tq.append_paged(K, V, dev(rows), p.cache, p.t)
+        check_append(p, before, K.double().cpu().numpy(), V.double().cpu().numpy(), rows)
+
+
 def test_append_special_rows(tq):
     """Zero, one-hot, huge, tiny and subnormal rows; rows with NaN or infinity; coordinates
     that lie exactly on a midpoint."""
