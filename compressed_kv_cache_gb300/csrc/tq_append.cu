@@ -27,7 +27,7 @@ constexpr float kNear = 1.f / 131072.f;
 
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  asm("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));   // the table stays as it is while its readers run
   return v;
 }
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
@@ -302,9 +302,63 @@ __device__ __forceinline__ uint32_t exact_cell(const float* P, const T* x, const
   return code;
 }
 
-// A warp's share of a tile: 32 rows, CH times 32 coordinates each (where N is 32: 32, on the
-// first four warps), from tensor memory to the planes.
-template <typename T, int BITS, int CH>
+// The code of a near coordinate, eight lanes for it: its sum to 2^-24 of the row's length
+// against the fp32 length (within 2^-20), which settles all but a quarter of them, and
+// exact_cell for those.  All 32 lanes come here.
+template <typename T, int BITS>
+__device__ __forceinline__ uint32_t near_cell(const float* P, const T* x, const RowInfo& ri, const float* cb, const float* mids, bool live, int j) {
+  constexpr float kSure = 1.f / 524288.f;
+  const float s0 = ri.tiny ? 18446744073709551616.f : 1.f, s1 = ri.scale;
+  float s = 0.f, se = 0.f;
+  if (live) {
+    const float4* P4 = reinterpret_cast<const float4*>(P + 16 * j);
+    const uint4* x4 = reinterpret_cast<const uint4*>(x + 16 * j);
+    uint4 raw[2][sizeof(T) / 2];
+    float4 u[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) u[k] = __ldg(P4 + k);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int v = 0; v < static_cast<int>(sizeof(T) / 2); ++v) raw[k][v] = __ldg(x4 + k * (sizeof(T) / 2) + v);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float xv[8];
+      widen(raw[k], xv);
+      const float pv[8] = {u[2 * k].x, u[2 * k].y, u[2 * k].z, u[2 * k].w, u[2 * k + 1].x, u[2 * k + 1].y, u[2 * k + 1].z, u[2 * k + 1].w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float xs = xv[i] * s0 * s1;
+        const float d = __fmul_rn(xs, pv[i]);
+        se += fmaf(xs, pv[i], -d) + add_exact(s, d);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    const float so = __shfl_xor_sync(0xffffffffu, s, o), seo = __shfl_xor_sync(0xffffffffu, se, o);
+    se += seo + add_exact(s, so);
+  }
+  const float y = (s + se) * (128.f * ri.inv);
+  uint32_t code = 0;
+  float least = 1.f;
+#pragma unroll
+  for (int i = 0; i + 1 < (1 << BITS); ++i) {
+    const float d = y - mids[i];
+    code += d > 0.f ? 1u : 0u;
+    least = fminf(least, fabsf(d));
+  }
+  const bool open = live && least < kSure;
+  if (__any_sync(0xffffffffu, open)) {
+    const uint32_t exact = exact_cell<T, BITS>(P, x, ri, cb, mids, open, j);
+    if (open) code = exact;                                // lane 0 of the eight has it
+  }
+  return code;
+}
+
+// A warp's share of a tile: 32 rows, 32 coordinates each (where N is 32, on the first four
+// warps), from tensor memory to the planes.
+template <typename T, int BITS>
 __device__ __forceinline__ void search_tile(const AppendArgs& a, int kv, int h, int part, int tile, uint32_t tmem,
                                             const RowInfo* info, const float* mids, const Grid* grid, uint32_t cells) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -318,39 +372,30 @@ __device__ __forceinline__ void search_tile(const AppendArgs& a, int kv, int h, 
   const T* X = static_cast<const T*>(a.X[kv]);
   const float* P = a.Pi[kv] + (static_cast<size_t>(h % a.rot) * kPD + part * a.N) * kPD;
   uint32_t* dst = reinterpret_cast<uint32_t*>((kv ? a.pg.vp : a.pg.kp) + ri.at * (16 * BITS)) + part * (whole ? 0 : BITS);
-  const int c0 = whole ? CH * (warp >> 2) : 0;
-  uint32_t w[CH * BITS];
-  uint64_t mask = 0;
+  const int c0 = whole ? warp >> 2 : 0;
+  uint32_t w[BITS], mask = 0;
 #pragma unroll
-  for (int i = 0; i < CH * BITS; ++i) w[i] = 0;
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    if (c == 1 && !whole) break;
-    uint32_t v[BITS], near = 0;
-#pragma unroll
-    for (int i = 0; i < BITS; ++i) v[i] = 0;
-    const uint32_t from = tmem + (static_cast<uint32_t>(r0) << 16) + 32 * (c0 + c);
+  for (int i = 0; i < BITS; ++i) w[i] = 0;
+  {
+    const uint32_t from = tmem + (static_cast<uint32_t>(r0) << 16) + 32 * c0;
     float y[16];
     if (g.ok) {
       const float scale = ri.inv * g.scale;
       tmem_ld16(from, y);
-      look_up16<BITS, 0>(y, ri.inv, scale, g.shift, at, step, v, near);
+      look_up16<BITS, 0>(y, ri.inv, scale, g.shift, at, step, w, mask);
       tmem_ld16(from + 16, y);
-      look_up16<BITS, 16>(y, ri.inv, scale, g.shift, at, step, v, near);
+      look_up16<BITS, 16>(y, ri.inv, scale, g.shift, at, step, w, mask);
     } else {
       float m[15];
 #pragma unroll
       for (int i = 0; i + 1 < (1 << BITS); ++i) m[i] = mids[i];
       tmem_ld16(from + 16, y);
-      search16<BITS, 31, 16>(y, ri.inv, m, v, near);
+      search16<BITS, 31, 16>(y, ri.inv, m, w, mask);
       tmem_ld16(from, y);
-      search16<BITS, 15, 16>(y, ri.inv, m, v, near);
+      search16<BITS, 15, 16>(y, ri.inv, m, w, mask);
 #pragma unroll
-      for (int i = 0; i < BITS; ++i) v[i] = ~v[i];
+      for (int i = 0; i < BITS; ++i) w[i] = ~w[i];
     }
-#pragma unroll
-    for (int i = 0; i < BITS; ++i) w[c * BITS + i] = v[i];
-    mask |= static_cast<uint64_t>(near) << (32 * c);
   }
   if (ri.kind != 1) {
     mask = 0;
@@ -358,8 +403,7 @@ __device__ __forceinline__ void search_tile(const AppendArgs& a, int kv, int h, 
     for (int i = 0; i < BITS; ++i) {                       // one code throughout
       uint32_t x = 0;
       for (int j = 0; j < 32; ++j) x |= ((static_cast<uint32_t>(ri.code) >> ((32 * i + j) % BITS)) & 1u) << j;
-#pragma unroll
-      for (int c = 0; c < CH; ++c) w[c * BITS + i] = x;
+      w[i] = x;
     }
   }
   // near coordinates, four lanes' at a time
@@ -368,9 +412,9 @@ __device__ __forceinline__ void search_tile(const AppendArgs& a, int kv, int h, 
     for (int k = 0; k < (lane >> 3); ++k) left &= left - 1;
     const bool live = left != 0;
     const int owner = live ? __ffs(left) - 1 : 0;
-    const int mine = __ffsll(static_cast<long long>(mask)) - 1;
+    const int mine = __ffs(mask) - 1;
     const int at = __shfl_sync(0xffffffffu, mine, owner);
-    const uint32_t code = exact_cell<T, BITS>(P + (32 * c0 + (live ? at : 0)) * kPD,
+    const uint32_t code = near_cell<T, BITS>(P + (32 * c0 + (live ? at : 0)) * kPD,
                                               X + (static_cast<size_t>(tile * kRows + r0 + owner) * a.pg.H + h) * kPD,
                                               info[r0 + owner], a.cb[kv], mids, live, lane & 7);
     const int rank = __popc(waiting & ((1u << lane) - 1));
@@ -379,7 +423,7 @@ __device__ __forceinline__ void search_tile(const AppendArgs& a, int kv, int h, 
       mask &= mask - 1;
       constexpr uint32_t ones = (1u << BITS) - 1;
 #pragma unroll
-      for (int i = 0; i < CH * BITS; ++i) {
+      for (int i = 0; i < BITS; ++i) {
         const int sh = BITS * mine - 32 * i;               // where the code begins in this word
         if (sh > -BITS && sh < 32) {
           const uint32_t on = sh >= 0 ? ones << sh : ones >> -sh, v = sh >= 0 ? exact << sh : exact >> -sh;
@@ -390,56 +434,103 @@ __device__ __forceinline__ void search_tile(const AppendArgs& a, int kv, int h, 
   }
   if (ri.kind != 0) {
     uint32_t* o = dst + BITS * c0;
-    if (!whole || (CH == 1 && BITS == 3)) {                // 4 * BITS bytes
+    if constexpr (BITS == 4) {
+      *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else if constexpr (BITS == 2) {
+      *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
+    } else {
 #pragma unroll
       for (int i = 0; i < BITS; ++i) o[i] = w[i];
-    } else if constexpr ((CH * BITS) % 4 == 0) {
-#pragma unroll
-      for (int i = 0; i < CH * BITS / 4; ++i)
-        reinterpret_cast<uint4*>(o)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    } else if constexpr ((CH * BITS) % 2 == 0) {           // 8 or 24 bytes, from a multiple of 8
-#pragma unroll
-      for (int i = 0; i < CH * BITS / 2; ++i) reinterpret_cast<uint2*>(o)[i] = make_uint2(w[2 * i], w[2 * i + 1]);
     }
   }
   if (part == 0 && warp < 4 && ri.kind != 0) (kv ? a.pg.vn : a.pg.kn)[ri.at] = static_cast<uint16_t>(ri.norm);
 }
 
+constexpr int kThreads = 512;
+
 template <typename T>
 constexpr int append_smem(int N) {
-  return kRows * 256 * (sizeof(T) == 4 ? 2 : 1) + N * 256 * 2 + 2 * kRows * static_cast<int>(sizeof(RowInfo)) +
+  return 2 * kRows * 256 * (sizeof(T) == 4 ? 2 : 1) + N * 256 * 2 + 3 * kRows * static_cast<int>(sizeof(RowInfo)) +
          kCells * kCopies * 8 + 64 + 64;
 }
 
-// fp32 rows take twice the shared memory: one CTA of 16 warps an SM instead of two of 8.
-template <typename T>
-constexpr int threads_of() { return sizeof(T) == 4 ? 512 : 256; }
+// Where a CTA is among the items: tile by tile, then the next part of a rotation.
+struct Place {
+  int item, tile, hkp;
+  __device__ __forceinline__ void next(int tiles) {
+    ++item;
+    if (++tile == tiles) {
+      tile = 0;
+      ++hkp;
+    }
+  }
+};
 
+// One CTA of 16 warps an SM.  Two tiles are under way: while one is searched, the product of
+// the next one runs and the rows of the one behind it are loaded.  One barrier a tile.
 template <typename T>
-__global__ void __launch_bounds__(threads_of<T>(), sizeof(T) == 4 ? 1 : 2)
+__global__ void __launch_bounds__(kThreads, 1)
 append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr bool XLO = sizeof(T) == 4;                     // rows need a lo part
   constexpr int V = sizeof(T) / 2;                         // 16-byte loads of 8 values
-  constexpr int kThreads = threads_of<T>();
-  constexpr int RG = 512 / kThreads;                       // groups of 8 rows a warp takes, and chunks of 32 coordinates it searches
+  constexpr int kA = kRows * 256 * (XLO ? 2 : 1);          // operand of a tile: hi, then lo
   extern __shared__ __align__(128) char smem[];
   const int N = a.N;
-  char* sA = smem;                                         // hi, then lo of the rows
-  char* sB = sA + kRows * 256 * (XLO ? 2 : 1);             // hi, then lo of the rotation
-  RowInfo* infos = reinterpret_cast<RowInfo*>(sB + N * 512);   // of this tile and of the one before, in turn
-  Cell* cells = reinterpret_cast<Cell*>(infos + 2 * kRows);
+  char* sA = smem;                                         // of two tiles
+  char* sB = sA + 2 * kA;                                  // hi, then lo of the rotation
+  RowInfo* infos = reinterpret_cast<RowInfo*>(sB + N * 512);   // of three tiles: a warp may still search the one before
+  Cell* cells = reinterpret_cast<Cell*>(infos + 3 * kRows);
   float* mids = reinterpret_cast<float*>(cells + kCells * kCopies);
-  uint64_t* bar = reinterpret_cast<uint64_t*>(mids + 16);
-  uint32_t* slot = reinterpret_cast<uint32_t*>(bar + 1);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(mids + 16);
+  uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 2);
   Grid* grid = reinterpret_cast<Grid*>(slot + 1);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
+  const bool whole = N == kPD;
+  const int per = a.items / gridDim.x, more = a.items - per * gridDim.x;
+  const int cta = blockIdx.x;
+  const int first = cta * per + min(cta, more), last = first + per + (cta < more ? 1 : 0);
+  auto part_of = [&](int hkp) { return whole ? 0 : hkp & 3; };
+  auto hk_of = [&](int hkp) { return whole ? hkp : hkp >> 2; };
+
+  // Loads of a tile, and where its rows go, both a tile ahead.  Lane 8g + j of warp w holds
+  // chunks g, g + 4, g + 8, g + 12 (eight values) of row 8w + j.
+  uint4 raw[4][V];
+  int seq = -1, slt = -1, pos = 0, page = -1;
+  auto request = [&](const Place& p) {
+    const int hk = hk_of(p.hkp), i = p.tile * kRows + 8 * warp + (lane & 7);
+    const T* X = static_cast<const T*>(a.X[hk & 1]) + (static_cast<size_t>(i) * a.pg.H + (hk >> 1)) * kPD + 8 * (lane >> 3);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) raw[k][v] = i < a.n ? __ldg(reinterpret_cast<const uint4*>(X + 32 * k) + v) : make_uint4(0, 0, 0, 0);
+    }
+    const int j = p.tile * kRows + tid;
+    seq = -1;
+    if (tid < kRows && j < a.n) {
+      const int* r = a.rows + 3 * static_cast<size_t>(j);
+      seq = r[0];
+      slt = r[1];
+      pos = r[2];
+    }
+  };
+  auto find_page = [&]() {
+    const bool in = seq >= 0 && slt >= 0 && seq < a.B && slt < a.cap;
+    page = in ? a.pg.table[static_cast<size_t>(seq) * a.pg.max_pages + (slt >> a.pg.shift)] : -1;
+  };
+
+  Place ahead = {first, first % a.tiles, first / a.tiles};   // the tile whose loads are under way
+  if (first < last) {
+    request(ahead);
+    find_page();
+  }
   if (tid == 0) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(bar)) : "memory");
+#pragma unroll
+    for (int i = 0; i < 2; ++i) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(bars + i)) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(N) : "memory");
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(2 * N) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -447,81 +538,41 @@ append_kernel(const __grid_constant__ AppendArgs a) {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *slot;
 
-  const int parts = kPD / N;
-  const int per = a.items / gridDim.x, more = a.items - per * gridDim.x;
-  const int cta = blockIdx.x;
-  const int first = cta * per + min(cta, more), last = first + per + (cta < more ? 1 : 0);
-
-  // Loads of an item, in registers while the tile before is searched.  Lane 8g + j of warp w
-  // holds chunks g, g + 4, g + 8, g + 12 (eight values) of rows 8w + j (and 64 + 8w + j).
-  uint4 raw[RG][4][V];
-  int seq = -1, slt = -1, pos = 0, page = -1;
-  auto request = [&](int item) {
-    const int tile = item % a.tiles, hk = item / a.tiles / parts;
-    const T* X = static_cast<const T*>(a.X[hk & 1]) + static_cast<size_t>(hk >> 1) * kPD;
-#pragma unroll
-    for (int rg = 0; rg < RG; ++rg) {
-      const int i = tile * kRows + 64 * rg + 8 * warp + (lane & 7);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint4* src = reinterpret_cast<const uint4*>(X + static_cast<size_t>(i) * a.pg.H * kPD + 8 * ((lane >> 3) + 4 * k));
-#pragma unroll
-        for (int v = 0; v < V; ++v) raw[rg][k][v] = i < a.n ? __ldg(src + v) : make_uint4(0, 0, 0, 0);
-      }
+  // Rows part * N .. of a head's rotation, times 2^7, and its codebook's midpoints.  Every warp is
+  // past the products and the search of the tiles before.
+  auto load_rotation = [&](int hkp) {
+    const int hk = hk_of(hkp), kv = hk & 1, h = hk >> 1;
+    const float* P = a.Pi[kv] + (static_cast<size_t>(h % a.rot) * kPD + part_of(hkp) * N) * kPD;
+#pragma unroll 2
+    for (int e = tid; e < N * 16; e += kThreads) {
+      const int d = (e >> 5) / 4 * 8 + (e & 7), c = (e >> 5) % 4 * 4 + ((e >> 3) & 3);   // as the rows: 8 rows x 4 chunks a warp
+      const float4 u = __ldg(reinterpret_cast<const float4*>(P + d * kPD + 8 * c));
+      const float4 v = __ldg(reinterpret_cast<const float4*>(P + d * kPD + 8 * c + 4));
+      const float x[8] = {128.f * u.x, 128.f * u.y, 128.f * u.z, 128.f * u.w, 128.f * v.x, 128.f * v.y, 128.f * v.z, 128.f * v.w};
+      const int at = c * (N * 16) + (d >> 3) * 128 + (d & 7) * 16;
+      *reinterpret_cast<uint4*>(sB + at) = hi_chunk(x);
+      *reinterpret_cast<uint4*>(sB + N * 256 + at) = lo_chunk(x);
     }
-    seq = -1;
-    if (tid < kRows && tile * kRows + tid < a.n) {
-      const int* r = a.rows + 3 * static_cast<size_t>(tile * kRows + tid);
-      seq = r[0];
-      slt = r[1];
-      pos = r[2];
-    }
+    const int n = (1 << a.bits[kv]) - 1;
+    if (tid < n) mids[tid] = 0.5f * (a.cb[kv][tid] + a.cb[kv][tid + 1]);   // within 2^-24: kNear has room
+    __syncthreads();
+    const Grid g = make_grid(mids, n, lane);
+    if (tid == 0) *grid = g;
+    if (g.ok) cells[tid] = make_cell(mids, n, g, tid / kCopies);
+    static_assert(kCells * kCopies == kThreads, "an entry a thread");
   };
-  // The page of this thread's row: its number is wanted a tile later.
-  auto find_page = [&]() {
-    const bool in = seq >= 0 && slt >= 0 && seq < a.B && slt < a.cap;
-    page = in ? a.pg.table[static_cast<size_t>(seq) * a.pg.max_pages + (slt >> a.pg.shift)] : -1;
-  };
-  if (first < last) {
-    request(first);
-    find_page();
-  }
 
-  int loaded = -1;
-  uint32_t phase = 0;
-  bool lost = false;
-  for (int item = first; item < last; ++item) {
-    const int tile = item % a.tiles, hkp = item / a.tiles, part = hkp % parts, hk = hkp / parts, kv = hk & 1, h = hk >> 1;
-    if (hkp != loaded) {                                   // rows part * N .. of the head's rotation, times 2^7
-      loaded = hkp;
-      // the warps are past the tile before this one's products, but not past its midpoints
-      __syncthreads();
-      const int n = (1 << a.bits[kv]) - 1;
-      if (tid < n) mids[tid] = 0.5f * (a.cb[kv][tid] + a.cb[kv][tid + 1]);   // within 2^-24: kNear has room
-      __syncthreads();
-      const Grid g = make_grid(mids, n, lane);
-      if (tid == 0) *grid = g;
-      if (g.ok)
-        for (int e = tid; e < kCells * kCopies; e += kThreads) cells[e] = make_cell(mids, n, g, e / kCopies);
-      const float* P = a.Pi[kv] + (static_cast<size_t>(h % a.rot) * kPD + part * N) * kPD;
-      for (int e = tid; e < N * 16; e += kThreads) {
-        const int d = (e >> 5) / 4 * 8 + (e & 7), c = (e >> 5) % 4 * 4 + ((e >> 3) & 3);   // as the rows: 8 rows x 4 chunks a warp
-        const float4 u = __ldg(reinterpret_cast<const float4*>(P + d * kPD + 8 * c));
-        const float4 v = __ldg(reinterpret_cast<const float4*>(P + d * kPD + 8 * c + 4));
-        const float x[8] = {128.f * u.x, 128.f * u.y, 128.f * u.z, 128.f * u.w, 128.f * v.x, 128.f * v.y, 128.f * v.z, 128.f * v.w};
-        const int at = c * (N * 16) + (d >> 3) * 128 + (d & 7) * 16;
-        *reinterpret_cast<uint4*>(sB + at) = hi_chunk(x);
-        *reinterpret_cast<uint4*>(sB + N * 256 + at) = lo_chunk(x);
-      }
-    }
-    RowInfo* info = infos + (item & 1) * kRows;
-    // where each row goes
-    if (tid < kRows) {
+  // The loaded tile to fp16 rows, its product on the way, and the next one's loads.
+  auto start_tile = [&]() {
+    const int hk = hk_of(ahead.hkp), kv = hk & 1, h = hk >> 1, buf = (ahead.item - first) & 1;
+    RowInfo* info = infos + (ahead.item % 3) * kRows;
+    char* A = sA + buf * kA;
+    if (tid < kRows) {                                     // where each row goes
       long long at = -1;
       if (seq >= 0 && slt >= 0) {
         if (static_cast<unsigned>(page) < static_cast<unsigned>(a.pg.n_pages)) {
           at = static_cast<long long>(a.pg.row(page, h, slt));
-          if (kv == 0 && part == 0) {
+          if (kv == 0 && part_of(ahead.hkp) == 0) {
             const size_t m = (static_cast<size_t>(seq) * a.pg.H + h) * a.S + slt;
             if (a.mass != nullptr) a.mass[m] = 0.f;
             if (a.positions != nullptr) a.positions[m] = pos;
@@ -532,99 +583,117 @@ append_kernel(const __grid_constant__ AppendArgs a) {
       }
       info[tid].at = at;
     }
-    // rows to fp16, scaled to 2^7
+    // rows scaled to 2^7
+    uint32_t top = 0;
+    float x[4][8];
 #pragma unroll
-    for (int rg = 0; rg < RG; ++rg) {
-      uint32_t top = 0;
-      float x[4][8];
+    for (int k = 0; k < 4; ++k) {
+      widen(raw[k], x[k]);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        widen(raw[rg][k], x[k]);
+      for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[k][i]) & 0x7fffffffu);
+    }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
+    const bool finite = top < 0x7f800000u;
+    // powers of two: up to 2^64 first for rows that are tiny throughout, then to 2^7
+    const float s0 = top < 0x21800000u ? 18446744073709551616.f : 1.f;            // below 2^-60
+    const int e = static_cast<int>(__float_as_uint(__uint_as_float(top) * s0) >> 23);   // 1 .. 254 for a row that is neither zero nor infinite
+    int k2 = 134 - e;                                                             // -120 .. 126
+    k2 = k2 > 126 ? 126 : k2;
+    const float s1 = finite && top != 0 ? __uint_as_float(static_cast<uint32_t>(127 + k2) << 23) : 0.f;
+    if (s0 != 1.f) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[k][i]) & 0x7fffffffu);
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[k][i] *= s0;
+    }
+    float sum = 0.f;
+    const int r = 8 * warp + (lane & 7);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {                        // NaN and infinity stay within their row, which takes no codes from it
+        x[k][i] *= s1;
+        sum = fmaf(x[k][i], x[k][i], sum);
       }
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
-      const bool finite = top < 0x7f800000u;
-      // powers of two: up to 2^64 first for rows that are tiny throughout, then to 2^7
-      const float s0 = top < 0x21800000u ? 18446744073709551616.f : 1.f;          // below 2^-60
-      const float t = __uint_as_float(top) * s0;
-      const int e = static_cast<int>(__float_as_uint(t) >> 23);                   // 1 .. 254 for a row that is neither zero nor infinite
-      const int k2 = 134 - e;                                                     // -120 .. 126
-      const float s1 = finite && top != 0 ? __uint_as_float(static_cast<uint32_t>(127 + (k2 > 126 ? 126 : k2)) << 23) : 0.f;
-      if (s0 != 1.f) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[k][i] *= s0;
-      }
-      float sum = 0.f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {                      // NaN and infinity stay within their row, which takes no codes from it
-          x[k][i] *= s1;
-          sum = fmaf(x[k][i], x[k][i], sum);
-        }
-        const int r = 64 * rg + 8 * warp + (lane & 7), c = (lane >> 3) + 4 * k;
-        const int at = c * (kRows * 16) + (r >> 3) * 128 + (r & 7) * 16;
-        *reinterpret_cast<uint4*>(sA + at) = hi_chunk(x[k]);
-        if constexpr (XLO) *reinterpret_cast<uint4*>(sA + kRows * 256 + at) = lo_chunk(x[k]);
-      }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-      if (lane < 8) {
-        RowInfo& ri = info[64 * rg + 8 * warp + lane];
-        const float len = sqrtf(sum);
-        const int kind = !finite ? 3 : top == 0 ? 2 : 1;
-        ri.kind = kind;
-        ri.scale = s1;
-        ri.tiny = s0 != 1.f;
-        ri.inv = kind == 1 ? 1.f / (128.f * len) : 0.f;
-        // the length: powers of two taken back, one rounding in fp32 and one to fp16
-        const float n = kind == 1 ? len / s1 / s0 : kind == 2 ? 0.f : __uint_as_float(top > 0x7f800000u ? 0x7fc00000u : 0x7f800000u);
-        ri.norm = __half_as_ushort(__float2half_rn(n));
-        int zero = 0;
-        if (kind == 2)
-          for (int i = 0; i + 1 < (1 << a.bits[kv]); ++i)
-            zero += static_cast<double>(a.cb[kv][i]) + static_cast<double>(a.cb[kv][i + 1]) < 0.0 ? 1 : 0;
-        ri.code = zero;
-      }
+      const int at = ((lane >> 3) + 4 * k) * (kRows * 16) + (r >> 3) * 128 + (r & 7) * 16;
+      *reinterpret_cast<uint4*>(A + at) = hi_chunk(x[k]);
+      if constexpr (XLO) *reinterpret_cast<uint4*>(A + kRows * 256 + at) = lo_chunk(x[k]);
+    }
+    sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+    if (lane < 8) {
+      RowInfo& ri = info[r];
+      const float len = sqrtf(sum);
+      const int kind = !finite ? 3 : top == 0 ? 2 : 1;
+      ri.kind = kind;
+      ri.scale = s1;
+      ri.tiny = s0 != 1.f;
+      ri.inv = kind == 1 ? 1.f / (128.f * len) : 0.f;
+      // the length: powers of two taken back, one rounding in fp32 and one to fp16
+      const float back = __uint_as_float(static_cast<uint32_t>(127 - k2) << 23) * (s0 != 1.f ? 5.42101086e-20f : 1.f);
+      const float n = kind == 1 ? len * back : kind == 2 ? 0.f : __uint_as_float(top > 0x7f800000u ? 0x7fc00000u : 0x7f800000u);
+      ri.norm = __half_as_ushort(__float2half_rn(n));
+      int zero = 0;
+      if (kind == 2)
+        for (int i = 0; i + 1 < (1 << a.bits[kv]); ++i) zero += a.cb[kv][i] + a.cb[kv][i + 1] < 0.f ? 1 : 0;   // the sign is exact
+      ri.code = zero;
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     if (tid == 0) {
-      const uint32_t A = smem_u32(sA), Bm = smem_u32(sB);
+      const uint32_t Aa = smem_u32(A), Bm = smem_u32(sB), d = tmem + buf * N;
       const uint32_t la = kRows * 16, lb = N * 16;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) mma_f16(tmem, operand(A + k * 2 * la, la), operand(Bm + k * 2 * lb, lb), N, k != 0);
+      for (int k = 0; k < 8; ++k) mma_f16(d, operand(Aa + k * 2 * la, la), operand(Bm + k * 2 * lb, lb), N, k != 0);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) mma_f16(tmem, operand(A + k * 2 * la, la), operand(Bm + N * 256 + k * 2 * lb, lb), N, true);
+      for (int k = 0; k < 8; ++k) mma_f16(d, operand(Aa + k * 2 * la, la), operand(Bm + N * 256 + k * 2 * lb, lb), N, true);
       if constexpr (XLO) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) mma_f16(tmem, operand(A + kRows * 256 + k * 2 * la, la), operand(Bm + k * 2 * lb, lb), N, true);
+        for (int k = 0; k < 8; ++k) mma_f16(d, operand(Aa + kRows * 256 + k * 2 * la, la), operand(Bm + k * 2 * lb, lb), N, true);
       }
-      asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+      asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bars + buf)) : "memory");
     }
-    if (item + 1 < last) request(item + 1);
-    if (!lost && !wait_parity_bounded(smem_u32(bar), phase, kFaultPaged)) lost = true;
-    phase ^= 1;
-    find_page();
+    ahead.next(a.tiles);
+    if (ahead.item < last) request(ahead);
+  };
+
+  bool lost = false;
+  Place now = ahead;
+  int loaded = -1;
+  while (now.item < last) {
+    if (ahead.item == now.item) {                          // a rotation begins: nothing is under way
+      if (loaded != now.hkp) {
+        __syncthreads();
+        load_rotation(now.hkp);
+        loaded = now.hkp;
+      }
+      start_tile();
+      if (ahead.item < last) find_page();
+    }
+    if (ahead.item < last && ahead.hkp == loaded) start_tile();
+    const int i = now.item - first;
+    if (!lost && !wait_parity_bounded(smem_u32(bars + (i & 1)), (i >> 1) & 1, kFaultPaged)) lost = true;
+    if (ahead.item < last) find_page();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     if (!__any_sync(0xffffffffu, lost)) {                  // else the product never came: nothing is written
+      const int hk = hk_of(now.hkp), kv = hk & 1, h = hk >> 1, part = part_of(now.hkp);
+      const RowInfo* info = infos + (now.item % 3) * kRows;
+      const uint32_t d = tmem + (i & 1) * N;
       switch (a.bits[kv]) {
-        case 2: search_tile<T, 2, RG>(a, kv, h, part, tile, tmem, info, mids, grid, smem_u32(cells)); break;
-        case 3: search_tile<T, 3, RG>(a, kv, h, part, tile, tmem, info, mids, grid, smem_u32(cells)); break;
-        default: search_tile<T, 4, RG>(a, kv, h, part, tile, tmem, info, mids, grid, smem_u32(cells)); break;
+        case 2: search_tile<T, 2>(a, kv, h, part, now.tile, d, info, mids, grid, smem_u32(cells)); break;
+        case 3: search_tile<T, 3>(a, kv, h, part, now.tile, d, info, mids, grid, smem_u32(cells)); break;
+        default: search_tile<T, 4>(a, kv, h, part, now.tile, d, info, mids, grid, smem_u32(cells)); break;
       }
     }
+    now.next(a.tiles);
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(N) : "memory");
+  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * N) : "memory");
 }
 
 template <typename T>
@@ -664,12 +733,12 @@ cudaError_t launch(const tq_paged_cache& c, const T* K, const T* V, const int* r
   a.bits[1] = c.v_bits;
   a.tiles = ceil_div(n, kRows);
   const int64_t whole = static_cast<int64_t>(a.tiles) * c.H * 2;
-  a.N = whole * 4 <= 2 * sms ? 32 : kPD;
+  a.N = whole * 4 <= sms ? 32 : kPD;
   const int64_t items = whole * (kPD / a.N);
   if (items > INT32_MAX) return cudaErrorInvalidValue;
   a.items = static_cast<int>(items);
-  const int64_t most = static_cast<int64_t>(sms) * (sizeof(T) == 4 ? 1 : 2);
-  append_kernel<T><<<static_cast<int>(items < most ? items : most), threads_of<T>(), append_smem<T>(a.N), st>>>(a);
+  const int64_t most = sms;
+  append_kernel<T><<<static_cast<int>(items < most ? items : most), kThreads, append_smem<T>(a.N), st>>>(a);
   return cudaGetLastError();
 }
 
