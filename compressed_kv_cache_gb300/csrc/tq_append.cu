@@ -106,57 +106,9 @@ struct AppendArgs {
   int items;                 // (head, keys or values, part of the rotation, tile)
 };
 
-// One coordinate v, number J of 32: its cell among the midpoints m (ascending) by binary search.
-// Each step's bit is the sign of v - midpoint, moved into the packed word from below by one
-// funnel shift (so coordinates come from the last to the first, and the words hold the bits'
-// complement).  Returns the least distance to a midpoint it met; both neighbours of v are
-// among them.
-template <int BITS, int J>
-__device__ __forceinline__ float put_cell(float v, const float (&m)[15], uint32_t (&w)[BITS]) {
-  auto push = [&](float d, int bit) {
-    uint32_t& x = w[(BITS * J + bit) / 32];
-    x = __funnelshift_l(__float_as_uint(d), x, 1);
-  };
-  constexpr int n = 1 << BITS;
-  const float d0 = v - m[n / 2 - 1];
-  push(d0, BITS - 1);
-  const bool p = d0 > 0.f;
-  if constexpr (BITS == 2) {
-    const float d1 = v - (p ? m[2] : m[0]);
-    push(d1, 0);
-    return fminf(fabsf(d0), fabsf(d1));
-  } else if constexpr (BITS == 3) {
-    const float d1 = v - (p ? m[5] : m[1]);
-    const float a = p ? m[4] : m[0], b = p ? m[6] : m[2];
-    push(d1, 1);
-    const float d2 = v - (d1 > 0.f ? b : a);
-    push(d2, 0);
-    return fminf(fminf(fabsf(d0), fabsf(d1)), fabsf(d2));
-  } else {
-    const float d1 = v - (p ? m[11] : m[3]);
-    const float a0 = p ? m[8] : m[0], a1 = p ? m[9] : m[1], a2 = p ? m[10] : m[2];
-    const float b0 = p ? m[12] : m[4], b1 = p ? m[13] : m[5], b2 = p ? m[14] : m[6];
-    push(d1, 2);
-    const bool q = d1 > 0.f;
-    const float c0 = q ? b0 : a0, c1 = q ? b1 : a1, c2 = q ? b2 : a2;
-    const float d2 = v - c1;
-    push(d2, 1);
-    const float d3 = v - (d2 > 0.f ? c2 : c0);
-    push(d3, 0);
-    return fminf(fminf(fabsf(d0), fabsf(d1)), fminf(fabsf(d2), fabsf(d3)));
-  }
-}
-
-// Coordinates J .. J - 15 of 32: packed codes to w, near ones to the mask.
-template <int BITS, int J, int LEFT>
-__device__ __forceinline__ void search16(const float (&y)[16], float inv, const float (&m)[15], uint32_t (&w)[BITS], uint32_t& mask) {
-  if (put_cell<BITS, J>(y[J & 15] * inv, m, w) < kNear) mask |= 1u << J;
-  if constexpr (LEFT > 1) search16<BITS, J - 1, LEFT - 1>(y, inv, m, w, mask);
-}
-
 // Search table: the midpoints' range in cells, each with the midpoint k nearest to it; the code
 // of a v in the cell is k + (v > midpoint k).  The cells are a 62nd of the range or less
-// apart from every other midpoint (or the table is not used: search16), so that no v has
+// apart from every other midpoint (or the table is not used: count16), so that no v has
 // another midpoint nearer by.  The cell of v is a saturating FMA and a rounding.
 struct Cell {
   float mid;
@@ -188,6 +140,27 @@ __device__ __forceinline__ Cell make_cell(const float* mids, int n, const Grid& 
   for (int j = 1; j < n; ++j)
     if (fabsf(mids[j] - c) < fabsf(mids[k] - c)) k = j;
   return {mids[k], k + 1};
+}
+
+// 16 coordinates from J of 32 where the grid does not serve: every midpoint in turn.
+template <int BITS, int J>
+__device__ __forceinline__ void count16(const float (&y)[16], float inv, const float* mids, uint32_t (&w)[BITS], uint32_t& mask) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const float v = y[j] * inv;
+    uint32_t code = 0;
+    float least = 1.f;
+#pragma unroll 1
+    for (int i = 0; i + 1 < (1 << BITS); ++i) {
+      const float d = v - mids[i];
+      code += d > 0.f ? 1u : 0u;
+      least = fminf(least, fabsf(d));
+    }
+    if (least < kNear) mask |= 1u << (J + j);
+    const int bit = BITS * (J + j);
+    w[bit / 32] += code << (bit % 32);
+    if (bit % 32 + BITS > 32) w[bit / 32 + 1] += code >> (32 - bit % 32);
+  }
 }
 
 // Coordinates J .. J + 15 of 32 (J 0 or 16): packed codes to w, near ones to the mask.  at:
@@ -386,15 +359,10 @@ __device__ __forceinline__ void search_tile(const AppendArgs& a, int kv, int h, 
       tmem_ld16(from + 16, y);
       look_up16<BITS, 16>(y, ri.inv, scale, g.shift, at, step, w, mask);
     } else {
-      float m[15];
-#pragma unroll
-      for (int i = 0; i + 1 < (1 << BITS); ++i) m[i] = mids[i];
-      tmem_ld16(from + 16, y);
-      search16<BITS, 31, 16>(y, ri.inv, m, w, mask);
       tmem_ld16(from, y);
-      search16<BITS, 15, 16>(y, ri.inv, m, w, mask);
-#pragma unroll
-      for (int i = 0; i < BITS; ++i) w[i] = ~w[i];
+      count16<BITS, 0>(y, ri.inv, mids, w, mask);
+      tmem_ld16(from + 16, y);
+      count16<BITS, 16>(y, ri.inv, mids, w, mask);
     }
   }
   if (ri.kind != 1) {
@@ -450,7 +418,7 @@ constexpr int kThreads = 512;
 
 template <typename T>
 constexpr int append_smem(int N) {
-  return 2 * kRows * 256 * (sizeof(T) == 4 ? 2 : 1) + N * 256 * 2 + 3 * kRows * static_cast<int>(sizeof(RowInfo)) +
+  return kRows * 256 * (sizeof(T) == 4 ? 2 : 1) + kRows * kPD * static_cast<int>(sizeof(T)) + N * 256 * 2 + 3 * kRows * static_cast<int>(sizeof(RowInfo)) +
          kCells * kCopies * 8 + 64 + 64;
 }
 
@@ -466,8 +434,9 @@ struct Place {
   }
 };
 
-// One CTA of 16 warps an SM.  Two tiles are under way: while one is searched, the product of
-// the next one runs and the rows of the one behind it are loaded.  One barrier a tile.
+// One CTA of 16 warps an SM.  While a tile is searched, the product of the next one runs and the
+// rows of the one behind it are on their way to shared memory (each thread's own places:
+// registers would not hold them through the search).  One barrier a tile.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
 append_kernel(const __grid_constant__ AppendArgs a) {
@@ -476,9 +445,10 @@ append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int kA = kRows * 256 * (XLO ? 2 : 1);          // operand of a tile: hi, then lo
   extern __shared__ __align__(128) char smem[];
   const int N = a.N;
-  char* sA = smem;                                         // of two tiles
-  char* sB = sA + 2 * kA;                                  // hi, then lo of the rotation
-  RowInfo* infos = reinterpret_cast<RowInfo*>(sB + N * 512);   // of three tiles: a warp may still search the one before
+  char* sA = smem;
+  char* sB = sA + kA;                                      // hi, then lo of the rotation
+  char* sRaw = sB + N * 512;                               // rows as they come
+  RowInfo* infos = reinterpret_cast<RowInfo*>(sRaw + kRows * kPD * sizeof(T));   // of three tiles: a warp may still search the one before
   Cell* cells = reinterpret_cast<Cell*>(infos + 3 * kRows);
   float* mids = reinterpret_cast<float*>(cells + kCells * kCopies);
   uint64_t* bars = reinterpret_cast<uint64_t*>(mids + 16);
@@ -493,18 +463,26 @@ append_kernel(const __grid_constant__ AppendArgs a) {
   auto part_of = [&](int hkp) { return whole ? 0 : hkp & 3; };
   auto hk_of = [&](int hkp) { return whole ? hkp : hkp >> 2; };
 
-  // Loads of a tile, and where its rows go, both a tile ahead.  Lane 8g + j of warp w holds
+  // Loads of a tile, and where its rows go, both a tile ahead.  Lane 8g + j of warp w takes
   // chunks g, g + 4, g + 8, g + 12 (eight values) of row 8w + j.
-  uint4 raw[4][V];
+  const uint32_t mine = smem_u32(sRaw) + tid * 16;
   int seq = -1, slt = -1, pos = 0, page = -1;
   auto request = [&](const Place& p) {
     const int hk = hk_of(p.hkp), i = p.tile * kRows + 8 * warp + (lane & 7);
     const T* X = static_cast<const T*>(a.X[hk & 1]) + (static_cast<size_t>(i) * a.pg.H + (hk >> 1)) * kPD + 8 * (lane >> 3);
+    const int bytes = i < a.n ? 16 : 0;                    // zeros behind the last row
+    const T* src = i < a.n ? X : static_cast<const T*>(a.X[0]);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) raw[k][v] = i < a.n ? __ldg(reinterpret_cast<const uint4*>(X + 32 * k) + v) : make_uint4(0, 0, 0, 0);
+      for (int v = 0; v < V; ++v)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(mine + (k * V + v) * (kThreads * 16)),
+                     "l"(reinterpret_cast<const uint4*>(src + 32 * k) + v), "r"(bytes)
+                     : "memory");
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto places = [&](const Place& p) {
     const int j = p.tile * kRows + tid;
     seq = -1;
     if (tid < kRows && j < a.n) {
@@ -522,6 +500,7 @@ append_kernel(const __grid_constant__ AppendArgs a) {
   Place ahead = {first, first % a.tiles, first / a.tiles};   // the tile whose loads are under way
   if (first < last) {
     request(ahead);
+    places(ahead);
     find_page();
   }
   if (tid == 0) {
@@ -543,7 +522,7 @@ append_kernel(const __grid_constant__ AppendArgs a) {
   auto load_rotation = [&](int hkp) {
     const int hk = hk_of(hkp), kv = hk & 1, h = hk >> 1;
     const float* P = a.Pi[kv] + (static_cast<size_t>(h % a.rot) * kPD + part_of(hkp) * N) * kPD;
-#pragma unroll 2
+#pragma unroll 4
     for (int e = tid; e < N * 16; e += kThreads) {
       const int d = (e >> 5) / 4 * 8 + (e & 7), c = (e >> 5) % 4 * 4 + ((e >> 3) & 3);   // as the rows: 8 rows x 4 chunks a warp
       const float4 u = __ldg(reinterpret_cast<const float4*>(P + d * kPD + 8 * c));
@@ -566,7 +545,7 @@ append_kernel(const __grid_constant__ AppendArgs a) {
   auto start_tile = [&]() {
     const int hk = hk_of(ahead.hkp), kv = hk & 1, h = hk >> 1, buf = (ahead.item - first) & 1;
     RowInfo* info = infos + (ahead.item % 3) * kRows;
-    char* A = sA + buf * kA;
+    char* A = sA;
     if (tid < kRows) {                                     // where each row goes
       long long at = -1;
       if (seq >= 0 && slt >= 0) {
@@ -583,12 +562,18 @@ append_kernel(const __grid_constant__ AppendArgs a) {
       }
       info[tid].at = at;
     }
+    ahead.next(a.tiles);
+    if (ahead.item < last) places(ahead);
     // rows scaled to 2^7
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     uint32_t top = 0;
     float x[4][8];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      widen(raw[k], x[k]);
+      uint4 raw[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) raw[v] = *reinterpret_cast<const uint4*>(sRaw + (k * V + v) * (kThreads * 16) + tid * 16);
+      widen(raw, x[k]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[k][i]) & 0x7fffffffu);
     }
@@ -656,8 +641,10 @@ append_kernel(const __grid_constant__ AppendArgs a) {
       }
       asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bars + buf)) : "memory");
     }
-    ahead.next(a.tiles);
-    if (ahead.item < last) request(ahead);
+    if (ahead.item < last) {
+      request(ahead);
+      find_page();
+    }
   };
 
   bool lost = false;
@@ -671,12 +658,11 @@ append_kernel(const __grid_constant__ AppendArgs a) {
         loaded = now.hkp;
       }
       start_tile();
-      if (ahead.item < last) find_page();
     }
-    if (ahead.item < last && ahead.hkp == loaded) start_tile();
     const int i = now.item - first;
     if (!lost && !wait_parity_bounded(smem_u32(bars + (i & 1)), (i >> 1) & 1, kFaultPaged)) lost = true;
-    if (ahead.item < last) find_page();
+    // the operand is free again
+    if (ahead.item < last && ahead.hkp == loaded) start_tile();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     if (!__any_sync(0xffffffffu, lost)) {                  // else the product never came: nothing is written
       const int hk = hk_of(now.hkp), kv = hk & 1, h = hk >> 1, part = part_of(now.hkp);
