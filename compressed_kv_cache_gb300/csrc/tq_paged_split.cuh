@@ -330,9 +330,14 @@ __device__ __forceinline__ void load_value(uint32_t (&w)[2], uint32_t row, int g
   }
 }
 
-// Products of two keys (rows g and g + 8) with the queries, word I of their codes and on.
+// Products of two keys (rows g and g + 8) with the queries, word I of their codes and on.  With KX
+// the coordinates are summed in four parts: the tensor core's additions cut bits off, and two
+// of them in a row cost half the error of eight (fp32 queries, 8 x 32 heads of up to 2049
+// slots: 9.6e-7 of the output's norm in one part).
+template <bool KX>
+constexpr int parts_of() { return KX ? 4 : 1; }
 template <int KB, bool KX, int NB, int I>
-__device__ __forceinline__ void key_products(float (&c)[4], float (&cl)[4], const uint32_t (&w0)[KB], const uint32_t (&w1)[KB],
+__device__ __forceinline__ void key_products(float (&c)[parts_of<KX>()][4], float (&cl)[4], const uint32_t (&w0)[KB], const uint32_t (&w1)[KB],
                                              uint32_t low, uint32_t high, const SplitArgs& p, const uint32_t (&q)[16],
                                              const uint32_t (&ql)[NB]) {
   using Pr = Pairs<KB, KX>;
@@ -343,8 +348,9 @@ __device__ __forceinline__ void key_products(float (&c)[4], float (&cl)[4], cons
 #pragma unroll
   for (int k = 0; k < n; ++k) {
     const int m = I * n + k;
-    if (m == 0) mma0(c, a.hi[0], b.hi[0], a.hi[1], b.hi[1], q[0], q[1]);
-    else mma(c, a.hi[2 * k], b.hi[2 * k], a.hi[2 * k + 1], b.hi[2 * k + 1], q[2 * m], q[2 * m + 1]);
+    float (&cm)[4] = c[m % parts_of<KX>()];
+    if (m < parts_of<KX>()) mma0(cm, a.hi[2 * k], b.hi[2 * k], a.hi[2 * k + 1], b.hi[2 * k + 1], q[2 * m], q[2 * m + 1]);
+    else mma(cm, a.hi[2 * k], b.hi[2 * k], a.hi[2 * k + 1], b.hi[2 * k + 1], q[2 * m], q[2 * m + 1]);
     if constexpr (KX) {
       if (m == 0) mma0(cl, a.lo[0], b.lo[0], a.lo[1], b.lo[1], q[0], q[1]);
       else mma(cl, a.lo[2 * k], b.lo[2 * k], a.lo[2 * k + 1], b.lo[2 * k + 1], q[2 * m], q[2 * m + 1]);
@@ -604,11 +610,12 @@ paged_split_kernel(const __grid_constant__ SplitArgs p) {
         uint32_t w0[KB], w1[KB];
         load_words(w0, st + (16 * mt + r0) * (16 * KB) + t * 4 * KB);
         load_words(w1, st + (16 * mt + 8 + r0) * (16 * KB) + t * 4 * KB);
-        float cl[4];
-        key_products<KB, KX, NL, 0>(z[mt], cl, w0, w1, klow, khigh, p, q, ql);
-        if constexpr (KX) {
+        float c[parts_of<KX>()][4], cl[4];
+        key_products<KB, KX, NL, 0>(c, cl, w0, w1, klow, khigh, p, q, ql);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) z[mt][i] += cl[i];
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (KX) z[mt][i] = ((c[0][i] + c[1][i]) + (c[2][i] + c[3][i])) + cl[i];
+          else z[mt][i] = c[0][i];
         }
         if constexpr (COL) {
 #pragma unroll
