@@ -414,7 +414,8 @@ __device__ __forceinline__ void search_tile(const AppendArgs& a, int kv, int h, 
   if (part == 0 && warp < 4 && ri.kind != 0) (kv ? a.pg.vn : a.pg.kn)[ri.at] = static_cast<uint16_t>(ri.norm);
 }
 
-constexpr int kThreads = 512;
+constexpr int kWorkers = 512;          // 16 warps that make operands and search, and one more:
+constexpr int kThreads = 544;          // it issues the products
 
 template <typename T>
 constexpr int append_smem(int N) {
@@ -434,9 +435,11 @@ struct Place {
   }
 };
 
-// One CTA of 16 warps an SM.  While a tile is searched, the product of the next one runs and the
-// rows of the one behind it are on their way to shared memory (each thread's own places:
-// registers would not hold them through the search).  One barrier a tile.
+// One CTA of 16 + 1 warps an SM.  While a tile is searched, the product of the next one runs and
+// the rows of the one behind it are on their way to shared memory (each thread's own places:
+// registers would not hold them through the search; one bulk copy a row measured slower).  The
+// warps meet only where the last warp waits for an operand to be whole, so one that has
+// near coordinates to settle holds the others up a tile later, if at all.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
 append_kernel(const __grid_constant__ AppendArgs a) {
@@ -452,7 +455,7 @@ append_kernel(const __grid_constant__ AppendArgs a) {
   Cell* cells = reinterpret_cast<Cell*>(infos + 3 * kRows);
   float* mids = reinterpret_cast<float*>(cells + kCells * kCopies);
   uint64_t* bars = reinterpret_cast<uint64_t*>(mids + 16);
-  uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 2);
+  uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 3);
   Grid* grid = reinterpret_cast<Grid*>(slot + 1);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
@@ -463,25 +466,28 @@ append_kernel(const __grid_constant__ AppendArgs a) {
   auto part_of = [&](int hkp) { return whole ? 0 : hkp & 3; };
   auto hk_of = [&](int hkp) { return whole ? hkp : hkp >> 2; };
 
-  // Loads of a tile, and where its rows go, both a tile ahead.  Lane 8g + j of warp w takes
-  // chunks g, g + 4, g + 8, g + 12 (eight values) of row 8w + j.
-  const uint32_t mine = smem_u32(sRaw) + tid * 16;
+  const uint32_t done = smem_u32(bars), whole_op = smem_u32(bars + 2);
+  const bool worker = warp < kWorkers / 32;
   int seq = -1, slt = -1, pos = 0, page = -1;
+  // A worker's share of a tile's rows, to places of its own.  Lane 8g + j of warp w takes chunks
+  // g, g + 4, g + 8, g + 12 (eight values) of row 8w + j.
+  const uint32_t mine = smem_u32(sRaw) + tid * 16;
   auto request = [&](const Place& p) {
     const int hk = hk_of(p.hkp), i = p.tile * kRows + 8 * warp + (lane & 7);
-    const T* X = static_cast<const T*>(a.X[hk & 1]) + (static_cast<size_t>(i) * a.pg.H + (hk >> 1)) * kPD + 8 * (lane >> 3);
     const int bytes = i < a.n ? 16 : 0;                    // zeros behind the last row
-    const T* src = i < a.n ? X : static_cast<const T*>(a.X[0]);
+    const T* src = static_cast<const T*>(a.X[hk & 1]);
+    if (i < a.n) src += (static_cast<size_t>(i) * a.pg.H + (hk >> 1)) * kPD + 8 * (lane >> 3);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(mine + (k * V + v) * (kThreads * 16)),
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(mine + (k * V + v) * (kWorkers * 16)),
                      "l"(reinterpret_cast<const uint4*>(src + 32 * k) + v), "r"(bytes)
                      : "memory");
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  // Where a tile's rows go, asked for a tile ahead.
   auto places = [&](const Place& p) {
     const int j = p.tile * kRows + tid;
     seq = -1;
@@ -498,15 +504,17 @@ append_kernel(const __grid_constant__ AppendArgs a) {
   };
 
   Place ahead = {first, first % a.tiles, first / a.tiles};   // the tile whose loads are under way
-  if (first < last) {
+  if (tid == 0) {
+    const int counts[3] = {1, 1, kWorkers / 32};
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bars + i)), "r"(counts[i]) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (first < last && worker) {
     request(ahead);
     places(ahead);
     find_page();
-  }
-  if (tid == 0) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(bars + i)) : "memory");
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(2 * N) : "memory");
@@ -517,13 +525,22 @@ append_kernel(const __grid_constant__ AppendArgs a) {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *slot;
 
+  bool lost = false;                                       // a wait ran out: the rest is not written
+  auto wait = [&](uint32_t bar, int n) {                   // for the bar's n-th use, from 0
+    if (!lost && !wait_parity_bounded(bar, n & 1, kFaultPaged)) lost = true;
+  };
+
   // Rows part * N .. of a head's rotation, times 2^7, and its codebook's midpoints.  Every warp is
   // past the products and the search of the tiles before.
   auto load_rotation = [&](int hkp) {
+    if (!worker) {
+      __syncthreads();
+      return;
+    }
     const int hk = hk_of(hkp), kv = hk & 1, h = hk >> 1;
     const float* P = a.Pi[kv] + (static_cast<size_t>(h % a.rot) * kPD + part_of(hkp) * N) * kPD;
 #pragma unroll 4
-    for (int e = tid; e < N * 16; e += kThreads) {
+    for (int e = tid; e < N * 16; e += kWorkers) {
       const int d = (e >> 5) / 4 * 8 + (e & 7), c = (e >> 5) % 4 * 4 + ((e >> 3) & 3);   // as the rows: 8 rows x 4 chunks a warp
       const float4 u = __ldg(reinterpret_cast<const float4*>(P + d * kPD + 8 * c));
       const float4 v = __ldg(reinterpret_cast<const float4*>(P + d * kPD + 8 * c + 4));
@@ -538,12 +555,34 @@ append_kernel(const __grid_constant__ AppendArgs a) {
     const Grid g = make_grid(mids, n, lane);
     if (tid == 0) *grid = g;
     if (g.ok) cells[tid] = make_cell(mids, n, g, tid / kCopies);
-    static_assert(kCells * kCopies == kThreads, "an entry a thread");
+    static_assert(kCells * kCopies == kWorkers, "an entry a thread");
   };
 
-  // The loaded tile to fp16 rows, its product on the way, and the next one's loads.
-  auto start_tile = [&]() {
-    const int hk = hk_of(ahead.hkp), kv = hk & 1, h = hk >> 1, buf = (ahead.item - first) & 1;
+  // The last warp: a tile's product, once its operand is whole.
+  auto issue_tile = [&]() {
+    const int i = ahead.item - first;
+    wait(whole_op, i);
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    if (lane == 0) {
+      const uint32_t Aa = smem_u32(sA), Bm = smem_u32(sB), d = tmem + (i & 1) * N;
+      const uint32_t la = kRows * 16, lb = N * 16;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mma_f16(d, operand(Aa + k * 2 * la, la), operand(Bm + k * 2 * lb, lb), N, k != 0);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mma_f16(d, operand(Aa + k * 2 * la, la), operand(Bm + N * 256 + k * 2 * lb, lb), N, true);
+      if constexpr (XLO) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mma_f16(d, operand(Aa + kRows * 256 + k * 2 * la, la), operand(Bm + k * 2 * lb, lb), N, true);
+      }
+      asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(done + 8 * (i & 1)) : "memory");
+    }
+    __syncwarp();
+    ahead.next(a.tiles);
+  };
+
+  // A worker's rows of the tile that has come, as fp16, where they go, and the next tile's loads.
+  auto make_operand = [&]() {
+    const int hk = hk_of(ahead.hkp), kv = hk & 1, h = hk >> 1;
     RowInfo* info = infos + (ahead.item % 3) * kRows;
     char* A = sA;
     if (tid < kRows) {                                     // where each row goes
@@ -565,6 +604,7 @@ append_kernel(const __grid_constant__ AppendArgs a) {
     ahead.next(a.tiles);
     if (ahead.item < last) places(ahead);
     // rows scaled to 2^7
+    const int r = 8 * warp + (lane & 7);
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     uint32_t top = 0;
     float x[4][8];
@@ -572,7 +612,7 @@ append_kernel(const __grid_constant__ AppendArgs a) {
     for (int k = 0; k < 4; ++k) {
       uint4 raw[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) raw[v] = *reinterpret_cast<const uint4*>(sRaw + (k * V + v) * (kThreads * 16) + tid * 16);
+      for (int v = 0; v < V; ++v) raw[v] = *reinterpret_cast<const uint4*>(sRaw + (k * V + v) * (kWorkers * 16) + tid * 16);
       widen(raw, x[k]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[k][i]) & 0x7fffffffu);
@@ -593,7 +633,6 @@ append_kernel(const __grid_constant__ AppendArgs a) {
         for (int i = 0; i < 8; ++i) x[k][i] *= s0;
     }
     float sum = 0.f;
-    const int r = 8 * warp + (lane & 7);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
 #pragma unroll
@@ -625,44 +664,36 @@ append_kernel(const __grid_constant__ AppendArgs a) {
       ri.code = zero;
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-    __syncthreads();
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    if (tid == 0) {
-      const uint32_t Aa = smem_u32(A), Bm = smem_u32(sB), d = tmem + buf * N;
-      const uint32_t la = kRows * 16, lb = N * 16;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) mma_f16(d, operand(Aa + k * 2 * la, la), operand(Bm + k * 2 * lb, lb), N, k != 0);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) mma_f16(d, operand(Aa + k * 2 * la, la), operand(Bm + N * 256 + k * 2 * lb, lb), N, true);
-      if constexpr (XLO) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) mma_f16(d, operand(Aa + kRows * 256 + k * 2 * la, la), operand(Bm + k * 2 * lb, lb), N, true);
-      }
-      asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bars + buf)) : "memory");
-    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");   // and this warp's reads of the tile before last
+    __syncwarp();
+    if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(whole_op) : "memory");
     if (ahead.item < last) {
       request(ahead);
       find_page();
     }
   };
 
-  bool lost = false;
   Place now = ahead;
   int loaded = -1;
   while (now.item < last) {
-    if (ahead.item == now.item) {                          // a rotation begins: nothing is under way
+    if (ahead.item == now.item) {                          // nothing is under way
       if (loaded != now.hkp) {
         __syncthreads();
         load_rotation(now.hkp);
         loaded = now.hkp;
       }
-      start_tile();
+      if (worker) make_operand();
+      else issue_tile();
     }
     const int i = now.item - first;
-    if (!lost && !wait_parity_bounded(smem_u32(bars + (i & 1)), (i >> 1) & 1, kFaultPaged)) lost = true;
+    if (!worker) {
+      if (ahead.item < last && ahead.hkp == loaded) issue_tile();
+      now.next(a.tiles);
+      continue;
+    }
+    wait(done + 8 * (i & 1), i >> 1);
     // the operand is free again
-    if (ahead.item < last && ahead.hkp == loaded) start_tile();
+    if (ahead.item < last && ahead.hkp == loaded) make_operand();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     if (!__any_sync(0xffffffffu, lost)) {                  // else the product never came: nothing is written
       const int hk = hk_of(now.hkp), kv = hk & 1, h = hk >> 1, part = part_of(now.hkp);
