@@ -4,16 +4,20 @@
 // select: a cluster of up to 8 CTAs per (sequence, head).  Each CTA keeps the keys (the order of
 // preference as unsigned numbers) of its share of the slots in shared memory; the keep-th
 // largest key is found by its digits from the top (11, 11 and 10 bits), the counts of a
-// digit added up over the cluster through distributed shared memory.  The slots given up below
-// `keep` and the kept ones behind it are then numbered in slot order and listed, and the
-// weights of the slots that stay are copied.  mass and positions are read once in order, and once
-// more, for the kept slots, from L2.
+// digit added up over the cluster through distributed shared memory; the keys that share the
+// first digit are listed, so that the third pass reads few.  One pass in slot order then lists
+// the slots given up below `keep` and the kept ones behind it (ballots; equal keys are counted
+// only where the last one kept has equals that are not), and copies the weights that stay.
 //
 // move: the i-th listed row behind `keep` goes to the i-th listed slot below it.  Sources and
-// targets are disjoint, so the rows move in any order; a thread moves 16 bytes.
+// targets are disjoint, so the rows move in any order; eight threads take a row.
 //
-// Bound by memory latency for the bounded cache's steady state, by the moved rows (read and
-// written once) after a long prompt.
+// Bound: select by dependent latencies (16 x 8 rows of 4224 slots: 13 us of some 40 loads,
+// barriers and scans in a row, 17 us a call); move by DRAM's sectors: a row's 48 + 48 + 2 + 2 + 4 + 4
+// bytes lie in scattered 32-byte sectors.  4 x 8 rows of 131072 slots to 32768: select 45 us, move
+// 60 us for 314 MB of DRAM traffic (5.2 TB/s) where the rows' own bytes are 157 MB; 105 us a call.
+// Measured on the way there: one CTA a row 1853 us; 1024 threads a CTA (one an SM, two waves)
+// 139 us, 512 threads 111 us; weights loaded eight deep 105 us.
 #include <cooperative_groups.h>
 
 #include "tq_paged.cuh"

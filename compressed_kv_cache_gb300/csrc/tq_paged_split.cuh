@@ -11,9 +11,19 @@
 // operand and up to 8 queries as its 8 columns, so grouped heads cost what one head costs.
 // The 16-row operand is made in registers: neighbouring codes select fp16 pairs of centroids
 // from tables in shared memory, where every lane that a load serves has a copy in its own banks,
-// so that a look-up never conflicts.  tcgen05 would need that operand
-// written to shared memory and read back (512 bytes a slot instead of none); at 4 to 8 queries
-// the tensor work is a small part either way.
+// so that a look-up never conflicts.  tcgen05 would need that operand written to shared memory
+// and read back (512 bytes a slot instead of none), where the kernel is already bound; at up
+// to 8 queries the tensor pipe is busy for 23 % of the time as it is.
+//
+// Bound: shared memory.  The look-ups read 512 bytes a slot whatever the codes' width, 4
+// wavefronts; codes, lengths and the copies into the ring add 2.8.  131072 slots x 8 heads, 3-bit
+// codes: 245 cycles a tile of 32 slots in the loop, 217 of them wavefronts; the ALU pipe is
+// 46 % and issue 58 % busy.  36 us (2.9 TB/s of codes) of a call of 42; 32 x 32768 x 8 heads, 4-bit
+// keys: a call of 274 us, 3.6 TB/s.  hi + lo look-ups (KX) are 8 bytes each: 335 cycles a tile.
+// Measured on the way there (131072 slots x 8 heads, whole call): two-code tables in 64 entries
+// with shifts and masks on the ALU pipe 63 us; shifts to the left on the FMA pipe and
+// aligned tables 49 us; 256 entries picked by a byte permute 46 us; 8, 12 or 16 warps within
+// 5 % of each other; without the products 1 us less, without the look-ups 4 us less.
 //
 // The order of the sum over coordinates and over slots is free, and is chosen for the loads:
 // lane (g, t) of a warp (g = lane / 4, t = lane % 4) takes coordinates 32t .. 32t+31 of two
