@@ -31,7 +31,7 @@ constexpr int kCluster = 8;             // CTAs of a cluster, at most
 constexpr int kSel = 512;               // threads of a CTA of select (two or more CTAs an SM)
 constexpr int kDigit = 2048;            // counts of the widest digit
 constexpr int kCached = 48 * 1024;      // keys a CTA can keep in shared memory
-constexpr int kListed = 3072;           // of them that share the first digit, listed for the last pass
+constexpr int kListed = 4096;           // of them that share the first digit, listed for the last pass
 constexpr int kMoves = 256;             // rows a CTA of move takes
 
 // Order of preference as an unsigned number: protected slots above every weight, then the

@@ -477,7 +477,7 @@ def test_evict(tq, S, budget, recent):
 def test_evict_long(tq):
     """Longer than one CTA, and than a cluster, keeps in shared memory."""
     rng = np.random.default_rng(7)
-    for S, budget in ((70001, 20000), (262147, 1000), (700003, 350000)):
+    for S, budget in ((70001, 20000), (262147, 1000), (393216, 100), (700003, 350000)):
         p = Pages(tq, 1, 1, S, 256, 2, 2, seed=9)
         mass = np.exp(rng.standard_normal((1, 1, S))).astype(np.float32)
         pos = rng.permutation(S).astype(np.int32).reshape(1, 1, S)
