@@ -12,12 +12,12 @@
 // move: the i-th listed row behind `keep` goes to the i-th listed slot below it.  Sources and
 // targets are disjoint, so the rows move in any order; eight threads take a row.
 //
-// Bound: select by dependent latencies (16 x 8 rows of 4224 slots: 13 us of some 40 loads,
-// barriers and scans in a row, 17 us a call); move by DRAM's sectors: a row's 48 + 48 + 2 + 2 + 4 + 4
+// Bound: select by dependent latencies (16 x 8 rows of 4224 slots: some 40 loads, barriers and
+// scans in a row, 15 us a call with the moves); move by DRAM's sectors: a row's 48 + 48 + 2 + 2 + 4 + 4
 // bytes lie in scattered 32-byte sectors.  4 x 8 rows of 131072 slots to 32768: select 45 us, move
-// 60 us for 314 MB of DRAM traffic (5.2 TB/s) where the rows' own bytes are 157 MB; 105 us a call.
+// 60 us for 314 MB of DRAM traffic (5.2 TB/s) where the rows' own bytes are 157 MB; 103 us a call.
 // Measured on the way there: one CTA a row 1853 us; 1024 threads a CTA (one an SM, two waves)
-// 139 us, 512 threads 111 us; weights loaded eight deep 105 us.
+// 139 us, 512 threads 111 us; weights loaded eight deep 105 us; 128 rows a CTA of move 103 us.
 #include <cooperative_groups.h>
 
 #include "tq_paged.cuh"
@@ -32,7 +32,7 @@ constexpr int kSel = 512;               // threads of a CTA of select (two or mo
 constexpr int kDigit = 2048;            // counts of the widest digit
 constexpr int kCached = 48 * 1024;      // keys a CTA can keep in shared memory
 constexpr int kListed = 4096;           // of them that share the first digit, listed for the last pass
-constexpr int kMoves = 256;             // rows a CTA of move takes
+constexpr int kMoves = 128;             // rows a CTA of move takes (256: 105 us instead of 103 for 4 x 131072)
 
 // Order of preference as an unsigned number: protected slots above every weight, then the
 // weight (its bits made monotone; -0 as 0, NaN as -inf).
@@ -289,7 +289,7 @@ evict_select_kernel(const SelectArgs a) {
 }
 
 // Eight threads of move take a row's 16-byte pieces (up to four of the key, up to four of the
-// value), eight rows each with all their loads in flight; a thread a row its two lengths, its
+// value), four rows each with all their loads in flight; a thread a row its two lengths, its
 // weight and its position.
 __global__ void __launch_bounds__(256)
 evict_move_kernel(Paged pg, const float* __restrict__ mass, const int* __restrict__ positions, int S,
@@ -342,11 +342,12 @@ evict_move_kernel(Paged pg, const float* __restrict__ mass, const int* __restric
 // Rows one (sequence, head) can move.
 int most_moves(int S, int budget) { return budget >= S ? 0 : (budget < S - budget ? budget : S - budget); }
 
-// CTAs of a cluster: enough to fill the device from few rows, at least 2048 slots each, and as
-// many as it takes to keep the keys in shared memory (where 8 do).
+// CTAs of a cluster: enough to fill the device from few rows, at least 4096 slots each (16 x 8
+// rows of 4224 slots: 14.8 us a call with one CTA a row, 17.4 with two, 31 with four), and
+// as many as it takes to keep the keys in shared memory (where 8 do).
 int cluster_size(int S, int64_t units, int sms) {
   int C = 1;
-  while (C < kCluster && ((units * C * 2 <= 2 * sms && S / (2 * C) >= 2048) || S > C * kCached)) C *= 2;
+  while (C < kCluster && ((units * C * 2 <= 2 * sms && S / (2 * C) >= 4096) || S > C * kCached)) C *= 2;
   return C;
 }
 bool keys_fit(int S) { return S <= kCluster * kCached; }
