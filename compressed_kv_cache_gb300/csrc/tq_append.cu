@@ -33,7 +33,7 @@ namespace {
 
 constexpr int kRows = 128;             // rows of a tile
 constexpr int kCells = 128;            // cells of the search table
-constexpr int kCopies = 4;             // of each, for every fourth lane
+constexpr int kCopies = 16;            // of each, one for every lane that a load serves at a time
 constexpr float kNear = 1.f / 131072.f;
 
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
@@ -565,8 +565,12 @@ append_kernel(const __grid_constant__ AppendArgs a) {
     __syncthreads();
     const Grid g = make_grid(mids, n, lane);
     if (tid == 0) *grid = g;
-    if (g.ok) cells[tid] = make_cell(mids, n, g, tid / kCopies);
-    static_assert(kCells * kCopies == kWorkers, "an entry a thread");
+    constexpr int kShare = kCells * kCopies / kWorkers;    // copies of one cell a thread writes
+    if (g.ok) {
+      const Cell c = make_cell(mids, n, g, tid * kShare / kCopies);
+#pragma unroll
+      for (int k = 0; k < kShare; ++k) cells[tid * kShare + k] = c;
+    }
   };
 
   // The last warp: a tile's product, once its operand is whole.
