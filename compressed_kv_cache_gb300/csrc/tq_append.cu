@@ -8,24 +8,25 @@
 // searches and packs its coordinates in registers.
 //
 // The codes are those of a 64-bit product: a coordinate within kNear of a midpoint (in units of
-// the row's length) is summed again in 64 bits from the inputs.  kNear = 2^-17 covers the
-// operands' 2^-21 and the up to 24 fp32 sums of 16 products, each of which is at most the
+// the row's length) is summed again in 64 bits from the inputs.  kNear = 5e-6 covers, in that
+// unit: the operands' 2^-21; the up to 24 fp32 sums of 16 products, each of which is at most the
 // row's length and is off by at most 2^-23 of it even where bits are cut off instead of rounded
-// (2^-18.4 together); it meets about 1 coordinate in 2600 (3 bits).
+// (2.9e-6 together); the fp32 length's 34 additions (half of 34 x 2^-24, a coordinate being at most
+// 1) and the scaling by it (1.2e-6): 4.5e-6.  It meets about 1 coordinate in 4000 (3 bits).
 //
 // N is 128 (the rotation of a head stays in shared memory from tile to tile) or, where that
 // leaves SMs without a tile, 32: a decode step of 64 tokens then runs on four times the SMs.
 //
-// Bound: latency and issue, not yet memory.  8192 tokens x 8 heads, bf16, 3-bit codes: 47 us, of
-// which 5 are set-up (tensor memory, the rotation's fp16 form) and about 5.5 a tile (7 tiles an
-// SM): rows to fp16 0.8, the search of the cells 2 to 3, waits on the slowest warp and on the
-// product the rest; 0.9 TB/s of the rows' and codes' bytes.  15003 fp32 rows x 8 heads: 97 us,
-// 1.45 TB/s.  Measured on the way there (8192 tokens): everything in 64 bits 13.5 ms; near
+// Bound: latency and issue, not yet memory.  8192 tokens x 8 heads, bf16, 3-bit codes: 44 us, of
+// which 5 are set-up (tensor memory, the rotation's fp16 form) and about 5 a tile (7 tiles an SM):
+// rows to fp16 0.8, the search of the cells 2 to 3, waits on the slowest warp and on the product
+// the rest; 0.94 TB/s of the rows' and codes' bytes.  15003 fp32 rows x 8 heads, 4-bit codes: 91
+// us, 1.55 TB/s.  Measured on the way there (8192 tokens): everything in 64 bits 13.5 ms; near
 // coordinates listed and summed again in 64 bits 75 us (a 64-bit instruction takes a warp 16
 // cycles); in pairs of fp32 50 us; binary search of the midpoints instead of the cells 52 us;
 // rows prefetched in registers 53 us (they spill); two CTAs of 8 warps an SM 52 us; a barrier
-// a tile instead of the product's own warp 49 us.  Without the second sums it would take 38 us,
-// without any search 31.
+// a tile instead of the product's own warp 49 us; four copies of a cell instead of sixteen 47 us,
+// of which the second sums took 9 and the search 7.
 #include "tq_paged.cuh"
 
 namespace tq {
@@ -34,7 +35,7 @@ namespace {
 constexpr int kRows = 128;             // rows of a tile
 constexpr int kCells = 128;            // cells of the search table
 constexpr int kCopies = 16;            // of each, one for every lane that a load serves at a time
-constexpr float kNear = 1.f / 131072.f;
+constexpr float kNear = 5e-6f;
 
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
