@@ -557,7 +557,10 @@ paged_split_kernel(const __grid_constant__ SplitArgs p) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) qraw[i] = src[i];
     }
-    __syncwarp();                                          // the ring is free
+    // The ring is free once its readers are done and the unit before has no copies left under way:
+    // those behind its last tile read nothing, but write zeros.
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();
 #pragma unroll
     for (int i = 0; i < L::stages - 1; ++i) issue(tile0 + i, ring + i * L::stage);
     uint32_t q[16], ql[NL];
