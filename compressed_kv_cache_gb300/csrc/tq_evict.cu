@@ -5,7 +5,8 @@
 // preference as unsigned numbers) of its share of the slots in shared memory; the keep-th
 // largest key is found by its digits from the top (11, 11 and 10 bits), the counts of a
 // digit added up over the cluster through distributed shared memory; the keys that share the
-// first digit are listed, so that the third pass reads few.  One pass in slot order then lists
+// first digit are listed, so that the third pass reads few.  Where more slots are protected than
+// are kept, the first digit is counted once more, by weight.  One pass in slot order then lists
 // the slots given up below `keep` and the kept ones behind it (ballots; equal keys are counted
 // only where the last one kept has equals that are not), and copies the weights that stay.
 //
@@ -34,10 +35,12 @@ constexpr int kCached = 48 * 1024;      // keys a CTA can keep in shared memory
 constexpr int kListed = 4096;           // of them that share the first digit, listed for the last pass
 constexpr int kMoves = 128;             // rows a CTA of move takes (256: 105 us instead of 103 for 4 x 131072)
 
-// Order of preference as an unsigned number: protected slots above every weight, then the
-// weight (its bits made monotone; -0 as 0, NaN as -inf).
-__device__ __forceinline__ uint32_t rank_key(float m, int pos, long long oldest) {
-  if (pos >= oldest) return 0xffffffffu;
+// Order of preference as an unsigned number: the weight (its bits made monotone; -0 as 0, NaN
+// as -inf), and protected slots above every weight.  `window`: where there are more of those than
+// are kept, they go by weight and the others are below all.
+__device__ __forceinline__ uint32_t rank_key(float m, int pos, long long oldest, bool window) {
+  const bool safe = pos >= oldest;
+  if (safe != window) return window ? 0u : 0xffffffffu;
   if (m != m) m = -INFINITY;
   const uint32_t u = __float_as_uint(m + 0.f);
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
@@ -88,7 +91,7 @@ struct SelectArgs {
 };
 
 template <bool CACHED>
-__global__ void __launch_bounds__(kSel)
+__global__ void __launch_bounds__(kSel, 2)
 evict_select_kernel(const SelectArgs a) {
   extern __shared__ uint32_t cache[];
   __shared__ __align__(16) int hist[2][kDigit];
@@ -126,52 +129,11 @@ evict_select_kernel(const SelectArgs a) {
   for (int i = t; i < kDigit; i += kSel) hist[0][i] = 0;
   if (t == 0) listed = 0;
   __syncthreads();
-  constexpr int U = 8;                                     // loads of each array in flight, a thread
-  for (int s0 = t; s0 < mine; s0 += U * kSel) {
-    float x[U];
-    int y[U];
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int s = min(s0 + i * kSel, mine - 1);
-      x[i] = m[s];
-      y[i] = ps[s];
-    }
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int s = s0 + i * kSel;
-      if (s < mine) {
-        const uint32_t k = rank_key(x[i], y[i], oldest);
-        key[s] = k;
-        atomicAdd(&hist[0][k >> 21], 1);
-      }
-    }
-  }
-
   // the keep-th largest key; what shares its first digit is listed for the last pass
   uint32_t prefix = 0;
   int want = keep, equal = 0;
-#pragma unroll
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
-    int* hs = hist[pass & 1];
-    if (pass == 1) {
-#pragma unroll 8
-      for (int s = t; s < mine; s += kSel) {
-        const uint32_t k = key[s];
-        if ((k >> 21) == (prefix >> 21)) {
-          atomicAdd(&hs[(k >> 10) & 2047u], 1);
-          const int i = atomicAdd(&listed, 1);
-          if (i < kListed) list[i] = k;
-        }
-      }
-    } else if (pass == 2) {
-      const bool all = listed > kListed;                   // more than the list holds: through all of them
-      const uint32_t* from = all ? key : list;
-      for (int s = t, e = all ? mine : listed; s < e; s += kSel)
-        if ((from[s] >> 10) == (prefix >> 10)) atomicAdd(&hs[from[s] & 1023u], 1);
-    }
-    cl.sync();
-    for (int i = t; i < kDigit; i += kSel) hist[(pass + 1) & 1][i] = 0;   // its readers are done: they have come to this sync
+  // pick: the digit that the want-th largest has, which it is among those, and their number
+  auto pick_digit = [&](int* hs, int width) {
     // four digits a thread, the largest first
     const int hi = (1 << width) - 1 - 4 * t;
     int4 v = make_int4(0, 0, 0, 0);
@@ -197,6 +159,66 @@ evict_select_kernel(const SelectArgs a) {
       above += at[i];
     }
     __syncthreads();
+  };
+  // The top digit of all is that of protected slots alone (infinity's is 2044).  Where there are
+  // more of them than are kept, the keys are made again, by weight among them.  (Two inlined
+  // copies of this took 96 registers, one CTA an SM: 137 us instead of 104 for 4 x 131072.)
+#pragma unroll 1
+  for (bool window = false;; window = true) {
+    constexpr int U = 8;                                   // loads of each array in flight, a thread
+    for (int s0 = t; s0 < mine; s0 += U * kSel) {
+      float x[U];
+      int y[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int s = min(s0 + i * kSel, mine - 1);
+        x[i] = m[s];
+        y[i] = ps[s];
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int s = s0 + i * kSel;
+        if (s < mine) {
+          const uint32_t k = rank_key(x[i], y[i], oldest, window);
+          key[s] = k;
+          atomicAdd(&hist[0][k >> 21], 1);
+        }
+      }
+    }
+    cl.sync();
+    for (int i = t; i < kDigit; i += kSel) hist[1][i] = 0;
+    pick_digit(hist[0], 11);
+    if (window || pick[0] != kDigit - 1 || pick[2] <= pick[1]) break;
+    cl.sync();                                             // every CTA has read the counts
+    for (int i = t; i < kDigit; i += kSel) hist[0][i] = 0;
+    __syncthreads();
+  }
+  prefix = static_cast<uint32_t>(pick[0]) << 21;
+  want = pick[1];
+  __syncthreads();
+#pragma unroll
+  for (int pass = 1; pass < 3; ++pass) {
+    const int shift = pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
+    int* hs = hist[pass & 1];
+    if (pass == 1) {
+#pragma unroll 8
+      for (int s = t; s < mine; s += kSel) {
+        const uint32_t k = key[s];
+        if ((k >> 21) == (prefix >> 21)) {
+          atomicAdd(&hs[(k >> 10) & 2047u], 1);
+          const int i = atomicAdd(&listed, 1);
+          if (i < kListed) list[i] = k;
+        }
+      }
+    } else {
+      const bool all = listed > kListed;                   // more than the list holds: through all of them
+      const uint32_t* from = all ? key : list;
+      for (int s = t, e = all ? mine : listed; s < e; s += kSel)
+        if ((from[s] >> 10) == (prefix >> 10)) atomicAdd(&hs[from[s] & 1023u], 1);
+    }
+    cl.sync();
+    for (int i = t; i < kDigit; i += kSel) hist[(pass + 1) & 1][i] = 0;   // its readers are done: they have come to this sync
+    pick_digit(hs, width);
     prefix |= static_cast<uint32_t>(pick[0]) << shift;
     want = pick[1];
     equal = pick[2];

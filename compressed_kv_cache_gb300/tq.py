@@ -656,8 +656,8 @@ def evict_paged_workspace_bytes(B: int, H: int, S: int, budget: int) -> int:
 
 def evict_paged(cache: PagedCache, page_table, lengths, seen, mass, positions, budget, recent, workspace=None,
                 out=None):
-    """Cuts each sequence and KV head to min(length, budget) slots: first those whose position
-    is at least seen - recent, then by mass, ties to the lower slot.  Kept rows behind the
+    """Cuts each sequence and KV head to min(length, budget) slots: those whose position is at
+    least seen - recent before the others, among either by mass, ties to the lower slot.  Kept rows behind the
     budget move to the slots given up.  lengths, seen int32 [B]; mass fp32, positions int32
     [B,H,S].  Returns (mass, positions) of the slots as they are now (`out`, or new tensors of
     0 and -1 behind the kept slots); `lengths` is the caller's to cut once all layers are done."""

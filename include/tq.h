@@ -354,8 +354,8 @@ tq_status tq_decode_paged(const tq_paged_cache* cache, const void* Q, tq_qtype q
 /* ------------------------------------------------------------------------
  * Eviction by accumulated attention weight: every (sequence, KV head) keeps
  * keep = min(lengths[b], budget) of its slots, in this order of preference: slots with
- * positions >= seen[b] - recent; then by mass, larger first (NaN counts as minus infinity);
- * then the lower slot.  Kept rows in slots >= keep move to the slots < keep that are given
+ * positions >= seen[b] - recent before the others, whatever their mass; among either by mass,
+ * larger first (NaN counts as minus infinity); then the lower slot.  recent may exceed budget.  Kept rows in slots >= keep move to the slots < keep that are given
  * up, both in ascending order, so that the kept rows fill slots 0 .. keep-1 (attention does
  * not depend on the order of slots) and nothing else of the cache is written.
  * mass_out, positions_out [B, H, S]: slots < keep get the mass and position of the row that

@@ -95,7 +95,8 @@ def decode_paged(Q, k_plane, k_norm, v_plane, v_norm, page_table, lengths, Pi_k,
 
 def evict_paged(mass, positions, lengths, seen, budget, recent):
     """For each (sequence, head): (kept slots ascending, slots filled, slots they are filled
-    from).  Preference: positions >= seen - recent, then mass (NaN as -inf), then lower slot."""
+    from).  Preference: positions >= seen - recent before the others, among either
+    mass (NaN as -inf), then the lower slot."""
     B, H, S = mass.shape
     got = {}
     for b in range(B):
@@ -105,8 +106,7 @@ def evict_paged(mass, positions, lengths, seen, budget, recent):
             m = mass[b, h, :n].astype(np.float64)
             m = np.where(np.isnan(m), -np.inf, m)
             safe = positions[b, h, :n].astype(np.int64) >= int(seen[b]) - recent
-            # protected slots are equal among themselves: the lower one first
-            order = sorted(range(n), key=lambda s: (not safe[s], 0.0 if safe[s] else -m[s], s))
+            order = sorted(range(n), key=lambda s: (not safe[s], -m[s], s))
             kept = np.array(sorted(order[:keep]), dtype=np.int64)
             got[b, h] = (kept, np.setdiff1d(np.arange(keep), kept), kept[kept >= keep])
     return got
