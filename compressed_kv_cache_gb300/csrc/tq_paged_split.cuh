@@ -33,6 +33,13 @@
 // hi hi + hi lo + lo hi are summed.  COL: four queries, whose hi and lo parts are columns
 // 0..3 and 4..7 of one product.  Centroids, queries, and values' lengths are scaled by
 // powers of two to 2^7 before they become fp16, so that lo stays out of the subnormals.
+//
+// The tensor core's additions cut bits off, so that the errors of a long sum of like terms add up
+// (fp32 queries, flat weights, 1150 tiles a run: 6.8e-5).  A warp therefore takes a unit in
+// pieces of at most kPiece tiles, and adds each piece to its partial with rounded additions; with
+// VX it keeps their rounding errors too.  What is left is the error of one piece, whatever the
+// cache's length.  Additions every 8 tiles within the loop cost the registers they took: 2.5 % of
+// a call.
 #pragma once
 
 #include "tq_paged.cuh"
@@ -43,6 +50,7 @@ constexpr int kSplitWarps = 12;
 constexpr int kTile = 32;            // slots a warp takes at a time
 constexpr int kPartF = 132;          // partial of a query: 128 sums, maximum, sum, 2 unused
 constexpr int kMaxCtas = 192;        // partials are laid out for at most this many CTAs
+constexpr int kPieceX = 32, kPiece = 256;   // tiles of a piece (VX: 128 additions of the tensor core in a row)
 
 // A unit's share of the tiles is cut where the warps' runs are cut: run w covers
 // [w q + min(w, r), ...) of T = q W + r tiles.
@@ -64,7 +72,7 @@ struct SplitArgs {
   const int* lengths;    // [B] as cut by the plan
   const float* kcb;
   const float* vcb;
-  float* part;           // [runs + units][QT][kPartF]
+  float* part;           // [runs + units][QT][kPartF]; VX: and [runs][QT][kPartF] rounding errors
   float* z;              // [units][Sz][QT] logits times log2(e), or null
   int B, G, nqt, Sz;
   float scale2;          // scale * log2(e)
@@ -424,6 +432,34 @@ __device__ __forceinline__ int find_sequence(const int* tiles, int B, int per, i
   return lo;
 }
 
+// a * f + b rounded, and its rounding error.
+__device__ __forceinline__ float add_err(float a, float f, float b, float* err) {
+  const float p = __fmul_rn(a, f), s = p + b, x = s - p;
+  *err = ((p - (s - x)) + (b - x)) + fmaf(a, f, -p);
+  return s;
+}
+// Four sums of a partial: what it has, times f, and v.  X: `rest` has (`more`) and gets their
+// rounding errors, which go to the sums at the end.
+template <bool X>
+__device__ __forceinline__ float4 join_sum(const float4& a, const float4& v, float f, float4* rest, bool more, bool last) {
+  if constexpr (!X) {
+    return make_float4(fmaf(a.x, f, v.x), fmaf(a.y, f, v.y), fmaf(a.z, f, v.z), fmaf(a.w, f, v.w));
+  } else {
+    float4 e, s;
+    s.x = add_err(a.x, f, v.x, &e.x);
+    s.y = add_err(a.y, f, v.y, &e.y);
+    s.z = add_err(a.z, f, v.z, &e.z);
+    s.w = add_err(a.w, f, v.w, &e.w);
+    if (more) {
+      const float4 r = *rest;
+      e = make_float4(fmaf(r.x, f, e.x), fmaf(r.y, f, e.y), fmaf(r.z, f, e.z), fmaf(r.w, f, e.w));
+    }
+    if (last) return make_float4(s.x + e.x, s.y + e.y, s.z + e.z, s.w + e.w);
+    *rest = e;
+    return s;
+  }
+}
+
 template <int KB, int VB, bool KX, bool VX, bool COL>
 __global__ void __launch_bounds__(kSplitWarps * 32, 1)
 paged_split_kernel(const __grid_constant__ SplitArgs p) {
@@ -489,7 +525,9 @@ paged_split_kernel(const __grid_constant__ SplitArgs p) {
     const int in = at - first * per;
     const int u = in / nt;                                 // (head, query tile) of the sequence
     const int tile0 = in - u * nt;
-    const int tile1 = min(nt, tile0 + (end - at));
+    constexpr int piece = VX ? kPieceX : kPiece;
+    const int tile1 = min(min(nt, tile0 + (end - at)), tile0 + piece);
+    const int before = min(tile0, at - run_start(run, rq, rr));   // tiles of the unit that this warp has had
     at += tile1 - tile0;
     const int h = u / p.nqt, j = u - h * p.nqt;
     const int unit = b * per + u;
@@ -750,7 +788,7 @@ paged_split_kernel(const __grid_constant__ SplitArgs p) {
       }
     }
 
-    // this warp's partial of the unit
+    // this warp's partial of the unit, or what is added to it
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
       l0 += __shfl_xor_sync(0xffffffffu, l0, o);
@@ -764,18 +802,39 @@ paged_split_kernel(const __grid_constant__ SplitArgs p) {
     }
     const float fin = vs > 0.f ? vsinv * vinv : 0.f;
     float* part = p.part + static_cast<size_t>(run + unit) * (QT * kPartF);
+    float* rest = p.part + (static_cast<size_t>(W) + p.B * per + run) * (QT * kPartF);
     const int live = min(QT, p.G - j * QT);
-    if (!COL || t < 2) {
+    const bool last = tile1 == nt || at == end;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (c0 + i < live) {
-          float* o = part + (c0 + i) * kPartF;
-          float4* o4 = reinterpret_cast<float4*>(o + 16 * g);
+    for (int i = 0; i < 2; ++i) {
+      const bool writes = (!COL || t < 2) && c0 + i < live;
+      float* o = part + (c0 + i) * kPartF;
+      float4* r4 = reinterpret_cast<float4*>(rest + (c0 + i) * kPartF);
+      float mx = i ? m1 : m0, f = fin, had = 0.f;
+      float4 l = make_float4(i ? l1 : l0, 0.f, 0.f, 0.f);
+      float2 ml = make_float2(0.f, 0.f);
+      if (before > 0) {
+        if (writes) ml = *reinterpret_cast<const float2*>(o + kPD);
+        __syncwarp();                                      // every lane has read it
+        // as in the loop, the maximum moves only by 2^8 and more: what is there is hardly ever rounded again
+        const float top = mx > ml.x + 8.f || ml.x == -INFINITY ? mx : ml.x;
+        had = ml.x > -INFINITY ? ex2(ml.x - top) : 0.f;
+        const float now = mx > -INFINITY ? ex2(mx - top) : 0.f;
+        mx = top;
+        f *= now;
+        l.x *= now;
+      }
+      if (writes) {
+        float4* o4 = reinterpret_cast<float4*>(o + 16 * g);
 #pragma unroll
-          for (int m = 0; m < 4; ++m)
-            o4[m] = make_float4(acc[2 * m][i] * fin, acc[2 * m][2 + i] * fin, acc[2 * m + 1][i] * fin,
-                                acc[2 * m + 1][2 + i] * fin);
-          if (g == 0) *reinterpret_cast<float2*>(o + kPD) = make_float2(i ? m1 : m0, i ? l1 : l0);
+        for (int m = 0; m < 4; ++m) {
+          float4 v = make_float4(acc[2 * m][i] * f, acc[2 * m][2 + i] * f, acc[2 * m + 1][i] * f, acc[2 * m + 1][2 + i] * f);
+          if (before > 0) v = join_sum<VX>(o4[m], v, had, r4 + 4 * g + m, before > piece, last);
+          o4[m] = v;
+        }
+        if (g == 0) {
+          if (before > 0) l = join_sum<VX>(make_float4(ml.y, 0.f, 0.f, 0.f), l, had, r4 + kPD / 4, before > piece, last);
+          *reinterpret_cast<float2*>(o + kPD) = make_float2(mx, l.x);
         }
       }
     }

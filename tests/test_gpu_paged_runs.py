@@ -107,3 +107,87 @@ def test_long_runs_rise(tq, kind, page):
         assert (m[..., n:] == 1).all()
     again = tq.decode_paged(q, p.cache, p.t, p.n, scale=1.0, mass=None if m is None else torch.ones_like(m))
     assert torch.equal(got, again)
+
+
+@pytest.mark.parametrize("kind,S", [(k, 1 << 17) for k in KINDS] + [("f32", 1 << 20), ("bf16", 1 << 20)])   # with mass, 2^20 slots of logits take 8 GB
+@pytest.mark.parametrize("values", ["one", "some"])
+def test_sums_of_long_runs(tq, kind, values, S):
+    """Hundreds and thousands of tiles a warp with equal or nearly equal weights, over values
+    that are all the same row or 256 rows in turn: the errors of a sum's additions all point one
+    way.  Every slot of a sequence lies on one page, so the result is that of 256 slots."""
+    bf16, mass, _ = KINDS[kind]
+    G, B, H, page = 8 if kind == "mass8" else 4, 16 if mass else 64, 8, 256
+    p = Pages(tq, B, H, page, page, 3, 3, rot=1, seed=17)
+    p.kn[:] = 0.0 if values == "one" else 0.01
+    p.vn[:] = 1.0
+    if values == "one":
+        p.vp[:] = p.vp[:, :, :1]
+    p.upload(tq)
+    Q = np.random.default_rng(18).standard_normal((B, H * G, D)).astype(np.float32)
+    q = dev(Q).bfloat16() if bf16 else dev(Q)
+    ke = 2.0 ** -18 if (mass or not bf16) else 2.0 ** -11 + 2.0 ** -18
+    want, w, bound, wrel = p.want(q.float().cpu().numpy(), None, ke, 2.0 ** -11 if bf16 else 2.0 ** -18)
+    t = dev(np.repeat(p.table, S // page, axis=1))
+    n = torch.full((B,), S, dtype=torch.int32, device="cuda")
+    assert B * H * S // TILE > 200 * runs()
+    m = torch.zeros(B, H, S, device="cuda") if mass else None
+    out = tq.decode_paged(q, p.cache, t, n, mass=m)
+    check_out(out, want, bound, bf16)
+    if mass:
+        check_mass(m.view(B, H, S // page, page)[:, :, ::37].reshape(B, H, -1), np.zeros(1),
+                   np.tile(w / (S // page), len(range(0, S // page, 37))), wrel)
+
+
+@pytest.mark.parametrize("kind", ["f32", "f32_mass", "bf16", "mass4", "mass8"])
+def test_long_runs_of_rising_and_falling_pages(tq, kind):
+    """600 tiles a warp and more of 40 pages in changing order: logits that rise and fall by up
+    to 60 over a run, values whose lengths do.  A page that occurs k times counts k times."""
+    bf16, mass, _ = KINDS[kind]
+    G, B, page, U = 8 if kind == "mass8" else 4, 4, 256, 40
+    rng = np.random.default_rng(41)
+    p = Pages(tq, 1, 1, U * page, page, 3, 3, seed=42, spare=0)
+    p.kp[:] = p.kp[0, 0, 0]                                    # one direction: the lengths make the logits
+    level = rng.permutation(U)
+    p.kn[:] = (1.0 + 0.2 * level[:, None, None] + 0.3 * rng.random(p.kn.shape)).astype(np.float16)
+    p.vn[:] = (rng.uniform(0.5, 1, p.vn.shape) * 2.0 ** rng.integers(-3, 4, (U, 1, 1))).astype(np.float16)
+    p.upload(tq)
+    M = -(-600 * TILE * runs() // (B * page)) + 1
+    byl = np.argsort(level)
+    i = np.arange(B * M).reshape(B, M)
+    table = byl[np.where((i // 200) % 2, (i // 5) % U, U - 1 - (i // 7) % U)].astype(np.int32)
+    lengths = M * page - np.array([0, 1, 77, 255])
+    assert sum(-(-lengths // TILE)) >= 600 * runs()
+    count = np.zeros((B, U, page))
+    for b in range(B):
+        np.add.at(count[b], table[b], 1)
+        count[b, table[b, -1], page - (M * page - lengths[b]):] -= 1
+    c = p.kc.astype(np.float64)[oracle.unpack_indices(p.kp[0, 0, 0][None], 3, D)[0]]
+    k = c @ p.Pk[0]
+    Q = np.stack([x * k / (c @ c) for x in (6.0, -6.0, 0.01, 1.0, -1.0, 3.0, -2.0, 5.0)[:G]])[None].repeat(B, 0).astype(np.float32)
+    q = dev(Q).bfloat16() if bf16 else dev(Q)
+    qf = q.float().cpu().numpy().astype(np.float64)
+    m = torch.zeros(B, 1, M * page, device="cuda") if mass else None
+    got = tq.decode_paged(q, p.cache, dev(table), dev(lengths.astype(np.int32)), mass=m, scale=1.0).double().cpu().numpy()
+    ke, ve = 2.0 ** -18 if (mass or not bf16) else 2.0 ** -11 + 2.0 ** -18, 2.0 ** -11 if bf16 else 2.0 ** -18
+    Pv = p.Pv[0].astype(np.float64)
+    cv = p.vc.astype(np.float64)[oracle.unpack_indices(p.vp.reshape(-1, 48), 3, D)]
+    nk, nv = p.kn.reshape(-1).astype(np.float64), p.vn.reshape(-1).astype(np.float64)
+    for b in range(B):
+        a = qf[b] @ p.Pk[0].astype(np.float64).T
+        s = (a @ c)[:, None] * nk
+        e = np.exp(s - s.max(1, keepdims=True))
+        w = e / (e * count[b].reshape(-1)).sum(1, keepdims=True)        # of one slot
+        x = w * count[b].reshape(-1) * nv
+        want = (x @ cv) @ Pv
+        t = (nk.max() * (np.abs(a) @ np.abs(c)))[:, None]
+        grow = np.expm1(2 * t * (2 * ke + ke ** 2))
+        bound = (grow + 2 * ve + ve ** 2) * ((x @ np.abs(cv)) @ np.abs(Pv))
+        tol = bound + 8e-5 + 1e-5 * np.abs(want) + (2.0 ** -8 * np.abs(want) if bf16 else 0)
+        err = np.abs(got[b] - want)
+        assert (err <= tol).all(), np.max(err / tol)
+        if mass:
+            at = np.r_[0:M - 1:97]
+            wrel = np.expm1(2 * t[:, 0] * (2 * 2.0 ** -18 + 2.0 ** -36))
+            ww = w.reshape(G, U, page)[:, table[b, at]].reshape(1, 1, G, -1)
+            check_mass(m[b, 0].view(M, page)[dev(at)].view(1, 1, -1), np.zeros(1), ww, wrel[None, None])
+            assert not m[b, 0, lengths[b]:].any()
