@@ -333,7 +333,9 @@ __device__ __forceinline__ uint32_t near_cell(const float* P, const T* x, const 
     code += d > 0.f ? 1u : 0u;
     least = fminf(least, fabsf(d));
   }
-  const bool open = live && least < kSure;
+  // one answer for the eight: their sums may differ in the last bit (all lanes shuffle)
+  const float lead = __shfl_sync(0xffffffffu, least, threadIdx.x & 24);
+  const bool open = live && lead < kSure;
   if (__any_sync(0xffffffffu, open)) {
     const uint32_t exact = exact_cell<T, BITS>(P, x, ri, cb, mids, open, j);
     if (open) code = exact;                                // lane 0 of the eight has it

@@ -1,9 +1,11 @@
 """GPU parity of the paged cache's operators where their order or their arithmetic is decided by
-little: windows of protected tokens longer than the budget."""
+little: windows of protected tokens longer than the budget, coordinates next to a midpoint.
+Tolerances are those of test_gpu_paged.py."""
 import numpy as np
 import pytest
 
-from test_gpu_paged import D, Pages, dev, run_evict, some_positions, tq  # noqa: F401  (tq: the fixture)
+from conftest import codebook
+from test_gpu_paged import D, Pages, check_append, dev, run_evict, some_positions, tq  # noqa: F401  (tq: the fixture)
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -32,3 +34,39 @@ def test_evict_windows(tq, S, budget, recent):
     pos = some_positions(rng, B, p.H, S, lengths)
     for mass in (np.exp(2 * rng.standard_normal(pos.shape)), rng.integers(0, 3, pos.shape), -rng.random(pos.shape)):
         run_evict(tq, p, mass.astype(np.float32), pos, np.asarray(lengths, np.int32) + 5, budget, recent)
+
+
+# ---- append: coordinates next to midpoints ------------------------------------
+
+def append_and_check(tq, p, K, V, bf16):
+    n = len(K)
+    k, v = (dev(x.astype(np.float32)).bfloat16() if bf16 else dev(x.astype(np.float32)) for x in (K, V))
+    rows = np.stack([np.zeros(n), np.arange(n), np.arange(n)], 1).astype(np.int32)
+    before = p.host()
+    tq.append_paged(k, v, dev(rows), p.cache, p.t)
+    check_append(p, before, k.double().cpu().numpy(), v.double().cpu().numpy(), rows)
+
+
+def with_coordinate(rng, Pi, d, y):
+    """Vectors [n,128] of any length whose unit vectors' coordinate d[i] along Pi is y[i]."""
+    P = Pi.astype(np.float64)[d]
+    x = rng.standard_normal(P.shape)
+    x -= (x * P).sum(1, keepdims=True) * P
+    x *= np.sqrt(1 - y * y)[:, None] / np.linalg.norm(x, axis=1, keepdims=True)
+    return (x + y[:, None] * P) * np.exp(rng.standard_normal((len(d), 1)))
+
+
+@pytest.mark.parametrize("n", [128, 6000])
+@pytest.mark.parametrize("bits", [2, 3, 4])
+def test_append_at_the_bounds_of_the_second_sums(tq, n, bits):
+    """Coordinates at the distances from a midpoint where a code is taken from the first product,
+    from its second sum or from the pairs (5e-6, 2^-19), a few ulp to either side, and on it."""
+    rng = np.random.default_rng(n + bits)
+    p = Pages(tq, 1, 1, n, 256, bits, bits, seed=bits)
+    out = []
+    for Pi, cb in ((p.Pk, p.kc), (p.Pv, p.vc)):
+        mid = 0.5 * (cb[1:].astype(np.float64) + cb[:-1])
+        off = np.array([0.0, 1e-9, 2.0 ** -19, 2.0 ** -19 + 4e-9, 2.0 ** -19 - 4e-9, 2.0 ** -19 + 1e-8, 5e-6, 5e-6 + 4e-9, 5e-6 - 4e-9, 6e-6])
+        y = rng.choice(mid, n) + rng.choice(off, n) * rng.choice((-1.0, 1.0), n)
+        out.append(with_coordinate(rng, Pi[0], rng.integers(0, D, n), y)[:, None])
+    append_and_check(tq, p, out[0], out[1], False)
