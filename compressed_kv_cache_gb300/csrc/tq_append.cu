@@ -121,7 +121,9 @@ struct AppendArgs {
 // Search table: the midpoints' range in cells, each with the midpoint k nearest to it; the code
 // of a v in the cell is k + (v > midpoint k).  The cells are a 62nd of the range or less
 // apart from every other midpoint (or the table is not used: count16), so that no v has
-// another midpoint nearer by.  The cell of v is a saturating FMA and a rounding.
+// another midpoint nearer by.  A v at the edge of a cell may be as near as half a cell to the
+// next midpoint unseen: a cell is 2 kNear or wider.  The cell of v is a saturating FMA and a
+// rounding.
 struct Cell {
   float mid;
   int above;       // k + 1
@@ -140,7 +142,7 @@ __device__ __forceinline__ Grid make_grid(const float* mids, int n, int lane) {
   const float lo = mids[0], hi = mids[n - 1], w = (hi - lo) / static_cast<float>(kCells - 4);
   const bool close = lane + 1 < n && !(mids[min(lane + 1, n - 1)] - mids[min(lane, n - 1)] >= 2.f * w);
   Grid g;
-  g.ok = !__any_sync(0xffffffffu, close) && w > 1e-30f && w < 1e30f;
+  g.ok = !__any_sync(0xffffffffu, close) && w >= 2.f * kNear && w < 1e30f;
   g.scale = 1.f / (w * static_cast<float>(kCells - 1));
   g.shift = (1.5f * w - lo) * g.scale;
   return g;

@@ -70,3 +70,21 @@ def test_append_at_the_bounds_of_the_second_sums(tq, n, bits):
         y = rng.choice(mid, n) + rng.choice(off, n) * rng.choice((-1.0, 1.0), n)
         out.append(with_coordinate(rng, Pi[0], rng.integers(0, D, n), y)[:, None])
     append_and_check(tq, p, out[0], out[1], False)
+
+
+@pytest.mark.parametrize("w", [1e-6, 2e-6, 3.4e-6, 5e-6, 9e-6, 1.1e-5, 4e-5])
+@pytest.mark.parametrize("n", [128, 6000])
+def test_append_midpoints_two_cells_apart(tq, n, w):
+    """Three midpoints at m, m + 2w and m + 124w, so that cells are w wide and the first two as
+    near one another as the cells allow; coordinates between and about them."""
+    rng = np.random.default_rng(n)
+    p = Pages(tq, 1, 1, n, 256, 2, 2, seed=5)
+    out = []
+    for name, Pi, m in (("kc", p.Pk, 0.05), ("vc", p.Pv, -0.031)):
+        c = np.array([m - w, m + w, m + 3 * w, m + 245 * w]).astype(np.float32)
+        setattr(p, name, c)
+        mid = 0.5 * (c[1:].astype(np.float64) + c[:-1])
+        y = rng.choice(mid, n) + rng.choice([0.5, 0.7, 1.0, 1.3, 1.5, 1e-3, 0.0], n) * w * rng.choice((-1.0, 1.0), n)
+        out.append(with_coordinate(rng, Pi[0], rng.integers(0, D, n), y)[:, None])
+    p.upload(tq)
+    append_and_check(tq, p, out[0], out[1], False)
