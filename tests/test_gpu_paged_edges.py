@@ -88,3 +88,24 @@ def test_append_midpoints_two_cells_apart(tq, n, w):
         out.append(with_coordinate(rng, Pi[0], rng.integers(0, D, n), y)[:, None])
     p.upload(tq)
     append_and_check(tq, p, out[0], out[1], False)
+
+
+@pytest.mark.parametrize("n", [128, 6000])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_append_rows_along_the_rotation(tq, n, bf16):
+    """Rows that are sums of one, two or five rows of the rotation: all products of a coordinate
+    point one way, so that the tensor core's errors do.  Midpoints 1e-8 to 2e-5 about it."""
+    rng = np.random.default_rng(n)
+    p = Pages(tq, 1, 1, n, 256, 4, 4, seed=6)
+    for m in (1, 2, 5):
+        off = np.logspace(-8, -4.7, 4)
+        c = np.sort(np.concatenate([m ** -0.5 + s * off + e for s in (-1, 1) for e in (-2e-9, 2e-9)])).astype(np.float32)
+        p.kc = p.vc = c
+        p.upload(tq)
+        out = []
+        for Pi in (p.Pk[0], p.Pv[0]):
+            d, sign = np.stack([rng.permutation(D)[:m] for _ in range(n)]), rng.choice((-1.0, 1.0), (n, m))
+            sign[:, 0] = 1
+            x = (Pi.astype(np.float64)[d] * sign[..., None]).sum(1) * np.exp(rng.standard_normal((n, 1)))
+            out.append((x * (1 + 1e-6 * rng.standard_normal(x.shape)))[:, None])
+        append_and_check(tq, p, out[0], out[1], bf16)
