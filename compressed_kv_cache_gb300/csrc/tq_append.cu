@@ -544,9 +544,12 @@ append_kernel(const __grid_constant__ AppendArgs a) {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *slot;
 
-  bool lost = false;                                       // a wait ran out: the rest is not written
+  // A warp whose wait ran out makes no operand and announces none, issues no product and writes
+  // nothing more.  The others' waits for what it leaves out then run out as well, so that no warp
+  // searches a product whose operand may not have been whole.
+  bool lost = false;
   auto wait = [&](uint32_t bar, int n) {                   // for the bar's n-th use, from 0
-    if (!lost && !wait_parity_bounded(bar, n & 1, kFaultPaged)) lost = true;
+    if (!lost) lost = __any_sync(0xffffffffu, !wait_parity_bounded(bar, n & 1, kFaultPaged));
   };
 
   // Rows part * N .. of a head's rotation, times 2^7, and its codebook's midpoints.  Every warp is
@@ -586,7 +589,7 @@ append_kernel(const __grid_constant__ AppendArgs a) {
     const int i = ahead.item - first;
     wait(whole_op, i);
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    if (lane == 0) {
+    if (lane == 0 && !lost) {
       const uint32_t Aa = smem_u32(sA), Bm = smem_u32(sB), d = tmem + (i & 1) * N;
       const uint32_t la = kRows * 16, lb = N * 16;
 #pragma unroll
@@ -605,6 +608,10 @@ append_kernel(const __grid_constant__ AppendArgs a) {
 
   // A worker's rows of the tile that has come, as fp16, where they go, and the next tile's loads.
   auto make_operand = [&]() {
+    if (lost) {
+      ahead.next(a.tiles);
+      return;
+    }
     const int hk = hk_of(ahead.hkp), kv = hk & 1, h = hk >> 1;
     RowInfo* info = infos + (ahead.item % 3) * kRows;
     char* A = sA;
@@ -718,7 +725,7 @@ append_kernel(const __grid_constant__ AppendArgs a) {
     // the operand is free again
     if (ahead.item < last && ahead.hkp == loaded) make_operand();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    if (!__any_sync(0xffffffffu, lost)) {                  // else the product never came: nothing is written
+    if (!lost) {
       const int hk = hk_of(now.hkp), kv = hk & 1, h = hk >> 1, part = part_of(now.hkp);
       const RowInfo* info = infos + (now.item % 3) * kRows;
       const uint32_t d = tmem + (i & 1) * N;
