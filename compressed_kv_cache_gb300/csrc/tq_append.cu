@@ -549,7 +549,7 @@ append_kernel(const __grid_constant__ AppendArgs a) {
   // searches a product whose operand may not have been whole.
   bool lost = false;
   auto wait = [&](uint32_t bar, int n) {                   // for the bar's n-th use, from 0
-    if (!lost) lost = __any_sync(0xffffffffu, !wait_parity_bounded(bar, n & 1, kFaultPaged));
+    if (!lost) lost = __any_sync(0xffffffffu, !wait_parity_bounded(bar, n & 1, kFaultPagedWait));
   };
 
   // Rows part * N .. of a head's rotation, times 2^7, and its codebook's midpoints.  Every warp is

@@ -163,7 +163,7 @@ __device__ __forceinline__ void prefetch_l2(const void* p, size_t bytes) {
 
 // Fault bits, one per kernel family.
 enum : unsigned int { kFaultLut = 1u, kFaultMma = 2u, kFaultDecode = 4u, kFaultCompress = 8u,
-                      kFaultPaged = 32u };
+                      kFaultPaged = 32u, kFaultPagedWait = 64u };
 
 // Reads and clears the fault word of each translation unit that has bounded waits
 // (synchronous: a cudaMemcpyFromSymbol per unit); ORs the bits into *bits.

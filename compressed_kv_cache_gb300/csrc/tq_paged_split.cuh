@@ -100,6 +100,7 @@ namespace {
 // addresses that are multiples of 64 KB.
 constexpr int kBlock = 65536;
 constexpr int kSmem = 232448;          // all a CTA can have
+constexpr int kFirst = 4096;           // it begins here at the latest: behind what the driver keeps (1 KB)
 
 template <int BITS>
 constexpr int tables_of() { return BITS == 3 ? 2 : 1; }
@@ -112,8 +113,8 @@ struct Lay {
   static constexpr int mask = norms + 4 * kTile;         // which slots of the tile are there
   static constexpr int stage = mask + 16;
   // The warps' rings of stages lie before and behind the blocks; the dynamic shared memory
-  // begins somewhere in the first 4 KB.
-  static constexpr int room0 = kBlock - 4096, room1 = kSmem - (1 + blocks) * kBlock;
+  // begins somewhere in the first 4 KB (kFirst).
+  static constexpr int room0 = kBlock - kFirst, room1 = kSmem - (1 + blocks) * kBlock;
   static constexpr int rings(int stages) { return room0 / (stage * stages) + room1 / (stage * stages); }
   static constexpr int stages = rings(4) >= kSplitWarps ? 4 : rings(3) >= kSplitWarps ? 3 : 2;   // a warp's tiles in flight or in use
   static constexpr int ring = stage * stages;
@@ -470,11 +471,7 @@ paged_split_kernel(const __grid_constant__ SplitArgs p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
 
-  const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-  if (base > 4096) {                                       // not the layout the rings are cut for
-    atomicOr(&g_wait_fault, static_cast<unsigned int>(kFaultPaged));
-    return;
-  }
+  const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));   // kFirst or less: checked by the host
   const uint32_t ring = warp < L::before ? base + warp * L::ring
                                          : (1 + L::blocks) * kBlock + (warp - L::before) * L::ring;
 
@@ -850,6 +847,10 @@ cudaError_t launch_one(const SplitArgs& a, int ctas, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(configured.load(std::memory_order_acquire) & bit)) {
+    int kept = 0;                                          // shared memory before the kernel's own, all of which is dynamic
+    e = cudaDeviceGetAttribute(&kept, cudaDevAttrReservedSharedMemoryPerBlock, dev);
+    if (e == cudaSuccess && kept > kFirst) e = cudaErrorInvalidConfiguration;
+    if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_acq_rel);

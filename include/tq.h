@@ -84,8 +84,8 @@ tq_path tq_auto_path(int B, int D);
  * tq_device_faults ORs into *bits the fault bits set on the CURRENT device since the
  * last call and clears them: 1 = fp32 lookup-table scorers, 2 = tensor-core scorer,
  * 4 = fused decode, 8 = compressor, 16 = tq_check_wait_expiry, 32 = a paged call met a
- * length, slot or page number out of range (see the paged cache below).  It synchronises
- * with the device (it reads device memory) and is not for use inside stream capture.
+ * length, slot or page number out of range (see the paged cache below), 64 = a wait of
+ * tq_append_paged ran out (not all of its rows are written).  It synchronises with the device (it reads device memory) and is not for use inside stream capture.
  * bits: host pointer, not NULL.
  * Errors: TQ_ERR_INVALID_VALUE (bits NULL), TQ_ERR_LAUNCH (the device read failed). */
 tq_status tq_device_faults(unsigned int* bits);
