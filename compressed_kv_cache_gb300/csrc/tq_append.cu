@@ -11,11 +11,11 @@
 // the row's length) is summed again in 64 bits from the inputs.  kNear = 5e-6 covers, in that
 // unit: the operands' 2^-21; the up to 24 fp32 sums of 16 products, each of which is at most the
 // row's length and is off by at most 2^-23 of it even where bits are cut off instead of rounded
-// (2.9e-6 together); the fp32 length's 34 additions (half of 34 x 2^-24, a coordinate being at most
-// 1) and the scaling by it (1.2e-6): 4.5e-6.  Where the tensor core cuts is not documented, so it
-// was measured: without the second sums the farthest coordinate from a midpoint with another code
-// than in 64 bits was 7e-7 away (rows that are one, two or five rows of the rotation, whose products
-// all point one way; 1.3e-7 for random rows).  The window meets about 1 coordinate in 4000 (3 bits).
+// (2.9e-6 together); the fp32 length (8e-7, a coordinate being at most 1) and the scaling by it:
+// 4.4e-6.  Where the tensor core cuts is not documented, so it was measured: without the second
+// sums the farthest coordinate from a midpoint with another code than in 64 bits was 7e-7 away
+// (rows that are one, two or five rows of the rotation, whose products all point one way; 1.3e-7
+// for random rows).  The window meets about 1 coordinate in 4000 (3 bits).
 //
 // N is 128 (the rotation of a head stays in shared memory from tile to tile) or, where that
 // leaves SMs without a tile, 32: a decode step of 64 tokens then runs on four times the SMs.
@@ -39,6 +39,7 @@ constexpr int kRows = 128;             // rows of a tile
 constexpr int kCells = 128;            // cells of the search table
 constexpr int kCopies = 16;            // of each, one for every lane that a load serves at a time
 constexpr float kNear = 5e-6f;
+constexpr float kLength = 8e-7f;       // an fp32 length is off by less: 19 roundings of its square (half of 19 x 2^-24), two of its own
 
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
@@ -218,7 +219,7 @@ struct RowInfo {
   float inv;         // 1 / (length * scales): turns a sum into a unit coordinate; 0 where there is none
   float scale;       // the power of two that takes the row to 2^7 (in two factors for tiny rows)
   int kind;          // 0: no row, 1: an ordinary one, 2: zero, 3: NaN or infinity within
-  uint32_t norm;     // fp16 length
+  float norm;        // length, to kLength
   int tiny;          // the other factor is 2^64
   int code;          // kinds 2 and 3: the code of every coordinate
   long long at;      // row on the cache's planes
@@ -348,6 +349,38 @@ __device__ __forceinline__ uint32_t near_cell(const float* P, const T* x, const 
   return code;
 }
 
+// The length of a row, as fp16, of which `below` or the next number is the nearest: the sum of
+// squares as a pair of fp32 against the square of the middle (12 bits, so the square is exact; the
+// even one on it).  The whole warp, four coordinates a lane.  A row in 300 to 600 comes here; inlined
+// it cost prompts 1 to 2 us, in the warps that make operands 1.5 (bf16) and 14 (fp32).
+template <typename T>
+__device__ __noinline__ uint32_t nearest_length(const T* x, float scale, uint32_t below, int lane) {
+  float v[4], q = 0.f, e = 0.f;
+  if constexpr (sizeof(T) == 4) {
+    const float4 u = __ldg(reinterpret_cast<const float4*>(x) + lane);
+    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+  } else {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(x) + lane);
+    v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xffff0000u);
+    v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xffff0000u);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float z = v[i] * scale, z2 = __fmul_rn(z, z);
+    e += fmaf(z, z, -z2) + add_exact(q, z2);
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float qo = __shfl_xor_sync(0xffffffffu, q, o), eo = __shfl_xor_sync(0xffffffffu, e, o);
+    e += eo + add_exact(q, qo);
+  }
+  // behind the largest number comes 65536
+  const float next = below == 0x7bffu ? 65536.f : __half2float(__ushort_as_half(static_cast<uint16_t>(below + 1)));
+  const float mid = 0.5f * (__half2float(__ushort_as_half(static_cast<uint16_t>(below))) + next) * scale;
+  const float diff = (q - __fmul_rn(mid, mid)) + e;
+  return diff > 0.f || (diff == 0.f && (below & 1)) ? below + 1 : below;
+}
+
 // A warp's share of a tile: 32 rows, 32 coordinates each (where N is 32, on the first four
 // warps), from tensor memory to the planes.
 template <typename T, int BITS>
@@ -430,7 +463,18 @@ __device__ __forceinline__ void search_tile(const AppendArgs& a, int kv, int h, 
       for (int i = 0; i < BITS; ++i) o[i] = w[i];
     }
   }
-  if (part == 0 && warp < 4 && ri.kind != 0) (kv ? a.pg.vn : a.pg.kn)[ri.at] = static_cast<uint16_t>(ri.norm);
+  {                                                        // lengths: each warp (or part) those of 8 of the rows
+    const bool mine = ri.kind != 0 && (lane >> 3) == (whole ? c0 : part);
+    const uint32_t below = __half_as_ushort(__float2half_rn(ri.norm * (1.f - kLength)));
+    uint32_t norm = __half_as_ushort(__float2half_rn(ri.norm * (1.f + kLength)));   // another number: the next
+    for (uint32_t left = __ballot_sync(0xffffffffu, mine && ri.kind == 1 && below != norm); left != 0; left &= left - 1) {
+      const int owner = __ffs(left) - 1;
+      const uint32_t near = nearest_length(X + (static_cast<size_t>(tile * kRows + r0 + owner) * a.pg.H + h) * kPD, info[r0 + owner].scale,
+                                           __shfl_sync(0xffffffffu, below, owner), lane);
+      if (lane == owner) norm = near;
+    }
+    if (mine) (kv ? a.pg.vn : a.pg.kn)[ri.at] = static_cast<uint16_t>(norm);
+  }
 }
 
 constexpr int kWorkers = 512;          // 16 warps that make operands and search, and one more:
@@ -662,18 +706,20 @@ append_kernel(const __grid_constant__ AppendArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[k][i] *= s0;
     }
-    float sum = 0.f;
+    float sums[2] = {0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
+      float& sum2 = sums[k & 1];                           // two chains: 19 roundings instead of 34
 #pragma unroll
       for (int i = 0; i < 8; ++i) {                        // NaN and infinity stay within their row, which takes no codes from it
         x[k][i] *= s1;
-        sum = fmaf(x[k][i], x[k][i], sum);
+        sum2 = fmaf(x[k][i], x[k][i], sum2);
       }
       const int at = ((lane >> 3) + 4 * k) * (kRows * 16) + (r >> 3) * 128 + (r & 7) * 16;
       *reinterpret_cast<uint4*>(A + at) = hi_chunk(x[k]);
       if constexpr (XLO) *reinterpret_cast<uint4*>(A + kRows * 256 + at) = lo_chunk(x[k]);
     }
+    float sum = sums[0] + sums[1];
     sum += __shfl_xor_sync(0xffffffffu, sum, 8);
     sum += __shfl_xor_sync(0xffffffffu, sum, 16);
     if (lane < 8) {
@@ -684,10 +730,10 @@ append_kernel(const __grid_constant__ AppendArgs a) {
       ri.scale = s1;
       ri.tiny = s0 != 1.f;
       ri.inv = kind == 1 ? 1.f / (128.f * len) : 0.f;
-      // the length: powers of two taken back, one rounding in fp32 and one to fp16
+      // the length, the powers of two taken back
       const float back = __uint_as_float(static_cast<uint32_t>(127 - k2) << 23) * (s0 != 1.f ? 5.42101086e-20f : 1.f);
       const float n = kind == 1 ? len * back : kind == 2 ? 0.f : __uint_as_float(top > 0x7f800000u ? 0x7fc00000u : 0x7f800000u);
-      ri.norm = __half_as_ushort(__float2half_rn(n));
+      ri.norm = n;
       int zero = 0;
       if (kind == 2)
         for (int i = 0; i + 1 < (1 << a.bits[kv]); ++i) zero += a.cb[kv][i] + a.cb[kv][i + 1] < 0.f ? 1 : 0;   // the sign is exact

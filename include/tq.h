@@ -315,7 +315,7 @@ typedef struct {
  * K, V: [n, H, D] of `type`.  rows: [n, 3] int32 (sequence, slot, position); a negative
  * sequence or slot skips the row (padding), a sequence >= B or a slot outside the capacity
  * (or a slot on an absent page) skips it too and sets fault bit 32.  For row i and head h
- *   length = ||k||_2, rounded to fp16 (to nearest, infinity above 65504),
+ *   length = ||k||_2, rounded once to fp16 (to the nearest, ties to even, infinity from 65520),
  *   idx_d = number of codebook midpoints strictly below (Pi k / ||k||)_d, decided as in
  *   64 bits (a coordinate near a midpoint is summed again in 64 bits; the rows of Pi are
  *   taken as unit vectors there); a zero key takes the cells of 0, a key that holds a NaN

@@ -109,3 +109,47 @@ def test_append_rows_along_the_rotation(tq, n, bf16):
             x = (Pi.astype(np.float64)[d] * sign[..., None]).sum(1) * np.exp(rng.standard_normal((n, 1)))
             out.append((x * (1 + 1e-6 * rng.standard_normal(x.shape)))[:, None])
         append_and_check(tq, p, out[0], out[1], bf16)
+
+
+# ---- append: lengths ----------------------------------------------------------
+
+def lengths_of(tq, K):
+    n = K.shape[0]
+    p = Pages(tq, 1, 1, n, 256, 3, 3, seed=8)
+    rows = np.stack([np.zeros(n), np.arange(n), np.arange(n)], 1).astype(np.int32)
+    tq.append_paged(K, K, dev(rows), p.cache, p.t)
+    kn, vn = (x[p.table[0, rows[:, 1] // 256], 0, rows[:, 1] % 256] for x in (p.host()[1], p.host()[3]))
+    assert np.array_equal(kn, vn)
+    return kn
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_append_lengths_are_the_nearest(tq, bf16):
+    """fp16 lengths of random rows of all sizes are those of the 64-bit ones."""
+    rng = np.random.default_rng(1)
+    K = rng.standard_normal((20000, 1, D)) * np.exp(3 * rng.standard_normal((20000, 1, 1)))
+    K[::3, :, 1:] *= 1e-3
+    k = dev(K.astype(np.float32)).bfloat16() if bf16 else dev(K.astype(np.float32))
+    got = lengths_of(tq, k)
+    with np.errstate(over="ignore"):
+        want = np.sqrt((k[:, 0].double().cpu().numpy() ** 2).sum(-1)).astype(np.float16)
+    assert np.array_equal(got, want), f"{(got != want).sum()} lengths differ"
+
+
+def test_append_lengths_between_two_steps(tq):
+    """Lengths on the middle of two fp16 numbers (to the even one), and 2^-25 of it to either
+    side; about the largest number, among the subnormal ones, and about the smallest."""
+    steps = np.arange(0x7c00, dtype=np.uint16).view(np.float16).astype(np.float64)
+    rng = np.random.default_rng(2)
+    i = np.concatenate([rng.integers(0, 0x7bff, 400), np.arange(6), np.arange(0x3fa, 0x405), [0x7bfe, 0x7bff]])
+    lo, hi = steps[i], np.append(steps, 65536.0)[i + 1]
+    mid = 0.5 * (lo + hi)
+    K = np.zeros((3 * i.size, 1, D), np.float32)
+    for j, d in enumerate((0, 1, -1)):
+        K[j * i.size:(j + 1) * i.size, 0, 70] = np.nextafter(mid.astype(np.float32), np.float32(np.inf * d)) if d else mid
+    K[i.size:2 * i.size:2, 0, 70] = mid[::2]                   # above it by another coordinate
+    K[i.size:2 * i.size:2, 0, 3] = mid[::2] * 2.0 ** -12
+    got = lengths_of(tq, dev(K))
+    with np.errstate(over="ignore"):
+        want = np.sqrt((K[:, 0].astype(np.float64) ** 2).sum(-1)).astype(np.float16)
+    assert np.array_equal(got, want), np.flatnonzero(got != want)
