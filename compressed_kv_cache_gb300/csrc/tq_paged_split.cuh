@@ -35,11 +35,14 @@
 // powers of two to 2^7 before they become fp16, so that lo stays out of the subnormals.
 //
 // The tensor core's additions cut bits off, so that the errors of a long sum of like terms add up
-// (fp32 queries, flat weights, 1150 tiles a run: 6.8e-5).  A warp therefore takes a unit in
-// pieces of at most kPiece tiles, and adds each piece to its partial with rounded additions; with
-// VX it keeps their rounding errors too.  What is left is the error of one piece, whatever the
-// cache's length.  Additions every 8 tiles within the loop cost the registers they took: 2.5 % of
-// a call.
+// (fp32 queries, flat weights, 1150 tiles a run: 6.8e-5).  With VX the value products of 16 slots
+// begin at zero and are added to the sums with rounded additions, two a tile.  A warp takes a unit in
+// pieces of at most kPiece tiles, and adds each piece to its partial; with VX it keeps the rounding
+// errors of that too.  What is left is the error of one piece, whatever the cache's length: fp32 256
+// additions of 2^-24 of a sum that grows evenly, 7.6e-6 at worst and 7e-7 measured (flat
+// weights, one value row).  32 x 32768 x 64 heads on 8, fp32: 731 us, and 691 without either; one
+// chain of the tensor core in pieces of 64 tiles 721 (5.5e-6 off), of 32 tiles 758 (2.6e-6).
+// Additions to the partial from within the loop (721) take registers that the other variants miss.
 #pragma once
 
 #include "tq_paged.cuh"
@@ -50,7 +53,7 @@ constexpr int kSplitWarps = 12;
 constexpr int kTile = 32;            // slots a warp takes at a time
 constexpr int kPartF = 132;          // partial of a query: 128 sums, maximum, sum, 2 unused
 constexpr int kMaxCtas = 192;        // partials are laid out for at most this many CTAs
-constexpr int kPieceX = 32, kPiece = 256;   // tiles of a piece (VX: 128 additions of the tensor core in a row)
+constexpr int kPieceX = 128, kPiece = 256;   // tiles of a piece
 
 // A unit's share of the tiles is cut where the warps' runs are cut: run w covers
 // [w q + min(w, r), ...) of T = q W + r tiles.
@@ -396,6 +399,7 @@ __device__ __forceinline__ void value_pairs(Pairs<VB, VX>& r, uint32_t w, uint32
 }
 
 // Weighted sum of four keys' values (slots 2t, 2t+1, 2t+8, 2t+9 of the product), word I and on.
+// VX: the product is added with a rounding of its own.
 template <int VB, bool VX, int I>
 __device__ __forceinline__ void value_products(float (&acc)[8][4], const uint32_t (&wa)[2], const uint32_t (&wb)[2],
                                                const uint32_t (&wc)[2], const uint32_t (&wd)[2], uint32_t low,
@@ -412,8 +416,15 @@ __device__ __forceinline__ void value_products(float (&acc)[8][4], const uint32_
 #pragma unroll
   for (int k = 0; k < Pr::n; ++k) {
     const int m = I * Pr::n + k;
-    mma(acc[m], f0.hi[k], f1.hi[k], f2.hi[k], f3.hi[k], b0, b1);
-    if constexpr (VX) mma(acc[m], f0.lo[k], f1.lo[k], f2.lo[k], f3.lo[k], b0, b1);
+    if constexpr (VX) {
+      float c[4];
+      mma0(c, f0.hi[k], f1.hi[k], f2.hi[k], f3.hi[k], b0, b1);
+      mma(c, f0.lo[k], f1.lo[k], f2.lo[k], f3.lo[k], b0, b1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[m][i] += c[i];
+    } else {
+      mma(acc[m], f0.hi[k], f1.hi[k], f2.hi[k], f3.hi[k], b0, b1);
+    }
   }
   if constexpr ((I + 1) * Pr::n < 8)
     value_products<VB, VX, I + 1>(acc, wa, wb, wc, wd, low, high, p, b0, b1);
