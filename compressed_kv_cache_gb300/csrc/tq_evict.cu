@@ -364,12 +364,14 @@ evict_move_kernel(Paged pg, const float* __restrict__ mass, const int* __restric
 // Rows one (sequence, head) can move.
 int most_moves(int S, int budget) { return budget >= S ? 0 : (budget < S - budget ? budget : S - budget); }
 
-// CTAs of a cluster: enough to fill the device from few rows, at least 4096 slots each (16 x 8
-// rows of 4224 slots: 14.8 us a call with one CTA a row, 17.4 with two, 31 with four), and
-// as many as it takes to keep the keys in shared memory (where 8 do).
+// CTAs of a cluster: as many as it takes to keep the keys in shared memory (where 8 do), and
+// enough to fill the device from few rows.  Up to one CTA an SM a share is 2048 slots or more (8 x 8
+// rows of 8191: 15.6 us a call with two CTAs a row, 17.3 with one; 1 row of 8191: 13.4 and 15.8, 1
+// of 4224: 12.5 and 13.6), up to two 4096 or more (16 x 8 rows of 4224: 15.1 us with one, 17.4
+// with two, 31 with four).
 int cluster_size(int S, int64_t units, int sms) {
   int C = 1;
-  while (C < kCluster && ((units * C * 2 <= 2 * sms && S / (2 * C) >= 4096) || S > C * kCached)) C *= 2;
+  while (C < kCluster && (S > C * kCached || (units * C * 2 <= sms && S / (2 * C) >= 2048) || (units * C <= sms && S / (2 * C) >= 4096))) C *= 2;
   return C;
 }
 bool keys_fit(int S) { return S <= kCluster * kCached; }
