@@ -28,13 +28,6 @@ struct Paged {
   __device__ __forceinline__ size_t row(int pg, int h, int s) const {
     return ((static_cast<size_t>(pg) * H + h) << shift) + (s & ((1 << shift) - 1));
   }
-  // A sequence's length, cut to the capacity (recorded when it had to be).
-  __device__ __forceinline__ int length(const int* lengths, int b, int cap) const {
-    const int n = lengths[b];
-    if (n >= 0 && n <= cap) return n;
-    atomicOr(&g_wait_fault, static_cast<unsigned int>(kFaultPaged));
-    return n < 0 ? 0 : cap;
-  }
 };
 
 inline Paged paged_view(const tq_paged_cache& c, const int* table, int max_pages) {
