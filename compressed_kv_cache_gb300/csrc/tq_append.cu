@@ -23,8 +23,8 @@
 // Bound: latency and issue, not yet memory.  8192 tokens x 8 heads, bf16, 3-bit codes: 44 us, of
 // which 5 are set-up (tensor memory, the rotation's fp16 form) and about 5 a tile (7 tiles an SM):
 // rows to fp16 0.8, the search of the cells 2 to 3, waits on the slowest warp and on the product
-// the rest; 0.94 TB/s of the rows' and codes' bytes.  15003 fp32 rows x 8 heads, 4-bit codes: 91
-// us, 1.55 TB/s.  Measured on the way there (8192 tokens): everything in 64 bits 13.5 ms; near
+// the rest; 0.94 TB/s of the rows' and codes' bytes.  15003 fp32 rows x 8 heads, 4-bit codes: 95
+// us, 1.48 TB/s.  Measured on the way there (8192 tokens): everything in 64 bits 13.5 ms; near
 // coordinates listed and summed again in 64 bits 75 us (a 64-bit instruction takes a warp 16
 // cycles); in pairs of fp32 50 us; binary search of the midpoints instead of the cells 52 us;
 // rows prefetched in registers 53 us (they spill); two CTAs of 8 warps an SM 52 us; a barrier

@@ -15,8 +15,8 @@
 //
 // Bound: select by dependent latencies (16 x 8 rows of 4224 slots: some 40 loads, barriers and
 // scans in a row, 15 us a call with the moves); move by DRAM's sectors: a row's 48 + 48 + 2 + 2 + 4 + 4
-// bytes lie in scattered 32-byte sectors.  4 x 8 rows of 131072 slots to 32768: select 45 us, move
-// 58 us for 314 MB of DRAM traffic (5.5 TB/s) where the rows' own bytes are 157 MB; 103 us a call.
+// bytes lie in scattered 32-byte sectors.  4 x 8 rows of 131072 slots to 32768: select 47 us, move
+// 58 us for 314 MB of DRAM traffic (5.4 TB/s) where the rows' own bytes are 157 MB; 104 us a call.
 // Measured on the way there (4 x 8 rows): one CTA a row 1853 us; 1024 threads a CTA (one an SM, two waves)
 // 139 us, 512 threads 111 us; weights loaded eight deep 105 us; 128 rows a CTA of move 103 us.
 #include <cooperative_groups.h>

@@ -7,7 +7,7 @@
 //
 // What each costs alone (16 ragged sequences of up to 8191 slots, 8 heads of 4 queries, with
 // mass): plan 6.5 us, split 31, join 8.1, mass 7.2; 40 us a call, as the next one's launch and
-// set-up overlap the one before.  The shortest call (1 sequence, 1021 slots) is 10.3 us, three
+// set-up overlap the one before.  The shortest call (1 sequence, 1021 slots) is 10.7 us, three
 // launches of 2 to 3 us of dependent loads each.  The logits go through the workspace (16 bytes a slot at 4
 // queries, written and read from L2): what a weight is divided by is known only after the join.
 #include "tq_paged_split.cuh"

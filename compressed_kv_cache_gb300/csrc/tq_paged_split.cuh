@@ -17,20 +17,28 @@
 //
 // Bound: shared memory.  The look-ups read 512 bytes a slot whatever the codes' width, 4
 // wavefronts; codes, lengths and the copies into the ring add 2.8.  131072 slots x 8 heads, 3-bit
-// codes: 245 cycles a tile of 32 slots in the loop, 217 of them wavefronts; the ALU pipe is
-// 46 % and issue 58 % busy.  36 us (2.9 TB/s of codes) of a call of 42; 32 x 32768 x 8 heads, 4-bit
-// keys: a call of 274 us, 3.6 TB/s.  hi + lo look-ups (KX) are 8 bytes each: 335 cycles a tile.
+// codes: 245 cycles a tile of 32 slots in the loop, 217 of them wavefronts; over the whole kernel
+// shared memory is 65 %, issue 58 % and the ALU pipe 46 % busy.  It takes 37 us (2.9 TB/s of codes)
+// of a call of 42: 26.5 in the loop, 4 for tables, set-up, first tiles and partials, the rest at the
+// grid's start and end.  32 x 32768 x 8 heads, 4-bit keys: a call of 275 us, 3.6 TB/s.  With
+// the look-ups' addresses in the place of what they read, the two calls take 38 and 197 us.
+// hi + lo look-ups (KX) are 8 bytes each: 335 cycles a tile.
 // Measured on the way there (131072 slots x 8 heads, whole call): two-code tables in 64 entries
 // with shifts and masks on the ALU pipe 63 us; shifts to the left on the FMA pipe and
 // aligned tables 49 us; 256 entries picked by a byte permute 46 us; 8, 12 or 16 warps within
-// 5 % of each other; without the products 1 us less, without the look-ups 4 us less.
+// 5 % of each other.
 //
 // The order of the sum over coordinates and over slots is free, and is chosen for the loads:
 // lane (g, t) of a warp (g = lane / 4, t = lane % 4) takes coordinates 32t .. 32t+31 of two
 // keys (whole words of their rows), and coordinates 16g .. 16g+15 of four values.
 //
 // Precision: a factor x is an fp16 pair hi + lo (22 bits) where KX / VX ask for it; then
-// hi hi + hi lo + lo hi are summed.  COL: four queries, whose hi and lo parts are columns
+// hi hi + hi lo + lo hi are summed.  bf16 queries get a bf16 output, so fp16 operands (2^-11) are
+// finer than what comes in and goes out: rotated queries, key and value centroids and weights are
+// single fp16 numbers (131072 slots: 2.2e-3 of the output's norm from 64 bits, products of fp32
+// operands 1.8e-3, mostly the output's rounding).  With mass the keys' factors are pairs, as the
+// weights are summed over many steps (and up to 4 queries a unit the weights).  fp32 queries: pairs
+// everywhere.  COL: four queries, whose hi and lo parts are columns
 // 0..3 and 4..7 of one product.  Centroids, queries, and values' lengths are scaled by
 // powers of two to 2^7 before they become fp16, so that lo stays out of the subnormals.
 //

@@ -512,7 +512,9 @@ class PagedCache:
     and v_norm likewise; Pi_k, Pi_v fp32 [h,D,D] (or [D,D]), KV head i using rotation i % h;
     k_codebook, v_codebook fp32 of 2^bits ascending centroids.  D is 128, bits 2 to 4, page a
     power of two from 16 to 256.  The tensors stay the caller's (they may be written between
-    calls, not resized); all are on one device, and the calls run there."""
+    calls, not resized); all are on one device, and the calls run there.  As everywhere in this
+    library arrays begin on a 16-byte boundary, so a slice of lengths, rows or a page table may
+    have to be copied first (TQ_ERR_MISALIGNED)."""
 
     __slots__ = ("k_plane", "k_norm", "v_plane", "v_norm", "Pi_k", "k_codebook", "Pi_v", "v_codebook", "device",
                  "H", "page_size", "D", "k_bits", "v_bits", "_struct", "_ref", "_index")
@@ -624,7 +626,8 @@ def decode_paged(Q, cache: PagedCache, page_table, lengths, mass=None, scale=Non
     fp32/bf16 (query head i reads KV head i // G); page_table int32 [B,max_pages], lengths
     int32 [B].  mass fp32 [B,H,S] (optional): the weights each slot received, summed over its
     group's queries, are added to it.  scale defaults to 1/sqrt(D).  Returns Q's shape and
-    type; zeros for a sequence of length 0."""
+    type; zeros for a sequence of length 0.  Q's type decides the precision: fp32 accuracy for
+    fp32, products of fp16 operands for bf16 (the logits keep fp32 accuracy with mass)."""
     if not isinstance(Q, torch.Tensor) or Q.dim() != 3 or Q.dtype not in QTYPE:
         raise ValueError("Q must be a [B, heads, D] fp32 or bf16 tensor")
     dev, H, D = cache._index, cache.H, cache.D
