@@ -339,7 +339,8 @@ tq_status tq_append_paged(const tq_paged_cache* cache, const void* K, const void
  *
  * Q: [B, H*G, D] of `qtype`, query head h*G + g reads KV head h.  out: the same shape and
  * type.  fp32 queries: every product to fp32 accuracy, |err| <= 1e-5 (1 + |out|) for value
- * lengths of order one.  bf16 queries: products of fp16 operands (each rounded to 2^-11)
+ * lengths of order one and logits of order ten, whatever the cache's length (a logit is off by
+ * at most 2^-17 of scale nk_i sum_d |a_d c_d|, a = Pi_k q).  bf16 queries: products of fp16 operands (each rounded to 2^-11)
  * summed in fp32, the output rounded to bf16; with mass the logits keep fp32 accuracy.
  * The same inputs give the same bits.  Sequences may share pages.  scale: finite.
  * workspace: at least tq_decode_paged_workspace_bytes(B, H, G, S, mass != NULL) bytes,
