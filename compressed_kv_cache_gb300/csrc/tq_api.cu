@@ -5,6 +5,7 @@
 #include <cmath>
 
 #include "tq_internal.cuh"
+#include "tq_paged.cuh"
 
 namespace {
 

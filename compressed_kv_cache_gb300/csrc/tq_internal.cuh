@@ -113,19 +113,6 @@ cudaError_t launch_decode_prod(const float* A, const float* T, const uint8_t* k_
                                const float* v_cb, int v_bits, const float* Pi_v, float* out,
                                float* part, int P, int H, int B, int S, float scale, cudaStream_t st);
 
-// Paged cache (D == 128): quantise and write new rows, decode, evict.
-cudaError_t launch_append_paged(const tq_paged_cache& c, const void* K, const void* V, tq_qtype type,
-                                const int* rows, int n, const int* table, int B, int max_pages, float* mass,
-                                int* positions, int S, cudaStream_t st);
-size_t decode_paged_bytes(int B, int H, int G, int S, bool with_mass);
-cudaError_t launch_decode_paged(const tq_paged_cache& c, const void* Q, tq_qtype qtype, const int* table,
-                                const int* lengths, int B, int G, int max_pages, float scale, float* mass,
-                                int S, void* out, void* ws, cudaStream_t st);
-size_t evict_paged_bytes(int B, int H, int S, int budget);
-cudaError_t launch_evict_paged(const tq_paged_cache& c, const int* table, const int* lengths, const int* seen,
-                               int B, int max_pages, const float* mass, const int* positions, int S, int budget,
-                               int recent, float* mass_out, int* positions_out, void* ws, cudaStream_t st);
-
 cudaError_t launch_pack_indices(const uint8_t* K_idx, uint8_t* plane, int64_t n, int D, int bits,
                                 cudaStream_t st);
 cudaError_t launch_unpack_indices(const uint8_t* plane, uint8_t* K_idx, int64_t n, int D,
@@ -162,8 +149,7 @@ __device__ __forceinline__ void prefetch_l2(const void* p, size_t bytes) {
 }
 
 // Fault bits, one per kernel family.
-enum : unsigned int { kFaultLut = 1u, kFaultMma = 2u, kFaultDecode = 4u, kFaultCompress = 8u,
-                      kFaultPaged = 32u, kFaultPagedWait = 64u };
+enum : unsigned int { kFaultLut = 1u, kFaultMma = 2u, kFaultDecode = 4u, kFaultCompress = 8u };
 
 // Reads and clears the fault word of each translation unit that has bounded waits
 // (synchronous: a cudaMemcpyFromSymbol per unit); ORs the bits into *bits.
@@ -171,9 +157,6 @@ cudaError_t take_faults_simt(unsigned int* bits);
 cudaError_t take_faults_mma(unsigned int* bits);
 cudaError_t take_faults_decode(unsigned int* bits);
 cudaError_t take_faults_compress(unsigned int* bits);
-cudaError_t take_faults_append(unsigned int* bits);
-cudaError_t take_faults_paged(unsigned int* bits);
-cudaError_t take_faults_evict(unsigned int* bits);
 
 namespace {
 // This translation unit's fault word (internal linkage: one per unit).

@@ -1,9 +1,30 @@
-// Shared pieces of the paged-cache kernels (tq_append.cu, tq_paged_*.cu, tq_evict.cu).
+// Shared pieces of the paged-cache kernels (tq_append.cu, tq_paged_*.cu, tq_evict.cu), and what
+// tq_api.cu calls of them.
 #pragma once
 
 #include "tq_internal.cuh"
 
 namespace tq {
+
+// Launches (D == 128): quantise and write new rows, decode, evict.
+cudaError_t launch_append_paged(const tq_paged_cache& c, const void* K, const void* V, tq_qtype type,
+                                const int* rows, int n, const int* table, int B, int max_pages, float* mass,
+                                int* positions, int S, cudaStream_t st);
+size_t decode_paged_bytes(int B, int H, int G, int S, bool with_mass);
+cudaError_t launch_decode_paged(const tq_paged_cache& c, const void* Q, tq_qtype qtype, const int* table,
+                                const int* lengths, int B, int G, int max_pages, float scale, float* mass,
+                                int S, void* out, void* ws, cudaStream_t st);
+size_t evict_paged_bytes(int B, int H, int S, int budget);
+cudaError_t launch_evict_paged(const tq_paged_cache& c, const int* table, const int* lengths, const int* seen,
+                               int B, int max_pages, const float* mass, const int* positions, int S, int budget,
+                               int recent, float* mass_out, int* positions_out, void* ws, cudaStream_t st);
+
+// Fault bits: a number out of range, a wait of the append that ran out.
+enum : unsigned int { kFaultPaged = 32u, kFaultPagedWait = 64u };
+cudaError_t take_faults_append(unsigned int* bits);
+cudaError_t take_faults_paged(unsigned int* bits);
+cudaError_t take_faults_evict(unsigned int* bits);
+
 namespace {
 
 constexpr int kPD = 128;   // head dimension

@@ -40,7 +40,7 @@ def test_fault_bits_of_the_paged_calls_have_one_meaning_each():
     for name in sorted(os.listdir(os.path.join(ROOT, "compressed_kv_cache_gb300", "csrc"))):
         t = source(name)
         assert not re.search(r"wait_parity_bounded\([^;]*kFaultPaged\)", t), name
-    assert "kFaultPagedWait = 64u" in source("tq_internal.cuh")
+    assert "kFaultPagedWait = 64u" in source("tq_paged.cuh")
     assert "kFaultPagedWait" in source("tq_append.cu")
     kernel = block(source("tq_paged_split.cuh"), "paged_split_kernel")
     assert "return;" not in kernel and kernel.count("kFaultPaged") == 1
