@@ -6,6 +6,7 @@
 
 #include "tq_internal.cuh"
 #include "tq_paged.cuh"
+#include "tq_int8.cuh"
 
 namespace {
 
@@ -124,6 +125,30 @@ tq_status check_paged(const tq_paged_cache* c, const int* page_table, int B, int
   return TQ_OK;
 }
 
+// The cache struct of the 8-bit calls, and the sizes they share.
+tq_status check_int8(const tq_int8_cache* c, const int* starts, const int* lengths, const int* page_table, int n,
+                     int B, int max_pages) {
+  if (c == nullptr) return TQ_ERR_INVALID_VALUE;
+  tq_status st = check_ptrs(c->k_codes, c->v_codes, c->exponents, starts, lengths, page_table);
+  if (st != TQ_OK) return st;
+  if (c->n_pages < 1 || c->H < 1 || c->H > kMaxGridYZ || c->D < 1 || c->page_size < 1) return TQ_ERR_INVALID_VALUE;
+  if (static_cast<int64_t>(c->n_pages) * c->H > INT_MAX) return TQ_ERR_INVALID_VALUE;
+  if (c->D != 64 && c->D != 128) return TQ_ERR_UNSUPPORTED;
+  const int ps = c->page_size;
+  if (ps < 16 || ps > 256 || (ps & (ps - 1)) != 0) return TQ_ERR_UNSUPPORTED;
+  if (B < 1 || B > kMaxGridYZ || max_pages < 1 || max_pages > (INT_MAX - 4096) / ps) return TQ_ERR_INVALID_VALUE;
+  if (n < 0 || static_cast<int64_t>(n) * c->H > INT_MAX || static_cast<int64_t>(B) * c->H > kMaxPagedQueries)
+    return TQ_ERR_INVALID_VALUE;
+  return TQ_OK;
+}
+
+// A stride in elements that keeps 16-byte pieces whole.
+bool bad_stride(int64_t stride, tq_qtype type) {
+  return stride < 0 || stride > (static_cast<int64_t>(1) << 40) || stride % (type == TQ_Q_F32 ? 4 : 8) != 0;
+}
+
+bool bad_type(tq_qtype type) { return type != TQ_Q_F32 && type != TQ_Q_BF16; }
+
 // An array that may be left out: null, or aligned.
 bool bad_optional(const void* p) { return p != nullptr && misaligned(p); }
 
@@ -167,6 +192,8 @@ tq_status tq_device_faults(unsigned int* bits) {
   if (e == cudaSuccess) e = tq::take_faults_append(&v);
   if (e == cudaSuccess) e = tq::take_faults_paged(&v);
   if (e == cudaSuccess) e = tq::take_faults_evict(&v);
+  if (e == cudaSuccess) e = tq::take_faults_int8_rows(&v);
+  if (e == cudaSuccess) e = tq::take_faults_int8_attend(&v);
   if (e != cudaSuccess) return TQ_ERR_LAUNCH;
   *bits |= v;
   return TQ_OK;
@@ -426,6 +453,91 @@ tq_status tq_evict_paged(const tq_paged_cache* cache, const int* page_table, con
   if (workspace_bytes < tq_evict_paged_workspace_bytes(B, cache->H, S, budget)) return TQ_ERR_WORKSPACE;
   return from_cuda(tq::launch_evict_paged(*cache, page_table, lengths, seen, B, max_pages, mass, positions, S,
                                           budget, recent, mass_out, positions_out, workspace, stream));
+}
+
+tq_status tq_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                       int64_t k_token_stride, int64_t k_head_stride, tq_qtype type,
+                       const void* q_weight, const void* k_weight, tq_qtype weight_type, float eps,
+                       const int* positions, int axes, const uint64_t* turns, const uint8_t* axis,
+                       int pairs, int paired, void* q_out, void* k_out, int n, int Hq, int Hk, int D,
+                       cudaStream_t stream) {
+  if (n < 0 || Hq < 1 || Hk < 0 || Hq > kMaxGridYZ || Hk > kMaxGridYZ || D < 1 || D > 256) return TQ_ERR_INVALID_VALUE;
+  if (bad_type(type) || bad_type(weight_type) || axes < 1 || axes > 8 || pairs < 1 || pairs > D / 2 ||
+      (paired != 0 && paired != 1) || !(eps >= 0.0f) || !std::isfinite(eps))
+    return TQ_ERR_INVALID_VALUE;
+  if (D % 8 != 0 || pairs % 4 != 0) return TQ_ERR_UNSUPPORTED;
+  if (bad_stride(q_token_stride, type) || bad_stride(q_head_stride, type)) return TQ_ERR_INVALID_VALUE;
+  if (Hk > 0 && (bad_stride(k_token_stride, type) || bad_stride(k_head_stride, type))) return TQ_ERR_INVALID_VALUE;
+  // rows in 32 bits: a grid of one warp a row still fits
+  if (static_cast<int64_t>(n) * (Hq + Hk) > INT_MAX) return TQ_ERR_INVALID_VALUE;
+  if (n == 0) return TQ_OK;
+  tq_status st = check_ptrs(q, positions, turns, axis, q_out);
+  if (st == TQ_OK && Hk > 0) st = check_ptrs(k, k_out);
+  if (st != TQ_OK) return st;
+  if (bad_optional(q_weight) || bad_optional(k_weight)) return TQ_ERR_MISALIGNED;
+  const size_t size = type == TQ_Q_F32 ? 4 : 2;
+  struct Range { uintptr_t a, z; bool dense; };
+  auto in = [&](const void* p, int64_t ts, int64_t hs, int H) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    return Range{a, a + (static_cast<uintptr_t>(n - 1) * ts + static_cast<uintptr_t>(H - 1) * hs + D) * size,
+                 (hs == D || H == 1) && (ts == static_cast<int64_t>(H) * D || n == 1)};
+  };
+  auto meets = [](const Range& x, const Range& y) { return x.a < y.z && y.a < x.z; };
+  const Range rq = in(q, q_token_stride, q_head_stride, Hq), oq = in(q_out, static_cast<int64_t>(Hq) * D, D, Hq);
+  if (meets(rq, oq) && !(rq.a == oq.a && rq.dense)) return TQ_ERR_INVALID_VALUE;
+  if (Hk > 0) {
+    const Range rk = in(k, k_token_stride, k_head_stride, Hk), ok = in(k_out, static_cast<int64_t>(Hk) * D, D, Hk);
+    if (meets(rk, ok) && !(rk.a == ok.a && rk.dense)) return TQ_ERR_INVALID_VALUE;
+    if (meets(rq, ok) || meets(rk, oq) || meets(oq, ok)) return TQ_ERR_INVALID_VALUE;
+  }
+  return from_cuda(tq::launch_norm_rope({q, k, q_token_stride, q_head_stride, k_token_stride, k_head_stride, q_weight, k_weight,
+                                         positions, turns, axis, q_out, k_out, n, Hq, Hk, D, axes, pairs, paired == 1,
+                                         weight_type == TQ_Q_BF16, eps}, type, stream));
+}
+
+tq_status tq_append_int8(const tq_int8_cache* cache, const void* K, int64_t k_stride, const void* V,
+                         int64_t v_stride, tq_qtype type, const int* starts, const int* lengths, int n,
+                         const int* page_table, int B, int max_pages, cudaStream_t stream) {
+  tq_status st = check_int8(cache, starts, lengths, page_table, n, B, max_pages);
+  if (st != TQ_OK) return st;
+  if (bad_type(type) || bad_stride(k_stride, type) || bad_stride(v_stride, type)) return TQ_ERR_INVALID_VALUE;
+  if (n == 0) return TQ_OK;
+  if ((st = check_ptrs(K, V)) != TQ_OK) return st;
+  return from_cuda(tq::launch_append_int8(*cache, K, k_stride, V, v_stride, type, {starts, lengths, n, B}, page_table,
+                                          max_pages, stream));
+}
+
+tq_status tq_read_int8(const tq_int8_cache* cache, void* K, void* V, tq_qtype type, const int* starts,
+                       const int* lengths, int n, const int* page_table, int B, int max_pages,
+                       cudaStream_t stream) {
+  tq_status st = check_int8(cache, starts, lengths, page_table, n, B, max_pages);
+  if (st != TQ_OK) return st;
+  if (bad_type(type)) return TQ_ERR_INVALID_VALUE;
+  if (n == 0) return TQ_OK;
+  if ((st = check_ptrs(K, V)) != TQ_OK) return st;
+  return from_cuda(tq::launch_read_int8(*cache, K, V, type, {starts, lengths, n, B}, page_table, max_pages, stream));
+}
+
+size_t tq_attend_int8_workspace_bytes(int n, int B, int H, int G, int D) {
+  if (n < 1 || B < 1 || H < 1 || G < 1 || B > kMaxGridYZ || H > kMaxGridYZ || G > kMaxGridYZ || (D != 64 && D != 128)) return 0;
+  return tq::attend_int8_bytes(n, B, H, G, D);
+}
+
+tq_status tq_attend_int8(const tq_int8_cache* cache, const void* Q, tq_qtype type, const int* starts,
+                         const int* lengths, int n, int G, const int* page_table, int B, int max_pages,
+                         int window, int sinks, float scale, void* out, void* workspace,
+                         size_t workspace_bytes, cudaStream_t stream) {
+  tq_status st = check_int8(cache, starts, lengths, page_table, n, B, max_pages);
+  if (st != TQ_OK) return st;
+  if (bad_type(type) || window < 0 || sinks < 0 || !std::isfinite(scale)) return TQ_ERR_INVALID_VALUE;
+  if (G < 1 || G > kMaxGridYZ || static_cast<int64_t>(n) * cache->H * G > INT_MAX) return TQ_ERR_INVALID_VALUE;
+  if (n == 0) return TQ_OK;
+  if ((st = check_ptrs(Q, out)) != TQ_OK) return st;
+  if (workspace == nullptr) return TQ_ERR_WORKSPACE;
+  if (misaligned(workspace)) return TQ_ERR_MISALIGNED;
+  if (workspace_bytes < tq_attend_int8_workspace_bytes(n, B, cache->H, G, cache->D)) return TQ_ERR_WORKSPACE;
+  return from_cuda(tq::launch_attend_int8(*cache, Q, type, {starts, lengths, n, B}, G, page_table, max_pages, window, sinks, scale,
+                                          out, workspace, stream));
 }
 
 tq_status tq_pack_indices(const uint8_t* K_idx, uint8_t* idx_plane, int64_t n_keys, int D,

@@ -1,0 +1,267 @@
+// Rows of the 8-bit paged cache: written (tq_append_int8) and read back (tq_read_int8).
+//
+// A code u of a block of 16 slots stands for (u - 127.5) * 2^e, e one exponent for the block and head.  Written:
+//   e = the least with |x| < 2^(e + 7) for every row of the block that is live, old or new,
+//   u = floor(x * 2^-e) + 128.
+// floor(floor(x) / 2^s) = floor(x / 2^s), so a block whose exponent grows by s has its old codes shifted and
+// holds exactly what it would hold had all its rows come at once: no row is rounded twice, and an error is at
+// most half of the block's present step however the tokens arrived.  (With the nearest code of a scale that
+// follows the largest value, each growth would round the old rows again.)  The power of two costs at most one of
+// the 8 bits; the half step in the middle of a cell is exact in bf16 (an odd number below 256 over two).
+//
+// A warp takes one block of one head's keys or values: its 16 rows lie one instruction's load apart, all in
+// flight at once, so that a unit is one trip to memory for its numbers, one for page and rows, one out.
+// Both directions are bound by memory (2 D (size + 1) bytes a token and head).
+#include "tq_int8.cuh"
+
+namespace tq {
+namespace {
+
+constexpr int kWarps = 4;
+
+// Unit u of a step: a block of 16 slots of one sequence.  Sequence b has at most starts[b + 1] / 16 - starts[b] / 16
+// + 2 blocks, so the units from starts[b] / 16 + 2 b on are its own and no prefix sum is needed: n / 16 + 2 B in all.
+__host__ __device__ __forceinline__ int64_t units_of(const Step& s) { return s.n / kBlockSlots + 2 * static_cast<int64_t>(s.B); }
+
+struct Unit {
+  int b, slot, rows0, rows1, token;   // block from `slot` on; its rows [rows0, rows1) are the step's tokens from `token` on
+  bool old;                           // rows before rows0 are live
+};
+
+// The sequence is looked for by 32 lanes at a time: 2 loads in a row for 1024 sequences.
+__device__ __forceinline__ bool unit_of(const Step& s, int u, int lane, Unit& t) {
+  int lo = 0, hi = s.B;
+  while (hi - lo > 1) {
+    const int stride = (hi - lo + 31) / 32;
+    const int i = lo + lane * stride;
+    const bool below = i < hi && (s.starts[i] >> 4) + 2 * static_cast<int64_t>(i) <= u;
+    const int n = __popc(__ballot_sync(0xffffffffu, below));
+    lo += (n > 0 ? n - 1 : 0) * stride;
+    hi = min(hi, lo + stride);
+  }
+  const Run r = run_of(s, lo);
+  const int64_t k = u - ((r.first >> 4) + 2 * static_cast<int64_t>(lo));
+  if (r.count == 0 || k < 0) return false;
+  const int64_t slot = ((r.len >> 4) + k) << 4;
+  const int64_t first = slot > r.len ? slot : r.len, stop = min(slot + kBlockSlots, static_cast<int64_t>(r.len) + r.count);
+  if (first >= stop) return false;
+  t = {lo, static_cast<int>(slot), static_cast<int>(first - slot), static_cast<int>(stop - slot), r.first + static_cast<int>(first - r.len),
+       slot < r.len};
+  return true;
+}
+
+// Eight values of a row.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<float> {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const float* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); b = __ldg(reinterpret_cast<const uint4*>(p) + 1); }
+  __device__ __forceinline__ void zero() { a = b = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void bits(uint32_t* w) const {
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w; w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+  }
+};
+template <>
+struct Eight<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void bits(uint32_t* w) const {
+    const uint32_t v[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { w[2 * i] = v[i] << 16; w[2 * i + 1] = v[i] & 0xffff0000u; }
+  }
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kWarps * 32)
+append_kernel(const Int8View c, const T* __restrict__ K, int64_t k_stride, const T* __restrict__ V, int64_t v_stride, const Step step) {
+  constexpr int kLanes = D / 8, kAt = 32 / kLanes, kIt = kBlockSlots / kAt;   // lanes a row, rows at a time, times
+  constexpr int kOld = kBlockSlots * D / 512;                                 // 16-byte pieces of the old codes a lane holds
+  const int lane = threadIdx.x & 31;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int of = static_cast<int>(w & 1), h = static_cast<int>((w >> 1) % c.H);
+  const int64_t u = (w >> 1) / c.H;
+  if (u >= units_of(step)) return;
+  Unit t;
+  if (!unit_of(step, static_cast<int>(u), lane, t)) return;
+
+  const int col = lane % kLanes * 8, sub = lane / kLanes;
+  const int64_t stride = of ? v_stride : k_stride;
+  const T* x = (of ? V : K) + t.token * stride + static_cast<int64_t>(h) * D + col;
+  Eight<T> in[kIt];
+#pragma unroll
+  for (int i = 0; i < kIt; ++i) {
+    const int r = i * kAt + sub;
+    if (r >= t.rows0 && r < t.rows1) in[i].load(x + (r - t.rows0) * stride);
+    else in[i].zero();
+  }
+  const int pg = c.page(t.b, t.slot);
+  if (pg < 0) return;
+  const size_t row = c.row(pg, h, t.slot);
+  uint8_t* to = (of ? c.vc : c.kc) + row * D;
+  int8_t* ex = c.ex + row / kBlockSlots * 2 + of;
+  uint4 was[kOld];
+  int e_old = kExpLow;
+  if (t.old) {
+    e_old = min(static_cast<int>(*ex), kExpHigh);
+#pragma unroll
+    for (int i = 0; i < kOld; ++i)
+      if ((i * 512 + lane * 16) / D < t.rows0) was[i] = *reinterpret_cast<const uint4*>(to + i * 512 + lane * 16);
+  }
+
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < kIt; ++i) {
+    uint32_t b[8];
+    in[i].bits(b);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) most = max(most, b[k] & 0x7fffffffu);
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  const bool odd = most >= 0x7f800000u;      // an infinity or NaN: the exponent goes by the finite values
+  if (odd) {
+    most = 0;
+#pragma unroll
+    for (int i = 0; i < kIt; ++i) {
+      uint32_t b[8];
+      in[i].bits(b);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if ((b[k] & 0x7fffffffu) < 0x7f800000u) most = max(most, b[k] & 0x7fffffffu);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+  }
+  int e = min(max(static_cast<int>(most >> 23) - 133, kExpLow), kExpHigh);   // 2^(e + 6) <= most < 2^(e + 7)
+  if (t.old) e = max(e, e_old);
+
+  if (t.old && e > e_old) {
+    // bytes: ((u - 128) >> s) + 128 = (u >> s) + 128 - (128 >> s); beyond 7 every code is next to the middle, as at 7
+    const int s = min(e - e_old, 7);
+    const uint32_t mask = (0xffu >> s) * 0x01010101u, add = (128u - (128u >> s)) * 0x01010101u;
+#pragma unroll
+    for (int i = 0; i < kOld; ++i)
+      if ((i * 512 + lane * 16) / D < t.rows0) {
+        const uint4 v = was[i];
+        *reinterpret_cast<uint4*>(to + i * 512 + lane * 16) = make_uint4((v.x >> s & mask) + add, (v.y >> s & mask) + add,
+                                                                         (v.z >> s & mask) + add, (v.w >> s & mask) + add);
+      }
+  }
+
+  // x * 2^-e, rounded down to a whole number by an addition at 1.5 * 2^23: its low byte is the code
+  const float scale = pow2(-e);
+#pragma unroll
+  for (int i = 0; i < kIt; ++i) {
+    const int r = i * kAt + sub;
+    uint32_t b[8];
+    in[i].bits(b);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float f = __uint_as_float(b[k]);
+      // infinity takes the highest code, minus infinity and NaN the lowest
+      if (odd && (b[k] & 0x7fffffffu) >= 0x7f800000u) f = (b[k] == 0x7f800000u ? 127.0f : -128.0f) * pow2(e);
+      b[k] = __float_as_uint(__fmaf_rd(f, scale, 12582912.0f + 128.0f));
+    }
+    uint2 o;
+    o.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+    o.y = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+    if (r >= t.rows0 && r < t.rows1) *reinterpret_cast<uint2*>(to + r * D + col) = o;
+  }
+  if (lane == 0) *ex = static_cast<int8_t>(e);
+}
+
+__device__ __forceinline__ void put8(float* p, const float* f) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+}
+__device__ __forceinline__ void put8(__nv_bfloat16* p, const float* f) {      // exact: the upper halves
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __byte_perm(__float_as_uint(f[2 * i]), __float_as_uint(f[2 * i + 1]), 0x7632);
+  *reinterpret_cast<uint4*>(p) = make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kWarps * 32)
+read_kernel(const Int8View c, T* __restrict__ K, T* __restrict__ V, const Step step) {
+  constexpr int kLanes = D / 8, kAt = 32 / kLanes, kIt = kBlockSlots / kAt;
+  const int lane = threadIdx.x & 31;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int of = static_cast<int>(w & 1), h = static_cast<int>((w >> 1) % c.H);
+  const int64_t u = (w >> 1) / c.H;
+  if (u >= units_of(step)) return;
+  Unit t;
+  if (!unit_of(step, static_cast<int>(u), lane, t)) return;
+
+  const int col = lane % kLanes * 8, sub = lane / kLanes;
+  const int pg = c.page(t.b, t.slot);
+  uint2 in[kIt];
+  int e = 0;
+  if (pg >= 0) {
+    const size_t row = c.row(pg, h, t.slot);
+    const uint8_t* from = (of ? c.vc : c.kc) + row * D + col;
+    e = c.ex[row / kBlockSlots * 2 + of];
+#pragma unroll
+    for (int i = 0; i < kIt; ++i) {
+      const int r = i * kAt + sub;
+      if (r >= t.rows0 && r < t.rows1) in[i] = *reinterpret_cast<const uint2*>(from + r * D);
+    }
+  }
+  // an exponent outside the range that is written has no power of two in fp32's normal numbers: cut to it
+  const float scale = pg >= 0 ? pow2(min(max(e, kExpLow), kExpHigh)) : 0.0f;
+  T* out = (of ? V : K) + (static_cast<int64_t>(t.token) * c.H + h) * D + col;
+  const int64_t stride = static_cast<int64_t>(c.H) * D;
+#pragma unroll
+  for (int i = 0; i < kIt; ++i) {
+    const int r = i * kAt + sub;
+    if (r >= t.rows0 && r < t.rows1) {
+      float f[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        // the byte below 2^23 is a whole number; u * 2^e - 127.5 * 2^e has one rounding, and none is needed
+        const float whole = __uint_as_float(__byte_perm(k < 4 ? in[i].x : in[i].y, 0x4b000000u, 0x7550 + (k & 3))) - 8388608.0f;
+        f[k] = pg >= 0 ? fmaf(whole, scale, -127.5f * scale) : 0.0f;
+      }
+      put8(out + (r - t.rows0) * stride, f);
+    }
+  }
+}
+
+template <typename T>
+cudaError_t append(const Int8View& v, int D, const void* K, int64_t ks, const void* V, int64_t vs, const Step& s, cudaStream_t st) {
+  const unsigned blocks = static_cast<unsigned>((units_of(s) * v.H * 2 + kWarps - 1) / kWarps);
+  const T* k = static_cast<const T*>(K);
+  const T* x = static_cast<const T*>(V);
+  if (D == 64) append_kernel<T, 64><<<blocks, kWarps * 32, 0, st>>>(v, k, ks, x, vs, s);
+  else append_kernel<T, 128><<<blocks, kWarps * 32, 0, st>>>(v, k, ks, x, vs, s);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t read(const Int8View& v, int D, void* K, void* V, const Step& s, cudaStream_t st) {
+  const unsigned blocks = static_cast<unsigned>((units_of(s) * v.H * 2 + kWarps - 1) / kWarps);
+  if (D == 64) read_kernel<T, 64><<<blocks, kWarps * 32, 0, st>>>(v, static_cast<T*>(K), static_cast<T*>(V), s);
+  else read_kernel<T, 128><<<blocks, kWarps * 32, 0, st>>>(v, static_cast<T*>(K), static_cast<T*>(V), s);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_append_int8(const tq_int8_cache& c, const void* K, int64_t k_stride, const void* V,
+                               int64_t v_stride, tq_qtype type, const Step& step, const int* table, int max_pages,
+                               cudaStream_t st) {
+  const Int8View v = int8_view(c, table, max_pages);
+  return type == TQ_Q_F32 ? append<float>(v, c.D, K, k_stride, V, v_stride, step, st)
+                          : append<__nv_bfloat16>(v, c.D, K, k_stride, V, v_stride, step, st);
+}
+
+cudaError_t launch_read_int8(const tq_int8_cache& c, void* K, void* V, tq_qtype type, const Step& step,
+                             const int* table, int max_pages, cudaStream_t st) {
+  const Int8View v = int8_view(c, table, max_pages);
+  return type == TQ_Q_F32 ? read<float>(v, c.D, K, V, step, st) : read<__nv_bfloat16>(v, c.D, K, V, step, st);
+}
+
+cudaError_t take_faults_int8_rows(unsigned int* bits) { return take_unit_faults(bits); }
+
+}  // namespace tq

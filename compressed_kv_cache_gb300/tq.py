@@ -69,6 +69,12 @@ _SIGNATURES = {
     "tq_decode_paged": ([_P, _P, _I, _P, _P, _I, _I, _I, ctypes.c_float, _P, _I, _P, _P, _Z, _P], _I),
     "tq_evict_paged_workspace_bytes": ([_I, _I, _I, _I], ctypes.c_size_t),
     "tq_evict_paged": ([_P, _P, _P, _P, _I, _I, _P, _P, _I, _I, _I, _P, _P, _P, _Z, _P], _I),
+    "tq_norm_rope": ([_P, _L, _L, _P, _L, _L, _I, _P, _P, _I, ctypes.c_float, _P, _I, _P, _P, _I, _I, _P, _P, _I, _I, _I,
+                      _I, _P], _I),
+    "tq_append_int8": ([_P, _P, _L, _P, _L, _I, _P, _P, _I, _P, _I, _I, _P], _I),
+    "tq_read_int8": ([_P, _P, _P, _I, _P, _P, _I, _P, _I, _I, _P], _I),
+    "tq_attend_int8_workspace_bytes": ([_I, _I, _I, _I, _I], ctypes.c_size_t),
+    "tq_attend_int8": ([_P, _P, _I, _P, _P, _I, _I, _P, _I, _I, _I, _I, ctypes.c_float, _P, _P, _Z, _P], _I),
     "tq_solve_packed_noalloc": ([_P, _I, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P], _I),
 }
 
@@ -680,4 +686,180 @@ def evict_paged(cache: PagedCache, page_table, lengths, seen, mass, positions, b
                 _on(dev, seen, "seen", torch.int32, (B,)), B, M, mp, pp, S, budget, recent,
                 _on(dev, out[0], "mass_out", torch.float32, shape),
                 _on(dev, out[1], "positions_out", torch.int32, shape), wp, wn)
+    return out
+
+
+def _strided(index: int, t: torch.Tensor, name: str, dtype, shape) -> int:
+    """Pointer of a [n, heads, D] tensor whose rows are dense: its type, device and shape are checked."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.stride(2) != 1 and shape[2] > 1:
+        raise ValueError(f"{name} must be dense in its last dimension")
+    return t.data_ptr()
+
+
+_INV_TWO_PI = 0x28BE60DB9391054A7F09D5F47D4D377036D8A5664F10E410      # 1 / (2 pi) * 2^192
+
+
+class Rotary:
+    """The rotation of a model's queries and keys: the handle norm_rope takes, made once.  inv_freq:
+    radians a position of each pair of coordinates (any sequence of floats, a multiple of 4 of
+    them, taken in 64 bits).  axis: which of a token's positions turns each pair (time, height,
+    width; default: the only one).  paired: pairs are coordinates (2i, 2i+1) instead of (i, i +
+    pairs)."""
+
+    __slots__ = ("turns", "axis", "pairs", "axes", "paired", "_index", "_ptrs")
+
+    def __init__(self, inv_freq, device, axis=None, paired=False):
+        import math
+        freq = [float(f) for f in inv_freq]
+        axes = [0] * len(freq) if axis is None else [int(a) for a in axis]
+        if not freq or len(freq) % 4 or len(freq) > 128 or not all(math.isfinite(f) for f in freq):
+            raise ValueError("inv_freq must hold a multiple of 4 finite numbers, 128 at most")
+        if len(axes) != len(freq) or min(axes) < 0 or max(axes) > 7:
+            raise ValueError("axis must name one of up to 8 positions for each frequency")
+        ratios = [f.as_integer_ratio() for f in freq]
+        bits = [(a * _INV_TWO_PI // b >> 128) & 0xffffffffffffffff for a, b in ratios]      # of 2^64 a turn
+        self.turns = torch.tensor([b - (1 << 64) if b >> 63 else b for b in bits], dtype=torch.int64).to(device)
+        self.axis = torch.tensor(axes, dtype=torch.uint8).to(device)
+        self.pairs, self.axes, self.paired, self._index = len(freq), max(axes) + 1, bool(paired), self.turns.get_device()
+        self._ptrs = _dev(self.turns, "turns", (torch.int64,)), _dev(self.axis, "axis", (torch.uint8,))
+
+
+def norm_rope(q, k, positions, rotary: Rotary, q_weight=None, k_weight=None, eps=1e-6, out=None):
+    """Root-mean-square norm of every head of q [n,Hq,D] and k [n,Hk,D] (fp32/bf16, dense in their last
+    dimension, as parts of a joint projection are; k may be None), times q_weight and k_weight [D]
+    (fp32/bf16; None: no norm), then rotated by positions int32 [n] or [n,axes].  Returns dense (q, k)
+    of the same type; `out`: a pair to write to, which may be q and k themselves where these are dense."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.dtype not in QTYPE:
+        raise ValueError("q must be a [n, heads, D] fp32 or bf16 tensor")
+    dev, dtype = rotary._index, q.dtype
+    n, Hq, D = q.shape
+    if not isinstance(positions, torch.Tensor) or positions.dim() not in (1, 2):
+        raise ValueError("positions must be a [n] or [n, axes] tensor")
+    axes = 1 if positions.dim() == 1 else positions.shape[1]
+    if axes < rotary.axes:
+        raise ValueError(f"positions have {axes} axes, the rotation takes {rotary.axes}")
+    qp, Hk, kp, ks = _strided(dev, q, "q", dtype, (n, Hq, D)), 0, None, (0, 0)
+    if k is not None:
+        if not isinstance(k, torch.Tensor) or k.dim() != 3:
+            raise ValueError("k must be a [n, heads, D] tensor or None")
+        Hk = k.shape[1]
+        kp, ks = _strided(dev, k, "k", dtype, (n, Hk, D)), k.stride()
+    weights, wtype = [], None
+    for t, name in ((q_weight, "q_weight"), (k_weight if Hk else None, "k_weight")):
+        if t is not None:
+            if t.dtype not in QTYPE or wtype not in (None, t.dtype):
+                raise TypeError("q_weight and k_weight must be fp32 or bf16, both alike")
+            wtype = t.dtype
+        weights.append(None if t is None else _on(dev, t, name, t.dtype, (D,)))
+    if out is None:
+        out = (torch.empty((n, Hq, D), device=q.device, dtype=dtype),
+               None if k is None else torch.empty((n, Hk, D), device=q.device, dtype=dtype))
+    qs = q.stride()
+    _paged_call("tq_norm_rope", dev, qp, qs[0], qs[1], kp, ks[0], ks[1], QTYPE[dtype], weights[0], weights[1], QTYPE.get(wtype, 0),
+                eps, _on(dev, positions, "positions", torch.int32, (n,) if positions.dim() == 1 else (n, axes)), axes,
+                rotary._ptrs[0], rotary._ptrs[1], rotary.pairs, 1 if rotary.paired else 0,
+                _on(dev, out[0], "q_out", dtype, (n, Hq, D)),
+                None if k is None else _on(dev, out[1], "k_out", dtype, (n, Hk, D)), n, Hq, Hk, D)
+    return out
+
+
+class _Int8CacheStruct(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("k_codes", "v_codes", "exponents")] + [(n, _I) for n in ("n_pages", "H", "page_size", "D")]
+
+
+class Int8Cache:
+    """A paged cache of keys and values in 8 bits with an exponent for each 16 slots of a head: the handle
+    the int8 calls take, made once per layer.  k_codes, v_codes uint8 [N,H,page,D], exponents int8
+    [N,H,page/16,2]; D 64 or 128, page a power of two from 16 to 256.  Fresh pages need no
+    initial values.  The tensors stay the caller's, as for PagedCache.
+
+    The calls share a step's form: tokens one behind the other, those of sequence b from starts[b] to
+    starts[b+1] (int32 [B+1]), at its slots from lengths[b] (int32 [B], slots in use before the step) on."""
+
+    __slots__ = ("k_codes", "v_codes", "exponents", "device", "H", "page_size", "D", "_struct", "_ref", "_index")
+
+    def __init__(self, k_codes, v_codes, exponents):
+        ptrs = [_dev(t, n, (d,)) for t, n, d in ((k_codes, "k_codes", torch.uint8), (v_codes, "v_codes", torch.uint8),
+                                                 (exponents, "exponents", torch.int8))]
+        if k_codes.device != v_codes.device or k_codes.device != exponents.device:
+            raise ValueError("the tensors of a cache must be on one device")
+        if k_codes.dim() != 4 or v_codes.shape != k_codes.shape:
+            raise ValueError("k_codes and v_codes must be [pages, H, page, D]")
+        N, H, page, D = k_codes.shape
+        if tuple(exponents.shape) != (N, H, page // 16, 2):
+            raise ValueError("exponents must be [pages, H, page / 16, 2]")
+        self.k_codes, self.v_codes, self.exponents = k_codes, v_codes, exponents
+        self.device, self.H, self.page_size, self.D = k_codes.device, H, page, D
+        self._struct = _Int8CacheStruct(*ptrs, N, H, page, D)
+        self._ref, self._index = ctypes.addressof(self._struct), k_codes.get_device()
+
+
+def _step(index: int, starts, lengths, B: int) -> tuple[int, int]:
+    return _on(index, starts, "starts", torch.int32, (B + 1,)), _on(index, lengths, "lengths", torch.int32, (B,))
+
+
+def append_int8(K, V, starts, cache: Int8Cache, page_table, lengths) -> None:
+    """Writes a step's keys and values to their slots.  K, V [n,H,D] fp32/bf16, heads dense, tokens at any
+    stride (parts of a joint projection); page_table int32 [B,max_pages].  The codes do not depend on
+    how a sequence's tokens are cut into steps."""
+    if not isinstance(K, torch.Tensor) or K.dim() != 3 or K.dtype not in QTYPE:
+        raise ValueError("K must be a [n, H, D] fp32 or bf16 tensor")
+    dev, H, D, n = cache._index, cache.H, cache.D, K.shape[0]
+    tp, B, M = _table(dev, page_table)
+    ptrs = []
+    for t, name in ((K, "K"), (V, "V")):
+        ptrs += [_strided(dev, t, name, K.dtype, (n, H, D)), t.stride(0)]
+        if H > 1 and t.stride(1) != D:
+            raise ValueError(f"the heads of {name} must be dense")
+    _paged_call("tq_append_int8", dev, cache._ref, *ptrs, QTYPE[K.dtype], *_step(dev, starts, lengths, B), n, tp, B, M)
+
+
+def read_int8(cache: Int8Cache, page_table, starts, lengths, n: int, dtype=torch.bfloat16, out=None):
+    """The values of n slots, keys and values [n,H,D] (exact in fp32 and bf16): those of sequence b from slot
+    lengths[b] on in rows starts[b] to starts[b+1].  `out`: a pair to write to, whose other rows stay."""
+    if dtype not in QTYPE:
+        raise ValueError("dtype must be fp32 or bf16")
+    dev, shape = cache._index, (int(n), cache.H, cache.D)
+    tp, B, M = _table(dev, page_table)
+    if out is None:
+        out = tuple(torch.empty(shape, device=cache.device, dtype=dtype) for _ in range(2))
+    _paged_call("tq_read_int8", dev, cache._ref, _on(dev, out[0], "K", dtype, shape), _on(dev, out[1], "V", dtype, shape),
+                QTYPE[dtype], *_step(dev, starts, lengths, B), shape[0], tp, B, M)
+    return out
+
+
+def attend_int8_workspace_bytes(n: int, B: int, H: int, G: int, D: int) -> int:
+    return int(lib().tq_attend_int8_workspace_bytes(n, B, H, G, D))
+
+
+def attend_int8(Q, starts, cache: Int8Cache, page_table, lengths, window=None, sinks=0, scale=None, workspace=None, out=None):
+    """Attention of a step's tokens over the cache, up to their own slots (append_int8 first).  Q [n,H*G,D]
+    fp32/bf16 (query head i reads KV head i // G).  window: how many slots up to its own a token sees
+    (None: all), besides the first `sinks` of its sequence.  scale defaults to 1/sqrt(D).  Returns Q's
+    shape and type; `out`: a tensor to write to, whose rows behind the last sequence's stay."""
+    if not isinstance(Q, torch.Tensor) or Q.dim() != 3 or Q.dtype not in QTYPE:
+        raise ValueError("Q must be a [n, heads, D] fp32 or bf16 tensor")
+    dev, H, D, dtype = cache._index, cache.H, cache.D, Q.dtype
+    tp, B, M = _table(dev, page_table)
+    n, heads = Q.shape[0], Q.shape[1]
+    if heads < H or heads % H:
+        raise ValueError(f"{heads} query heads over {H} KV heads")
+    if window is not None and not 0 < window < 2 ** 31 or not 0 <= sinks < 2 ** 31:
+        raise ValueError("window must be positive or None, sinks not negative, both below 2^31")
+    G, shape = heads // H, (n, heads, D)
+    qp = _on(dev, Q, "Q", dtype, shape)
+    wp, wn = _workspace_of(dev, workspace, 0 if workspace is not None else attend_int8_workspace_bytes(n, B, H, G, D))
+    if out is None:
+        out = torch.empty_like(Q)
+    _paged_call("tq_attend_int8", dev, cache._ref, qp, QTYPE[dtype], *_step(dev, starts, lengths, B), n, G, tp, B, M,
+                0 if window is None else window, sinks, 1.0 / D ** 0.5 if scale is None else float(scale),
+                _on(dev, out, "out", dtype, shape), wp, wn)
     return out

@@ -84,7 +84,7 @@ tq_path tq_auto_path(int B, int D);
  * tq_device_faults ORs into *bits the fault bits set on the CURRENT device since the
  * last call and clears them: 1 = fp32 lookup-table scorers, 2 = tensor-core scorer,
  * 4 = fused decode, 8 = compressor, 16 = tq_check_wait_expiry, 32 = a paged call met a
- * length, slot or page number out of range (see the paged cache below), 64 = a wait of
+ * length, slot or page number out of range (see the paged caches below), 64 = a wait of
  * tq_append_paged ran out (not all of its rows are written).  It synchronises with the device (it reads device memory) and is not for use inside stream capture.
  * bits: host pointer, not NULL.
  * Errors: TQ_ERR_INVALID_VALUE (bits NULL), TQ_ERR_LAUNCH (the device read failed). */
@@ -372,6 +372,110 @@ tq_status tq_evict_paged(const tq_paged_cache* cache, const int* page_table, con
                          const int* positions, int S, int budget, int recent, float* mass_out,
                          int* positions_out, void* workspace, size_t workspace_bytes,
                          cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Norms of queries and keys by head, and the rotation by their positions, in one pass (what
+ * comes before a cache is written or read; this library's own, without a counterpart in the
+ * pages).  For every head of every token
+ *   y = x / sqrt(mean(x^2) + eps) * weight                       (weight NULL: y = x)
+ *   out_a = y_a cos t - y_b sin t,  out_b = y_b cos t + y_a sin t   for each pair (a, b)
+ * with t = positions[token, axis[i]] * frequency_i of pair i.  Pairs: (i, i + pairs), or (2i, 2i + 1)
+ * where `paired` is 1; coordinates from 2 * pairs on are not turned.
+ *
+ * q, k: heads of n tokens of `type`, element (token, head, d) at token * token_stride + head *
+ * head_stride + d (strides in elements, multiples of 16 bytes, so that both may be parts of one
+ * projection); k may be NULL with Hk = 0.  q_weight, k_weight: [D] of weight_type, or NULL.
+ * positions: [n, axes] int32, negative ones too.  turns: [pairs] uint64, frequency / (2 pi) as a
+ * fraction of a turn times 2^64, whole turns dropped; axis: [pairs] uint8 below axes.
+ * q_out, k_out: [n, Hq, D] and [n, Hk, D] dense.  q_out may be q itself where q is dense, k_out
+ * likewise; else no output may overlap an input or the other output.
+ * D a multiple of 8, 8 <= D <= 256; pairs a multiple of 4, 4 <= pairs <= D / 2; 1 <= axes <= 8; eps >= 0.
+ * fp32 arithmetic, rounded once; the angle keeps 2^-32 of a turn at every position.
+ * Errors: TQ_ERR_INVALID_VALUE, TQ_ERR_MISALIGNED, TQ_ERR_UNSUPPORTED (D or pairs), TQ_ERR_LAUNCH.
+ * ---------------------------------------------------------------------- */
+tq_status tq_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                       int64_t k_token_stride, int64_t k_head_stride, tq_qtype type,
+                       const void* q_weight, const void* k_weight, tq_qtype weight_type, float eps,
+                       const int* positions, int axes, const uint64_t* turns, const uint8_t* axis,
+                       int pairs, int paired, void* q_out, void* k_out, int n, int Hq, int Hk, int D,
+                       cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Paged cache of keys and values in 8 bits, with a power of two for each 16 slots of a head
+ * (this library's own, without a counterpart in the pages): the tier above the paged cache of
+ * MSE rows, for layers whose keys do not bear 4 bits.
+ *
+ * The cache is n_pages pages of page_size rows for each of H KV heads:
+ *   k_codes, v_codes [n_pages, H, page_size, D] uint8, exponents [n_pages, H, page_size/16, 2]
+ *   int8 (key's, value's).  Code u of a block with exponent e stands for (u - 127.5) * 2^e.
+ * The struct lives in HOST memory and is read during the call only.
+ *
+ * A step: n tokens, those of sequence b being starts[b] .. starts[b + 1] - 1 (starts: [B + 1] int32,
+ * ascending; any number of them, none too), at slots lengths[b] on (lengths: [B] int32, slots in
+ * use before the step).  The three calls of a step take the same starts and lengths; the caller
+ * adds the counts to lengths once every layer is done.  Tokens from starts[B] on are
+ * padding: nothing of them is read, and their rows of the outputs are left as they were.
+ * page_table [B, max_pages] int32: slot s of sequence b is row s % page_size of page
+ * page_table[b, s / page_size].  Only entries of slots that a call writes or sees are read: pages
+ * that a window has left behind may go back to the pool.
+ * A sequence whose starts descend or leave [0, n], or whose length is negative, has no tokens; a
+ * slot beyond max_pages * page_size or on a page outside [0, n_pages) is absent.  Each sets
+ * fault bit 32 (tq_device_faults) where it is met, and nothing out of range is read or written.
+ *
+ * D is 64 or 128, page_size in {16,32,64,128,256}, 1 <= H <= 65535, 1 <= B <= 65535, B * H <=
+ * 2^24, n * H below 2^31.  n = 0 does nothing.  Errors of the calls: TQ_ERR_INVALID_VALUE (null pointer, size out of
+ * range), TQ_ERR_MISALIGNED, TQ_ERR_UNSUPPORTED (D or page_size), TQ_ERR_WORKSPACE, TQ_ERR_LAUNCH.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  int8_t* exponents;
+  int n_pages, H, page_size, D;
+} tq_int8_cache;
+
+/* ------------------------------------------------------------------------
+ * The write side.  K, V: [n, H, D] of `type`, token i at i * stride elements, its heads dense
+ * (strides in elements, multiples of 16 bytes).  For every block of 16 slots that gets rows
+ *   e = the least in [-120, 121] with |x| < 2^(e + 7) for all rows of the block and head that are
+ *       live: the step's, and those below lengths[b],
+ *   u = floor(x * 2^-e) + 128.
+ * Where old rows need it (e grew by s) their codes become floor((u - 128) / 2^s) + 128, which is what
+ * they had been with that exponent from the start: codes do not depend on how tokens arrived.
+ * (An exponent does not fall while its block holds live rows; rows cut off by a smaller
+ * `lengths` may have raised it.)  An infinity takes the code at its end, a NaN code 0; neither raises the
+ * exponent.  Two sequences must not write to one page (the caller's contract).
+ * ---------------------------------------------------------------------- */
+tq_status tq_append_int8(const tq_int8_cache* cache, const void* K, int64_t k_stride, const void* V,
+                         int64_t v_stride, tq_qtype type, const int* starts, const int* lengths, int n,
+                         const int* page_table, int B, int max_pages, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Reading back: K, V [n, H, D] of `type`, token i's row is the value of its slot, exact in
+ * either type.  With the starts and lengths of an append it gives what that append wrote;
+ * any other run of slots may be asked for.  Rows of absent slots are zeros.
+ * ---------------------------------------------------------------------- */
+tq_status tq_read_int8(const tq_int8_cache* cache, void* K, void* V, tq_qtype type, const int* starts,
+                       const int* lengths, int n, const int* page_table, int B, int max_pages,
+                       cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Attention of the step's tokens (one of each sequence, a few drafted ones, or a piece of a
+ * prompt) over the cache, their own rows included.  Token i of sequence b, at slot
+ * t = lengths[b] + i - starts[b], sees slots s <= t with s > t - window or s < sinks (window 0:
+ * all of them):
+ *   z[s] = scale <q, k_s>,  p = softmax(z),  out = sum_s p[s] v_s    (zeros if it sees no slot)
+ * Q: [n, H*G, D] of `type`, query head h*G + g reads KV head h.  out: the same shape and type.
+ * fp32 queries: fp32 accuracy throughout.  bf16 queries: logits to fp32 accuracy, weights rounded
+ * to fp16 (2^-12 at most) before the sum of values, sums in fp32, the output rounded to bf16.
+ * The same inputs give the same bits.  Sequences may share pages.  scale: finite.
+ * workspace: at least tq_attend_int8_workspace_bytes(n, B, H, G, D) bytes, scratch, not
+ * shared by concurrent calls or by graphs that may run concurrently.
+ * ---------------------------------------------------------------------- */
+size_t tq_attend_int8_workspace_bytes(int n, int B, int H, int G, int D);
+tq_status tq_attend_int8(const tq_int8_cache* cache, const void* Q, tq_qtype type, const int* starts,
+                         const int* lengths, int n, int G, const int* page_table, int B, int max_pages,
+                         int window, int sinks, float scale, void* out, void* workspace,
+                         size_t workspace_bytes, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------
  * Fused query transform + scoring: the challenge's `solve` without its
