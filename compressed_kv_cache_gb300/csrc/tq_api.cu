@@ -136,6 +136,7 @@ tq_status check_int8(const tq_int8_cache* c, const int* starts, const int* lengt
   if (c->D != 64 && c->D != 128) return TQ_ERR_UNSUPPORTED;
   const int ps = c->page_size;
   if (ps < 16 || ps > 256 || (ps & (ps - 1)) != 0) return TQ_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(c->n_pages) * c->H * (ps / 16) > INT_MAX) return TQ_ERR_INVALID_VALUE;   // blocks in 32 bits
   if (B < 1 || B > kMaxGridYZ || max_pages < 1 || max_pages > (INT_MAX - 4096) / ps) return TQ_ERR_INVALID_VALUE;
   if (n < 0 || static_cast<int64_t>(n) * c->H > INT_MAX || static_cast<int64_t>(B) * c->H > kMaxPagedQueries)
     return TQ_ERR_INVALID_VALUE;

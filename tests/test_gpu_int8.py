@@ -4,8 +4,9 @@ Codes, exponents and values read back are exact.  norm_rope: a coordinate is off
 |y_a| + |y_b| (angle to fp32: pi * 2^-24, sine and cosine one step each, 2^-23; the norm 16 roundings of 2^-24, the
 rotation's products and sum 4), and half a step of the result's type.  attend: logits to 2^-17 of
 scale sum |q_d k_d| (queries as two fp16 parts, 2^-22; 16 additions of a product's parts, each to 2^-22 of what is
-summed; exp2 and the scale's product 2^-22 more), weights of bf16 queries rounded to fp16 (2^-11, at most 2^-25 of the
-largest below its normal numbers), sums of values to 2^-14 (bf16) or 2^-17 (fp32), the output to half a step."""
+summed; exp2 and the scale's product 2^-22 more), weights rounded to fp16 (bf16 queries: one part, 2^-11; fp32: two, 2^-22), sums of values to 2^-14 (bf16) or
+2^-17 (fp32), the output to half a step.  Weights are taken 2^7 above the largest's 1, so that the rounding of small ones,
+2^-25 below fp16's normal numbers, is 2^-32 of the largest."""
 import numpy as np
 import pytest
 
@@ -78,7 +79,7 @@ class Setup:
 
 def bounds(dtype):
     """logit, value, least of a definition's bound"""
-    return (2.0 ** -17, 2.0 ** -11 + 2.0 ** -14, 2.0 ** -25) if dtype is BF16 else (2.0 ** -17, 2.0 ** -17, 2.0 ** -40)
+    return (2.0 ** -17, 2.0 ** -11 + 2.0 ** -14, 2.0 ** -32) if dtype is BF16 else (2.0 ** -17, 2.0 ** -17, 2.0 ** -32)
 
 
 def check_attend(tq, s, G=4, window=0, sinks=0, scale=None, size=1.0, Q=None, faults=0):
