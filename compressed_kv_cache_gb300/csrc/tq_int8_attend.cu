@@ -10,68 +10,124 @@ namespace {
 constexpr int kJoinWarps = 8;
 constexpr float kLifted = 7.0f;      // weights were taken 2^7 above their range
 
-
-// Block (i, k) takes columns 8 k .. 8 k + 7 of the unit that block i of the split starts in the middle of, if that is the
-// first start inside it: parts (i - 1, 1), (i, 0), (i + 1, 0) and on.  A warp takes a column, a lane its D / 32
-// dimensions; the factors of 32 parts are made by 32 lanes.
+// Block i of the split that starts in the middle of a unit, as the first to do so, names a unit to be joined: its parts are
+// (i - 1, 1), (i, 0), (i + 1, 0) and on.  Every block of the join lists these units and takes its share of their
+// columns.  Many columns: a warp each.  Few (one long sequence): a block each, its warps taking every eighth part, so
+// that all parts are on their way at once.  A lane holds D / 32 dimensions.
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const AttendArgs a, int NC) {
+__global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const AttendArgs a, int NC, int ctas) {
   constexpr int kDims = D / 32;
+  __shared__ int starts[kAttendCtas];
+  __shared__ int warp_count[kJoinWarps];
+  __shared__ float4 warp_top[kJoinWarps];
+  __shared__ float warp_acc[kJoinWarps][D];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const AttendRecord r = a.rec[blockIdx.x];
-  if (r.off == 0 || r.off > r.chunk) return;
-  const int lane = threadIdx.x & 31, col = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
-  const int64_t cc = static_cast<int64_t>(r.cb) * NC + col;
-  if (cc >= static_cast<int64_t>(r.count) * a.G) return;
-  const int pieces = 1 + static_cast<int>((r.quads - r.off + r.chunk - 1) / r.chunk);
-  auto place = [&](int p) {
-    return (static_cast<size_t>(p == 0 ? blockIdx.x - 1 : blockIdx.x + p - 1) * 2 + (p == 0 ? 1 : 0)) * NC + col;
-  };
-  float mt = -3.4e38f, Mt = -3.4e38f;
-  for (int p = lane; p < pieces; p += 32) {
-    const float4 v = a.top[place(p)];
-    mt = fmaxf(mt, v.x);
-    Mt = fmaxf(Mt, v.y);
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
-    Mt = fmaxf(Mt, __shfl_xor_sync(0xffffffffu, Mt, o));
-  }
-  float l = 0.0f, acc[kDims];
-#pragma unroll
-  for (int d = 0; d < kDims; ++d) acc[d] = 0.0f;
-  for (int p0 = 0; p0 < pieces; p0 += 32) {
-    float f = 0.0f;
-    if (p0 + lane < pieces) {
-      const float4 v = a.top[place(p0 + lane)];
-      l = fmaf(v.z, exp2f(v.x - mt), l);
-      f = exp2f(v.y - Mt);
+  int units = 0;
+  for (int i0 = 0; i0 < ctas; i0 += kJoinWarps * 32) {
+    bool first = false;
+    if (i0 + tid < ctas) {
+      const int4 r = *reinterpret_cast<const int4*>(a.rec + i0 + tid);      // chunk, off
+      first = r.y > 0 && r.y <= r.x;
     }
-    const int n = min(32, pieces - p0);
-#pragma unroll 8
-    for (int p = 0; p < n; ++p) {
-      const float g = __shfl_sync(0xffffffffu, f, p);
-      const float* from = a.part + place(p0 + p) * D + lane * kDims;
-      if constexpr (kDims == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(from);
-        acc[0] = fmaf(v.x, g, acc[0]); acc[1] = fmaf(v.y, g, acc[1]); acc[2] = fmaf(v.z, g, acc[2]); acc[3] = fmaf(v.w, g, acc[3]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(from);
-        acc[0] = fmaf(v.x, g, acc[0]); acc[1] = fmaf(v.y, g, acc[1]);
+    const uint32_t hit = __ballot_sync(0xffffffffu, first);
+    if (lane == 0) warp_count[warp] = __popc(hit);
+    __syncthreads();
+    int at = units + __popc(hit & ((1u << lane) - 1));
+    for (int w = 0; w < kJoinWarps; ++w) {
+      if (w < warp) at += warp_count[w];
+      units += warp_count[w];
+    }
+    if (first) starts[at] = i0 + tid;
+    __syncthreads();
+  }
+  const int items = units * NC;
+  const bool shared = items < static_cast<int>(gridDim.x) * 2;      // a block an item
+  const int step = shared ? kJoinWarps : 1, w0 = shared ? warp : 0;
+  for (int item = shared ? blockIdx.x : blockIdx.x * kJoinWarps + warp; item < items; item += gridDim.x * (shared ? 1 : kJoinWarps)) {
+    const int i = starts[item / NC], col = item % NC;
+    const AttendRecord r = a.rec[i];
+    const int64_t cc = static_cast<int64_t>(r.cb) * NC + col;
+    if (cc >= static_cast<int64_t>(r.count) * a.G) continue;
+    const int pieces = 1 + (r.quads - r.off + r.chunk - 1) / r.chunk;
+    float mt = -3.4e38f, Mt = -3.4e38f, l = 0.0f, acc[kDims];
+#pragma unroll
+    for (int d = 0; d < kDims; ++d) acc[d] = 0.0f;
+    constexpr int kAhead = 4;
+    for (int p0 = w0; p0 < pieces; p0 += kAhead * step) {
+      float4 top[kAhead], v[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int p = p0 + k * step;
+        top[k] = make_float4(-3.4e38f, -3.4e38f, 0.0f, 0.0f);
+        v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (p < pieces) {
+          const size_t place = (static_cast<size_t>(p == 0 ? i - 1 : i + p - 1) * 2 + (p == 0 ? 1 : 0)) * NC + col;
+          top[k] = a.top[place];
+          const float* from = a.part + place * D + lane * kDims;
+          if constexpr (kDims == 4) v[k] = *reinterpret_cast<const float4*>(from);
+          else {
+            const float2 u = *reinterpret_cast<const float2*>(from);
+            v[k].x = u.x;
+            v[k].y = u.y;
+          }
+        }
+      }
+      float m1 = mt, M1 = Mt;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        m1 = fmaxf(m1, top[k].x);
+        M1 = fmaxf(M1, top[k].y);
+      }
+      l *= exp2f(mt - m1);
+      const float back = exp2f(Mt - M1);
+#pragma unroll
+      for (int d = 0; d < kDims; ++d) acc[d] *= back;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        l = fmaf(top[k].z, exp2f(top[k].x - m1), l);
+        const float f = exp2f(top[k].y - M1);
+        acc[0] = fmaf(v[k].x, f, acc[0]);
+        acc[1] = fmaf(v[k].y, f, acc[1]);
+        if constexpr (kDims == 4) {
+          acc[2] = fmaf(v[k].z, f, acc[2]);
+          acc[3] = fmaf(v[k].w, f, acc[3]);
+        }
+      }
+      mt = m1;
+      Mt = M1;
+    }
+    if (shared) {
+      __syncthreads();      // the last item's sums have been read
+      if (lane == 0) warp_top[warp] = make_float4(mt, Mt, l, 0.0f);
+#pragma unroll
+      for (int d = 0; d < kDims; ++d) warp_acc[warp][lane * kDims + d] = acc[d];
+      __syncthreads();
+      if (warp != 0) continue;
+      mt = Mt = -3.4e38f;
+      for (int w = 0; w < kJoinWarps; ++w) {
+        mt = fmaxf(mt, warp_top[w].x);
+        Mt = fmaxf(Mt, warp_top[w].y);
+      }
+      l = 0.0f;
+#pragma unroll
+      for (int d = 0; d < kDims; ++d) acc[d] = 0.0f;
+      for (int w = 0; w < kJoinWarps; ++w) {
+        l = fmaf(warp_top[w].z, exp2f(warp_top[w].x - mt), l);
+        const float f = exp2f(warp_top[w].y - Mt);
+#pragma unroll
+        for (int d = 0; d < kDims; ++d) acc[d] = fmaf(warp_acc[w][lane * kDims + d], f, acc[d]);
       }
     }
-  }
+    const float f = 1.0f / l, up = exp2f(Mt - mt - kLifted);
+    const int token = static_cast<int>(cc / a.G), head = static_cast<int>(cc - static_cast<int64_t>(token) * a.G);
+    T* to = static_cast<T*>(a.out) + ((static_cast<size_t>(r.first) + token) * a.c.H * a.G + static_cast<size_t>(r.h) * a.G + head) * D + lane * kDims;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  const float f = 1.0f / l, up = exp2f(Mt - mt - kLifted);
-  const int token = static_cast<int>(cc / a.G), head = static_cast<int>(cc - static_cast<int64_t>(token) * a.G);
-  T* to = static_cast<T*>(a.out) + ((static_cast<size_t>(r.first) + token) * a.c.H * a.G + static_cast<size_t>(r.h) * a.G + head) * D + lane * kDims;
-#pragma unroll
-  for (int d = 0; d < kDims; ++d) {
-    const float v = l == 0.0f ? 0.0f : acc[d] * f * up;
-    if constexpr (sizeof(T) == 4) to[d] = v;
-    else to[d] = __float2bfloat16_rn(v);
+    for (int d = 0; d < kDims; ++d) {
+      const float v = l == 0.0f ? 0.0f : acc[d] * f * up;
+      if constexpr (sizeof(T) == 4) to[d] = v;
+      else to[d] = __float2bfloat16_rn(v);
+    }
   }
 }
 
@@ -110,8 +166,8 @@ cudaError_t launch_attend_int8(const tq_int8_cache& c, const void* Q, tq_qtype t
     if (e != cudaSuccess) return e;
     sms_cache[dev & 63].store(sms, std::memory_order_relaxed);
   }
-  const int ctas = 2 * sms < kAttendCtas ? 2 * sms : kAttendCtas;
-  const int nt = column_tiles(step.n, step.B, G);
+  const int nt = column_tiles(step.n, step.B, G), blocks = attend_blocks(type == TQ_Q_F32, c.D, nt);
+  const int ctas = blocks * sms < kAttendCtas ? blocks * sms : kAttendCtas;
   const Space sp(nt, c.D);
   char* w = static_cast<char*>(ws);
   const AttendArgs a = {int8_view(c, table, max_pages), step, Q, out, G, window, sinks, scale * 1.4426950408889634f,
@@ -128,13 +184,13 @@ cudaError_t launch_attend_int8(const tq_int8_cache& c, const void* Q, tq_qtype t
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3(ctas, nt);
+  cfg.gridDim = dim3(2 * sms);
   cfg.blockDim = dim3(kJoinWarps * 32);
   if (c.D == 64)
-    return f32 ? cudaLaunchKernelEx(&cfg, attend_join_kernel<float, 64>, a, 8 * nt)
-               : cudaLaunchKernelEx(&cfg, attend_join_kernel<__nv_bfloat16, 64>, a, 8 * nt);
-  return f32 ? cudaLaunchKernelEx(&cfg, attend_join_kernel<float, 128>, a, 8 * nt)
-             : cudaLaunchKernelEx(&cfg, attend_join_kernel<__nv_bfloat16, 128>, a, 8 * nt);
+    return f32 ? cudaLaunchKernelEx(&cfg, attend_join_kernel<float, 64>, a, 8 * nt, ctas)
+               : cudaLaunchKernelEx(&cfg, attend_join_kernel<__nv_bfloat16, 64>, a, 8 * nt, ctas);
+  return f32 ? cudaLaunchKernelEx(&cfg, attend_join_kernel<float, 128>, a, 8 * nt, ctas)
+             : cudaLaunchKernelEx(&cfg, attend_join_kernel<__nv_bfloat16, 128>, a, 8 * nt, ctas);
 }
 
 cudaError_t take_faults_int8_attend(unsigned int* bits) {

@@ -50,34 +50,44 @@ __device__ __forceinline__ bool unit_of(const Step& s, int u, int lane, Unit& t)
   return true;
 }
 
-// Eight values of a row.
+// Sixteen bytes of a row: 8 values of bf16 or 4 of fp32, so that a warp's accesses are whole lines of either.
 template <typename T>
-struct Eight;
+struct Piece;
 template <>
-struct Eight<float> {
-  uint4 a, b;
-  __device__ __forceinline__ void load(const float* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); b = __ldg(reinterpret_cast<const uint4*>(p) + 1); }
-  __device__ __forceinline__ void zero() { a = b = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ __forceinline__ void bits(uint32_t* w) const {
-    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w; w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+struct Piece<float> {
+  static constexpr int kN = 4;
+  uint4 a;
+  // the largest |x| as bits of fp32; above 0x7f800000 or at it where one is not finite
+  __device__ __forceinline__ uint32_t most() const {
+    const uint32_t m = 0x7fffffffu;
+    return max(max(a.x & m, a.y & m), max(a.z & m, a.w & m));
   }
+  __device__ __forceinline__ void bits(uint32_t* w) const { w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w; }
+  __device__ __forceinline__ void set(const uint32_t* w) { a = make_uint4(w[0], w[1], w[2], w[3]); }
 };
 template <>
-struct Eight<__nv_bfloat16> {
+struct Piece<__nv_bfloat16> {
+  static constexpr int kN = 8;
   uint4 a;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ uint32_t most() const {
+    const uint32_t m = 0x7fff7fffu;
+    const uint32_t v = __vmaxu2(__vmaxu2(a.x & m, a.y & m), __vmaxu2(a.z & m, a.w & m));
+    return max(v << 16, v & 0xffff0000u);
+  }
   __device__ __forceinline__ void bits(uint32_t* w) const {
     const uint32_t v[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) { w[2 * i] = v[i] << 16; w[2 * i + 1] = v[i] & 0xffff0000u; }
   }
+  __device__ __forceinline__ void set(const uint32_t* w) {
+    a = make_uint4(__byte_perm(w[0], w[1], 0x7632), __byte_perm(w[2], w[3], 0x7632), __byte_perm(w[4], w[5], 0x7632), __byte_perm(w[6], w[7], 0x7632));
+  }
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 4 ? 4 : 6)
 append_kernel(const Int8View c, const T* __restrict__ K, int64_t k_stride, const T* __restrict__ V, int64_t v_stride, const Step step) {
-  constexpr int kLanes = D / 8, kAt = 32 / kLanes, kIt = kBlockSlots / kAt;   // lanes a row, rows at a time, times
+  constexpr int kN = Piece<T>::kN, kLanes = D / kN, kAt = 32 / kLanes, kIt = kBlockSlots / kAt;   // lanes a row, rows at a time, times
   constexpr int kOld = kBlockSlots * D / 512;                                 // 16-byte pieces of the old codes a lane holds
   const int lane = threadIdx.x & 31;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
@@ -87,15 +97,14 @@ append_kernel(const Int8View c, const T* __restrict__ K, int64_t k_stride, const
   Unit t;
   if (!unit_of(step, static_cast<int>(u), lane, t)) return;
 
-  const int col = lane % kLanes * 8, sub = lane / kLanes;
+  const int col = lane % kLanes * kN, sub = lane / kLanes;
   const int64_t stride = of ? v_stride : k_stride;
   const T* x = (of ? V : K) + t.token * stride + static_cast<int64_t>(h) * D + col;
-  Eight<T> in[kIt];
+  Piece<T> in[kIt];
 #pragma unroll
   for (int i = 0; i < kIt; ++i) {
     const int r = i * kAt + sub;
-    if (r >= t.rows0 && r < t.rows1) in[i].load(x + (r - t.rows0) * stride);
-    else in[i].zero();
+    in[i].a = r >= t.rows0 && r < t.rows1 ? __ldg(reinterpret_cast<const uint4*>(x + (r - t.rows0) * stride)) : make_uint4(0u, 0u, 0u, 0u);
   }
   const int pg = c.page(t.b, t.slot);
   if (pg < 0) return;
@@ -113,28 +122,35 @@ append_kernel(const Int8View c, const T* __restrict__ K, int64_t k_stride, const
 
   uint32_t most = 0;
 #pragma unroll
-  for (int i = 0; i < kIt; ++i) {
-    uint32_t b[8];
-    in[i].bits(b);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) most = max(most, b[k] & 0x7fffffffu);
-  }
+  for (int i = 0; i < kIt; ++i) most = max(most, in[i].most());
   most = __reduce_max_sync(0xffffffffu, most);
   const bool odd = most >= 0x7f800000u;      // an infinity or NaN: the exponent goes by the finite values
   if (odd) {
     most = 0;
 #pragma unroll
     for (int i = 0; i < kIt; ++i) {
-      uint32_t b[8];
+      uint32_t b[kN];
       in[i].bits(b);
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
+      for (int k = 0; k < kN; ++k)
         if ((b[k] & 0x7fffffffu) < 0x7f800000u) most = max(most, b[k] & 0x7fffffffu);
     }
     most = __reduce_max_sync(0xffffffffu, most);
   }
   int e = min(max(static_cast<int>(most >> 23) - 133, kExpLow), kExpHigh);   // 2^(e + 6) <= most < 2^(e + 7)
   if (t.old) e = max(e, e_old);
+  if (odd) {
+    // infinity takes the highest code, minus infinity and NaN the lowest (both whole numbers times 2^e, exact in bf16)
+#pragma unroll
+    for (int i = 0; i < kIt; ++i) {
+      uint32_t b[kN];
+      in[i].bits(b);
+#pragma unroll
+      for (int k = 0; k < kN; ++k)
+        if ((b[k] & 0x7fffffffu) >= 0x7f800000u) b[k] = __float_as_uint((b[k] == 0x7f800000u ? 127.0f : -128.0f) * pow2(e));
+      in[i].set(b);
+    }
+  }
 
   if (t.old && e > e_old) {
     // bytes: ((u - 128) >> s) + 128 = (u >> s) + 128 - (128 >> s); beyond 7 every code is next to the middle, as at 7
@@ -154,28 +170,24 @@ append_kernel(const Int8View c, const T* __restrict__ K, int64_t k_stride, const
 #pragma unroll
   for (int i = 0; i < kIt; ++i) {
     const int r = i * kAt + sub;
-    uint32_t b[8];
+    uint32_t b[kN];
     in[i].bits(b);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      float f = __uint_as_float(b[k]);
-      // infinity takes the highest code, minus infinity and NaN the lowest
-      if (odd && (b[k] & 0x7fffffffu) >= 0x7f800000u) f = (b[k] == 0x7f800000u ? 127.0f : -128.0f) * pow2(e);
-      b[k] = __float_as_uint(__fmaf_rd(f, scale, 12582912.0f + 128.0f));
+    for (int k = 0; k < kN; ++k) b[k] = __float_as_uint(__fmaf_rd(__uint_as_float(b[k]), scale, 12582912.0f + 128.0f));
+    uint32_t o[kN / 4];
+#pragma unroll
+    for (int k = 0; k < kN / 4; ++k)
+      o[k] = __byte_perm(__byte_perm(b[4 * k], b[4 * k + 1], 0x0040), __byte_perm(b[4 * k + 2], b[4 * k + 3], 0x0040), 0x5410);
+    if (r >= t.rows0 && r < t.rows1) {
+      if constexpr (kN == 8) *reinterpret_cast<uint2*>(to + r * D + col) = make_uint2(o[0], o[1]);
+      else *reinterpret_cast<uint32_t*>(to + r * D + col) = o[0];
     }
-    uint2 o;
-    o.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-    o.y = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
-    if (r >= t.rows0 && r < t.rows1) *reinterpret_cast<uint2*>(to + r * D + col) = o;
   }
   if (lane == 0) *ex = static_cast<int8_t>(e);
 }
 
-__device__ __forceinline__ void put8(float* p, const float* f) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-}
-__device__ __forceinline__ void put8(__nv_bfloat16* p, const float* f) {      // exact: the upper halves
+__device__ __forceinline__ void put(float* p, const float* f) { *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]); }
+__device__ __forceinline__ void put(__nv_bfloat16* p, const float* f) {      // exact: the upper halves
   uint32_t v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = __byte_perm(__float_as_uint(f[2 * i]), __float_as_uint(f[2 * i + 1]), 0x7632);
@@ -185,7 +197,7 @@ __device__ __forceinline__ void put8(__nv_bfloat16* p, const float* f) {      //
 template <typename T, int D>
 __global__ void __launch_bounds__(kWarps * 32)
 read_kernel(const Int8View c, T* __restrict__ K, T* __restrict__ V, const Step step) {
-  constexpr int kLanes = D / 8, kAt = 32 / kLanes, kIt = kBlockSlots / kAt;
+  constexpr int kN = Piece<T>::kN, kLanes = D / kN, kAt = 32 / kLanes, kIt = kBlockSlots / kAt;
   const int lane = threadIdx.x & 31;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int of = static_cast<int>(w & 1), h = static_cast<int>((w >> 1) % c.H);
@@ -194,9 +206,9 @@ read_kernel(const Int8View c, T* __restrict__ K, T* __restrict__ V, const Step s
   Unit t;
   if (!unit_of(step, static_cast<int>(u), lane, t)) return;
 
-  const int col = lane % kLanes * 8, sub = lane / kLanes;
+  const int col = lane % kLanes * kN, sub = lane / kLanes;
   const int pg = c.page(t.b, t.slot);
-  uint2 in[kIt];
+  uint32_t in[kIt][kN / 4];
   int e = 0;
   if (pg >= 0) {
     const size_t row = c.row(pg, h, t.slot);
@@ -205,7 +217,15 @@ read_kernel(const Int8View c, T* __restrict__ K, T* __restrict__ V, const Step s
 #pragma unroll
     for (int i = 0; i < kIt; ++i) {
       const int r = i * kAt + sub;
-      if (r >= t.rows0 && r < t.rows1) in[i] = *reinterpret_cast<const uint2*>(from + r * D);
+      if (r >= t.rows0 && r < t.rows1) {
+        if constexpr (kN == 8) {
+          const uint2 v = *reinterpret_cast<const uint2*>(from + r * D);
+          in[i][0] = v.x;
+          in[i][1] = v.y;
+        } else {
+          in[i][0] = *reinterpret_cast<const uint32_t*>(from + r * D);
+        }
+      }
     }
   }
   // an exponent outside the range that is written has no power of two in fp32's normal numbers: cut to it
@@ -216,14 +236,14 @@ read_kernel(const Int8View c, T* __restrict__ K, T* __restrict__ V, const Step s
   for (int i = 0; i < kIt; ++i) {
     const int r = i * kAt + sub;
     if (r >= t.rows0 && r < t.rows1) {
-      float f[8];
+      float f[kN];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < kN; ++k) {
         // the byte below 2^23 is a whole number; u * 2^e - 127.5 * 2^e has one rounding, and none is needed
-        const float whole = __uint_as_float(__byte_perm(k < 4 ? in[i].x : in[i].y, 0x4b000000u, 0x7550 + (k & 3))) - 8388608.0f;
+        const float whole = __uint_as_float(__byte_perm(in[i][k / 4], 0x4b000000u, 0x7550 + (k & 3))) - 8388608.0f;
         f[k] = pg >= 0 ? fmaf(whole, scale, -127.5f * scale) : 0.0f;
       }
-      put8(out + (r - t.rows0) * stride, f);
+      put(out + (r - t.rows0) * stride, f);
     }
   }
 }

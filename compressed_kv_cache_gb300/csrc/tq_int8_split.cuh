@@ -28,15 +28,18 @@
 
 namespace tq {
 
-constexpr int kAttendCtas = 320;      // room for the parts of this many blocks
+constexpr int kAttendCtas = 480;      // room for the parts of this many blocks
 constexpr int kAttendWarps = 4;
-constexpr int kTileSlots = 32, kQuadTiles = kAttendWarps, kAttendStages = 3;
+constexpr int kTileSlots = 32, kQuadTiles = kAttendWarps;
+
+// Blocks an SM: what registers allow.  More of them hide a tile's latency better than deeper rings.
+constexpr int attend_blocks(bool f32, int D, int nt) { return nt == 1 && !f32 ? 3 : 2; }
 
 // What a block leaves for the join: the unit that it starts in the middle of.
-struct AttendRecord {
-  int64_t chunk;             // quads of a block
-  int64_t off, quads;        // of the unit: quads before this block's start, all
-  int first, count, h, cb;
+struct alignas(16) AttendRecord {
+  int chunk;                 // quads of a block (cut to 2^30: no unit has more)
+  int off, quads;            // of the unit: quads before this block's start, all
+  int first, count, h, cb, unused;
 };
 
 struct AttendArgs {
@@ -174,10 +177,11 @@ struct Shape {
   static constexpr bool kF32 = sizeof(T) == 4;
   static constexpr int NC = 8 * NT, kParts = kF32 ? 2 : 1, kSteps = D / 16, kTiles = D / 16;
   static constexpr int kStep = NT <= 2 ? 2 : 1;                        // blocks of 16 slots taken at a time
+  static constexpr int kBlocks = attend_blocks(kF32, D, NT), kStages = kBlocks == 3 ? 2 : 3;
   static constexpr bool kQReg = NT * kParts <= 2;                      // the queries' operand in registers, or in shared memory
   static constexpr int kRow = kBlockSlots * D;                         // bytes of a block of 16 rows
   static constexpr int kStage = 4 * kRow;                              // keys' two blocks, values' two blocks
-  static constexpr int kRing = kAttendWarps * kAttendStages * kStage;
+  static constexpr int kRing = kAttendWarps * kStages * kStage;
   static constexpr int kQBytes = kQReg ? 0 : kSteps * NT * kParts * 256;
   static constexpr int kJoin = kAttendWarps * NC * D * 4;
   static constexpr int kBytes = (kRing > kJoin ? kRing : kJoin) + kQBytes;
@@ -193,15 +197,14 @@ __device__ __forceinline__ int join_at(int col, int i) {
 }
 
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_split_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(kAttendWarps * 32, (attend_blocks(sizeof(T) == 4, D, NT))) attend_split_kernel(const AttendArgs a) {
   using S = Shape<T, D, NT>;
-  constexpr int NC = S::NC, MT = S::kTiles;
+  constexpr int NC = S::NC, MT = S::kTiles, kStages = S::kStages;
   extern __shared__ __align__(128) char smem[];
   __shared__ int64_t scan_of[kAttendWarps];
   __shared__ int64_t found_base;
   __shared__ int found_b;
-  __shared__ uint32_t stage_ex[kAttendWarps][kAttendStages];
-  __shared__ uint32_t stage_in[kAttendWarps][kAttendStages];
+  __shared__ float4 stage_ex[kAttendWarps][kStages];      // of the two blocks: 2^(key's exponent), 0 for an absent one; value's exponent
   __shared__ float3 warp_top[kAttendWarps][NC];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -260,7 +263,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_split_kernel(cons
   Plan plan = plan_of<NC>(a, b);
   int64_t pos = x0 - found_base;           // quads into sequence b
 
-  const uint32_t ring = smem_addr(smem) + warp * kAttendStages * S::kStage;
+  const uint32_t ring = smem_addr(smem) + warp * kStages * S::kStage;
   const uint32_t q_area = smem_addr(smem) + S::kBytes - S::kQBytes;
   // lane offsets within a block of 16 rows: copies, keys, values
   const int swap_w = D == 128 ? (((lane >> 3) >> 1 & 1) << 1) ^ (((lane >> 3) & 1) << 2) : (lane >> 3) << 1;
@@ -279,14 +282,17 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_split_kernel(cons
     const int h = static_cast<int>(unit / plan.ncb), cb = static_cast<int>(unit - static_cast<int64_t>(h) * plan.ncb);
     const Span sp = span_of<NC>(a, plan.r, cb);
     const Run run = plan.r;
-    if (tid == 0 && x == x0) a.rec[blockIdx.x] = {chunk, qa, plan.quads, run.first, run.count, h, cb};
+    if (tid == 0 && x == x0) 
+      a.rec[blockIdx.x] = {static_cast<int>(min(chunk, static_cast<int64_t>(1) << 30)), static_cast<int>(qa), static_cast<int>(plan.quads),
+                           run.first, run.count, h, cb, 0};
 
     // ---- the warp's tiles: 4 q + warp for quads q in [qa, qe)
     const int n = max(0, static_cast<int>(min(qe, (static_cast<int64_t>(sp.tiles) - warp + 3) / 4) - qa));
+    const int j0 = static_cast<int>(4 * qa) + warp;
     int blk0 = -1, blk1 = -1;
-    uint32_t ex = 0;
+    float4 ex;
     auto slot_of = [&](int i) {
-      const int j = static_cast<int>(4 * (qa + i)) + warp;
+      const int j = j0 + 4 * i;
       return (j < sp.sunk ? j : j - sp.sunk + sp.from) * kTileSlots;
     };
     auto block_of = [&](int s) {
@@ -297,23 +303,25 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_split_kernel(cons
     auto issue = [&](int i) {
       if ((i & 31) == 0) {      // a lane looks up one tile of the next 32
         blk0 = blk1 = -1;
-        ex = 0;
+        ex = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (i + lane < n) {
           const int s = slot_of(i + lane);
           blk0 = block_of(s);
           blk1 = block_of(s + kBlockSlots);
-          if (blk0 >= 0) ex = *reinterpret_cast<const uint16_t*>(a.c.ex + 2 * static_cast<size_t>(blk0));
-          if (blk1 >= 0) ex |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(a.c.ex + 2 * static_cast<size_t>(blk1))) << 16;
+          char2 e0 = make_char2(0, 0), e1 = e0;
+          if (blk0 >= 0) e0 = *reinterpret_cast<const char2*>(a.c.ex + 2 * static_cast<size_t>(blk0));
+          if (blk1 >= 0) e1 = *reinterpret_cast<const char2*>(a.c.ex + 2 * static_cast<size_t>(blk1));
+          auto cut = [](int e) { return min(max(e, kExpLow), kExpHigh); };
+          ex.x = blk0 >= 0 ? pow2(cut(e0.x)) : 0.0f;
+          ex.y = blk1 >= 0 ? pow2(cut(e1.x)) : 0.0f;
+          ex.z = static_cast<float>(cut(e0.y));
+          ex.w = static_cast<float>(cut(e1.y));
         }
       }
       if (i < n) {
-        const int stage = i % kAttendStages;
+        const int stage = i % kStages;
         const int p0 = __shfl_sync(0xffffffffu, blk0, i & 31), p1 = __shfl_sync(0xffffffffu, blk1, i & 31);
-        const uint32_t e = __shfl_sync(0xffffffffu, ex, i & 31);
-        if (lane == 0) {
-          stage_ex[warp][stage] = e;
-          stage_in[warp][stage] = (p0 >= 0 ? 1u : 0u) | (p1 >= 0 ? 2u : 0u);
-        }
+        if (lane == (i & 31)) stage_ex[warp][stage] = ex;
         const uint32_t to = ring + stage * S::kStage;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -332,7 +340,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_split_kernel(cons
     };
     __syncthreads();              // the ring has been the last unit's join
 #pragma unroll
-    for (int i = 0; i < kAttendStages - 1; ++i) issue(i);
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
 
     // ---- queries: lane (g, t) holds column g of each 8 at dimensions 64 k + 16 t .. + 15
     uint32_t qf[S::kQReg ? S::kSteps * NT * S::kParts * 2 : 1];
@@ -426,13 +434,13 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_split_kernel(cons
 
     for (int i = 0; i < n; ++i) {
       __syncwarp();               // the stage that is filled next has been read by all lanes
-      issue(i + kAttendStages - 1);
-      wait_copies<kAttendStages - 1>();
+      issue(i + kStages - 1);
+      wait_copies<kStages - 1>();
       __syncwarp();
-      const int stage = i % kAttendStages, s0 = slot_of(i);
+      const int stage = i % kStages, s0 = slot_of(i);
       const uint32_t at = ring + stage * S::kStage;
-      const uint32_t e2 = stage_ex[warp][stage], in = stage_in[warp][stage];
-      const bool plain = in == 3 && s0 + kTileSlots - 1 <= all_hi && (s0 > all_lo || s0 + kTileSlots <= a.sinks);
+      const float4 e2 = stage_ex[warp][stage];
+      const bool plain = e2.x != 0.0f && e2.y != 0.0f && s0 + kTileSlots - 1 <= all_hi && (s0 > all_lo || s0 + kTileSlots <= a.sinks);
 #pragma unroll
       for (int kb0 = 0; kb0 < 2; kb0 += S::kStep) {
         float z[S::kStep][NT][4];
@@ -468,15 +476,13 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_split_kernel(cons
           }
         }
         // ---- weights
-        float ev[S::kStep], top[NT][2], topv[NT][2];
+        float top[NT][2], topv[NT][2];
         bool over = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = topv[nt][0] = topv[nt][1] = -INFINITY;
 #pragma unroll
         for (int kb = 0; kb < S::kStep; ++kb) {
-          const uint32_t e = e2 >> (16 * (kb0 + kb));
-          const float ek = pow2(min(max(static_cast<int>(static_cast<int8_t>(e & 0xff)), kExpLow), kExpHigh));
-          ev[kb] = static_cast<float>(min(max(static_cast<int>(static_cast<int8_t>(e >> 8 & 0xff)), kExpLow), kExpHigh));
+          const float ek = kb0 + kb ? e2.y : e2.x, ev = kb0 + kb ? e2.w : e2.z;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -489,7 +495,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_split_kernel(cons
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                   const int s = s0 + (kb0 + kb) * kBlockSlots + g + 8 * r;
-                  const bool seen = (in >> (kb0 + kb) & 1) && s <= own && (a.window <= 0 || s > own - a.window || s < a.sinks);
+                  const bool seen = ek != 0.0f && s <= own && (a.window <= 0 || s > own - a.window || s < a.sinks);
                   if (!seen) z[kb][nt][2 * r + i2] = -INFINITY;
                 }
               }
@@ -498,7 +504,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_split_kernel(cons
             for (int i2 = 0; i2 < 2; ++i2) {
               const float v = fmaxf(z[kb][nt][i2], z[kb][nt][2 + i2]);
               top[nt][i2] = fmaxf(top[nt][i2], v);
-              topv[nt][i2] = fmaxf(topv[nt][i2], v + ev[kb]);
+              topv[nt][i2] = fmaxf(topv[nt][i2], v + ev);
             }
           }
         }
@@ -541,7 +547,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_split_kernel(cons
               for (int i2 = 0; i2 < 2; ++i2) {
                 const float v = z[kb][nt][2 * r + i2];
                 sum[nt][i2] += exp2_fast(v - m[nt][i2]);
-                w[i2] = exp2_fast(v + (ev[kb] + kLift - M[nt][i2]));
+                w[i2] = exp2_fast(v + ((kb0 + kb ? e2.w : e2.z) + kLift - M[nt][i2]));
                 W[nt][i2] += w[i2];
               }
               const uint32_t hi = pack(w[0], w[1]);

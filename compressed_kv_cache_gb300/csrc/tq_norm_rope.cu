@@ -3,7 +3,7 @@
 //   y = x / sqrt(mean(x^2) + eps) * w,   (a, b) -> (a cos t - b sin t, b cos t + a sin t),
 //   t = positions[axis of the pair] * frequency of the pair
 //
-// A row (one head of one token) lies across 2 to 32 lanes; a lane holds both members of four pairs, so that
+// A row (one head of one token) lies across 8 to 32 lanes; a lane holds both members of four pairs, so that
 // the rotation needs no exchange between lanes and a lane's four sines and cosines serve every head of its
 // token.  Sums are held in 32 bits, the result is rounded once.
 //
@@ -17,7 +17,8 @@ namespace tq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 4;         // rows a lane has in flight
+template <typename T>
+constexpr int kRowsOf = sizeof(T) == 4 ? 2 : 4;      // rows a lane has in flight, 16 registers either way
 
 template <typename T>
 struct Four;
@@ -44,137 +45,147 @@ struct Four<__nv_bfloat16> {
   }
 };
 
-// A warp takes `per` heads of one token, queries' or keys' (parts: slices of queries, then of keys).
-template <typename T>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRope a, int lanes_log2, int per, int q_parts, int parts) {
+// A warp takes `per` heads of one token, of the queries' heads and the keys' behind them.  kLanes lanes a row.
+template <typename T, int kLanes, bool kPaired>
+__global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const NormRope a, int per, int parts, float inv_d) {
+  constexpr int kAt = 32 / kLanes, kRows = kRowsOf<T>;         // rows at a time, loads of them in flight
   const int lane = threadIdx.x & 31;
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
   const int64_t token = unit / parts;
   if (token >= a.n) return;
-  int part = static_cast<int>(unit - token * parts);
-  const bool keys = part >= q_parts;
-  if (keys) part -= q_parts;
-  const int heads = keys ? a.Hk : a.Hq;
-  const int stop = min(heads, (part + 1) * per);
-  const T* x = static_cast<const T*>(keys ? a.k : a.q) + token * (keys ? a.k_token : a.q_token);
-  const int64_t head_stride = keys ? a.k_head : a.q_head;
-  T* out = static_cast<T*>(keys ? a.k_out : a.q_out) + token * heads * a.D;
-  const void* weight = keys ? a.k_weight : a.q_weight;
+  const int part = static_cast<int>(unit - token * parts);
 
   // where this lane's two groups of four lie: members of four pairs, or eight that are not rotated
-  const int j = lane & ((1 << lanes_log2) - 1), sub = lane >> lanes_log2, rows = 32 >> lanes_log2;
-  const int rot = 2 * a.pairs;
+  const int j = lane % kLanes, sub = lane / kLanes, rot = 2 * a.pairs;
   const bool turned = 8 * j < rot, there = 8 * j < a.D;
-  const int at_a = turned && !a.paired ? 4 * j : 8 * j;
-  const int at_b = turned && !a.paired ? rot / 2 + 4 * j : 8 * j + 4;
+  const int at_a = turned && !kPaired ? 4 * j : 8 * j;
+  const int at_b = turned && !kPaired ? a.pairs + 4 * j : 8 * j + 4;
 
-  Four<T> xa[kRows], xb[kRows];
-  auto fetch = [&](int h0) {
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const int h = h0 + r * rows + sub;
-      if (there && h < stop) {
-        xa[r].load(x + h * head_stride + at_a);
-        xb[r].load(x + h * head_stride + at_b);
-      }
-    }
-  };
-  int h0 = part * per;
-  fetch(h0);
-
-  float w[8], c[4], s[4];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = 1.0f;
-  if (weight != nullptr && there) {
-    if (a.weights_bf16) {
-      Four<__nv_bfloat16> u, v;
-      u.load(static_cast<const __nv_bfloat16*>(weight) + at_a);
-      v.load(static_cast<const __nv_bfloat16*>(weight) + at_b);
-      u.get(w); v.get(w + 4);
-    } else {
-      Four<float> u, v;
-      u.load(static_cast<const float*>(weight) + at_a);
-      v.load(static_cast<const float*>(weight) + at_b);
-      u.get(w); v.get(w + 4);
-    }
-  }
+  float c[4], s[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     c[i] = 1.0f;
     s[i] = 0.0f;
-    if (turned) {
-      const int axis = min(static_cast<int>(__ldg(a.axis + 4 * j + i)), a.axes - 1);
-      const int64_t pos = __ldg(a.positions + token * a.axes + axis);
-      const uint64_t turn = __ldg(reinterpret_cast<const unsigned long long*>(a.turns) + 4 * j + i) * static_cast<uint64_t>(pos);
-      sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &s[i], &c[i]);
-    }
   }
-
-  for (; h0 < stop; h0 += kRows * rows) {
-    if (h0 != part * per) fetch(h0);
+  bool made = false;
+  auto heads = [&](const T* x, int64_t stride, T* out, const void* weight, int h0, int h1) {
+    if (h0 >= h1) return;
+    const T* from = x + (h0 + sub) * stride;
+    T* to = out + static_cast<int64_t>(h0 + sub) * a.D;
+    Four<T> xa[kRows], xb[kRows];
+    auto fetch = [&](int left) {
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const int h = h0 + r * rows + sub;
-      float f[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = 0.0f;
-      if (there && h < stop) {
-        xa[r].get(f);
-        xb[r].get(f + 4);
-      }
-      if (weight != nullptr) {
-        float ss = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
-        for (int o = 1; o < 1 << lanes_log2; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float inv = rsqrtf(ss / static_cast<float>(a.D) + a.eps);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = f[i] * inv * w[i];
-      }
-      float g[8];
-      if (!turned) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = f[i];
-      } else if (a.paired) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          g[2 * i] = f[2 * i] * c[i] - f[2 * i + 1] * s[i];
-          g[2 * i + 1] = f[2 * i + 1] * c[i] + f[2 * i] * s[i];
+      for (int r = 0; r < kRows; ++r)
+        if (there && r * kAt + sub < left) {
+          xa[r].load(from + r * kAt * stride + at_a);
+          xb[r].load(from + r * kAt * stride + at_b);
         }
+    };
+    fetch(h1 - h0);
+    if (!made && turned) {      // under way while the rows come
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int axis = min(static_cast<int>(__ldg(a.axis + 4 * j + i)), a.axes - 1);
+        const int64_t pos = __ldg(a.positions + token * a.axes + axis);
+        const uint64_t turn = __ldg(reinterpret_cast<const unsigned long long*>(a.turns) + 4 * j + i) * static_cast<uint64_t>(pos);
+        sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &s[i], &c[i]);
+      }
+    }
+    made = true;
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 1.0f;
+    if (weight != nullptr && there) {
+      if (a.weights_bf16) {
+        Four<__nv_bfloat16> u, v;
+        u.load(static_cast<const __nv_bfloat16*>(weight) + at_a);
+        v.load(static_cast<const __nv_bfloat16*>(weight) + at_b);
+        u.get(w); v.get(w + 4);
       } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          g[i] = f[i] * c[i] - f[4 + i] * s[i];
-          g[4 + i] = f[4 + i] * c[i] + f[i] * s[i];
-        }
-      }
-      if (there && h < stop) {
-        Four<T>::put(out + static_cast<int64_t>(h) * a.D + at_a, g);
-        Four<T>::put(out + static_cast<int64_t>(h) * a.D + at_b, g + 4);
+        Four<float> u, v;
+        u.load(static_cast<const float*>(weight) + at_a);
+        v.load(static_cast<const float*>(weight) + at_b);
+        u.get(w); v.get(w + 4);
       }
     }
-  }
+    for (int left = h1 - h0;;) {
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        if (r * kAt >= left) break;      // the whole warp's
+        const bool mine = there && r * kAt + sub < left;
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = 0.0f;
+        if (mine) {
+          xa[r].get(f);
+          xb[r].get(f + 4);
+        }
+        if (weight != nullptr) {
+          float ss = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          const float inv = rsqrtf(fmaf(ss, inv_d, a.eps));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] *= inv * w[i];
+        }
+        if (turned) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int u = kPaired ? 2 * i : i, v = kPaired ? 2 * i + 1 : 4 + i;
+            const float y = f[u];
+            f[u] = y * c[i] - f[v] * s[i];
+            f[v] = f[v] * c[i] + y * s[i];
+          }
+        }
+        if (mine) {
+          Four<T>::put(to + r * kAt * a.D + at_a, f);
+          Four<T>::put(to + r * kAt * a.D + at_b, f + 4);
+        }
+      }
+      left -= kRows * kAt;
+      if (left <= 0) break;
+      from += kRows * kAt * stride;
+      to += kRows * kAt * a.D;
+      fetch(left);
+    }
+  };
+  const int h0 = part * per, h1 = min(a.Hq + a.Hk, h0 + per);
+  heads(static_cast<const T*>(a.q) + token * a.q_token, a.q_head, static_cast<T*>(a.q_out) + token * a.Hq * a.D, a.q_weight, min(h0, a.Hq),
+        min(h1, a.Hq));
+  heads(static_cast<const T*>(a.k) + token * a.k_token, a.k_head, static_cast<T*>(a.k_out) + token * a.Hk * a.D, a.k_weight, max(h0 - a.Hq, 0),
+        max(h1 - a.Hq, 0));
+}
+
+template <typename T, int kLanes>
+void launch(const NormRope& a, int per, int parts, cudaStream_t st) {
+  const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(a.n) * parts + kThreads / 32 - 1) / (kThreads / 32));
+  const float inv_d = 1.0f / static_cast<float>(a.D);
+  if (a.paired) norm_rope_kernel<T, kLanes, true><<<blocks, kThreads, 0, st>>>(a, per, parts, inv_d);
+  else norm_rope_kernel<T, kLanes, false><<<blocks, kThreads, 0, st>>>(a, per, parts, inv_d);
+}
+
+template <typename T>
+cudaError_t launch_of(const NormRope& a, cudaStream_t st) {
+  const int lanes = a.D <= 64 ? 8 : a.D <= 128 ? 16 : 32, rows = 32 / lanes;
+  // As many heads a warp as leave 16 warps for each of 152 SMs: a token's sines are then made once, and a
+  // single token is spread over warps of one row a lane.
+  const int heads = a.Hq + a.Hk;
+  const int64_t share = static_cast<int64_t>(a.n) * heads / (152 * 16);
+  int per = share < 1 ? 1 : share > heads ? heads : static_cast<int>(share);
+  per = (per + rows - 1) / rows * rows;
+  const int parts = (heads + per - 1) / per;
+  if (lanes == 8) launch<T, 8>(a, per, parts, st);
+  else if (lanes == 16) launch<T, 16>(a, per, parts, st);
+  else launch<T, 32>(a, per, parts, st);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_norm_rope(const NormRope& a, tq_qtype type, cudaStream_t st) {
-  int lanes_log2 = 0;
-  while ((8 << lanes_log2) < a.D) ++lanes_log2;
-  const int rows = 32 >> lanes_log2;
-  // As many heads a warp as leave 16 warps for each of 152 SMs: a token's sines are then made once for
-  // its queries and once for its keys, and a single token is spread over warps of one row a lane.
-  const int heads = a.Hq > a.Hk ? a.Hq : a.Hk;
-  int per = static_cast<int>(static_cast<int64_t>(a.n) * (a.Hq + a.Hk) / (152 * 16));
-  per = (per < 1 ? 1 : per > heads ? heads : per);
-  per = (per + rows - 1) / rows * rows;
-  const int q_parts = (a.Hq + per - 1) / per, parts = q_parts + (a.Hk + per - 1) / per;
-  const int64_t blocks = (static_cast<int64_t>(a.n) * parts + kThreads / 32 - 1) / (kThreads / 32);
-  if (type == TQ_Q_F32)
-    norm_rope_kernel<float><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(a, lanes_log2, per, q_parts, parts);
-  else
-    norm_rope_kernel<__nv_bfloat16><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(a, lanes_log2, per, q_parts, parts);
-  return cudaGetLastError();
+  return type == TQ_Q_F32 ? launch_of<float>(a, st) : launch_of<__nv_bfloat16>(a, st);
 }
 
 }  // namespace tq
