@@ -17,36 +17,47 @@ constexpr float kLifted = 7.0f;      // weights were taken 2^7 above their range
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const AttendArgs a, int NC, int ctas) {
   constexpr int kDims = D / 32;
-  __shared__ int starts[kAttendCtas];
+  __shared__ AttendRecord records[kAttendCtas];
   __shared__ int warp_count[kJoinWarps];
   __shared__ float4 warp_top[kJoinWarps];
   __shared__ float warp_acc[kJoinWarps][D];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  int units = 0;
-  for (int i0 = 0; i0 < ctas; i0 += kJoinWarps * 32) {
-    bool first = false;
-    if (i0 + tid < ctas) {
-      const int4 r = *reinterpret_cast<const int4*>(a.rec + i0 + tid);      // chunk, off
-      first = r.y > 0 && r.y <= r.x;
+  // all records are on their way at once: two a thread
+  static_assert(kAttendCtas <= 2 * kJoinWarps * 32, "records a thread");
+  AttendRecord mine[2];
+  bool first[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = 2 * tid + k;
+    first[k] = false;
+    if (i < ctas) {
+      mine[k] = a.rec[i];
+      first[k] = mine[k].off > 0 && mine[k].off <= mine[k].chunk;
     }
-    const uint32_t hit = __ballot_sync(0xffffffffu, first);
-    if (lane == 0) warp_count[warp] = __popc(hit);
-    __syncthreads();
-    int at = units + __popc(hit & ((1u << lane) - 1));
-    for (int w = 0; w < kJoinWarps; ++w) {
-      if (w < warp) at += warp_count[w];
-      units += warp_count[w];
-    }
-    if (first) starts[at] = i0 + tid;
-    __syncthreads();
   }
+  int at = (first[0] ? 1 : 0) + (first[1] ? 1 : 0);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, at, o);
+    if (lane >= o) at += y;
+  }
+  if (lane == 31) warp_count[warp] = at;
+  __syncthreads();
+  int units = 0;
+  for (int w = 0; w < kJoinWarps; ++w) {
+    if (w < warp) at += warp_count[w];
+    units += warp_count[w];
+  }
+#pragma unroll
+  for (int k = 1; k >= 0; --k)
+    if (first[k]) records[--at] = mine[k];
+  __syncthreads();
   const int items = units * NC;
   const bool shared = items < static_cast<int>(gridDim.x) * 2;      // a block an item
   const int step = shared ? kJoinWarps : 1, w0 = shared ? warp : 0;
   for (int item = shared ? blockIdx.x : blockIdx.x * kJoinWarps + warp; item < items; item += gridDim.x * (shared ? 1 : kJoinWarps)) {
-    const int i = starts[item / NC], col = item % NC;
-    const AttendRecord r = a.rec[i];
+    const AttendRecord r = records[item / NC];
+    const int i = r.block, col = item % NC;
     const int64_t cc = static_cast<int64_t>(r.cb) * NC + col;
     if (cc >= static_cast<int64_t>(r.count) * a.G) continue;
     const int pieces = 1 + (r.quads - r.off + r.chunk - 1) / r.chunk;

@@ -33,13 +33,14 @@ constexpr int kAttendWarps = 4;
 constexpr int kTileSlots = 32, kQuadTiles = kAttendWarps;
 
 // Blocks an SM: what registers allow.  More of them hide a tile's latency better than deeper rings.
-constexpr int attend_blocks(bool f32, int D, int nt) { return nt == 1 && !f32 ? 3 : 2; }
+constexpr int attend_blocks(bool f32, int D, int nt) { return D == 64 && nt == 1 ? 3 : 2; }
 
 // What a block leaves for the join: the unit that it starts in the middle of.
 struct alignas(16) AttendRecord {
   int chunk;                 // quads of a block (cut to 2^30: no unit has more)
   int off, quads;            // of the unit: quads before this block's start, all
-  int first, count, h, cb, unused;
+  int first, count, h, cb;
+  int block;                 // the block's own number
 };
 
 struct AttendArgs {
@@ -177,7 +178,7 @@ struct Shape {
   static constexpr bool kF32 = sizeof(T) == 4;
   static constexpr int NC = 8 * NT, kParts = kF32 ? 2 : 1, kSteps = D / 16, kTiles = D / 16;
   static constexpr int kStep = NT <= 2 ? 2 : 1;                        // blocks of 16 slots taken at a time
-  static constexpr int kBlocks = attend_blocks(kF32, D, NT), kStages = kBlocks == 3 ? 2 : 3;
+  static constexpr int kBlocks = attend_blocks(kF32, D, NT), kStages = kBlocks == 3 && D == 128 ? 2 : 3;
   static constexpr bool kQReg = NT * kParts <= 2;                      // the queries' operand in registers, or in shared memory
   static constexpr int kRow = kBlockSlots * D;                         // bytes of a block of 16 rows
   static constexpr int kStage = 4 * kRow;                              // keys' two blocks, values' two blocks
@@ -204,26 +205,40 @@ __global__ void __launch_bounds__(kAttendWarps * 32, (attend_blocks(sizeof(T) ==
   __shared__ int64_t scan_of[kAttendWarps];
   __shared__ int64_t found_base;
   __shared__ int found_b;
+  __shared__ Plan found_plan;
   __shared__ float4 stage_ex[kAttendWarps][kStages];      // of the two blocks: 2^(key's exponent), 0 for an absent one; value's exponent
   __shared__ float3 warp_top[kAttendWarps][NC];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int B = a.step.B, H = a.c.H;
 
-  // ---- this block's share: all quads counted, then the sequence that the share starts in
-  int64_t all = 0;
-  for (int b0 = 0; b0 < B; b0 += kAttendWarps * 32) {
-    int64_t v = 0;
+  // ---- this block's share: the quads of all sequences counted (128 at a time), then the sequence that the share starts in
+  constexpr int kAt = kAttendWarps * 32;
+  Plan plan;
+  int64_t own, upto;              // quads of this thread's sequence; of those up to it, within the 128
+  auto count = [&](int b0) {
+    own = 0;
     if (b0 + tid < B) {
-      const Plan p = plan_of<NC>(a, b0 + tid);
-      v = p.quads * p.ncb * H;
+      plan = plan_of<NC>(a, b0 + tid);
+      own = plan.quads * plan.ncb * H;
     }
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    upto = own;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
     __syncthreads();
-    if (lane == 0) scan_of[warp] = v;
+    if (lane == 31) scan_of[warp] = upto;
     __syncthreads();
-    for (int i = 0; i < kAttendWarps; ++i) all += scan_of[i];
-  }
+    int64_t sum = 0;
+    for (int i = 0; i < kAttendWarps; ++i) {
+      if (i < warp) upto += scan_of[i];
+      sum += scan_of[i];
+    }
+    return sum;
+  };
+  int64_t sum0 = count(0), all = sum0;
+  for (int b0 = kAt; b0 < B; b0 += kAt) all += count(b0);
   const int64_t chunk = (all + gridDim.x - 1) / gridDim.x;
   const int64_t x0 = chunk * blockIdx.x, x1 = min(x0 + chunk, all);
   if (x0 >= x1) {
@@ -231,37 +246,21 @@ __global__ void __launch_bounds__(kAttendWarps * 32, (attend_blocks(sizeof(T) ==
     return;
   }
   int64_t base = 0;
-  for (int b0 = 0; b0 < B; b0 += kAttendWarps * 32) {
-    int64_t v = 0;
-    if (b0 + tid < B) {
-      const Plan p = plan_of<NC>(a, b0 + tid);
-      v = p.quads * p.ncb * H;
-    }
-    int64_t x = v;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) scan_of[warp] = x;
-    __syncthreads();
-    int64_t before = base, sum = 0;
-    for (int i = 0; i < kAttendWarps; ++i) {
-      if (i < warp) before += scan_of[i];
-      sum += scan_of[i];
-    }
-    const int64_t lo = before + x - v;
-    if (lo <= x0 && x0 < lo + v) {
+  for (int b0 = 0;; b0 += kAt) {
+    if (B > kAt) sum0 = count(b0);
+    const int64_t lo = base + upto - own;
+    if (lo <= x0 && x0 < lo + own) {
       found_b = b0 + tid;
       found_base = lo;
+      found_plan = plan;
     }
-    base += sum;
-    if (base > x0) break;      // the same for all threads
+    base += sum0;
+    if (base > x0) break;         // the same for all threads
   }
   __syncthreads();
   int b = found_b;
-  Plan plan = plan_of<NC>(a, b);
-  int64_t pos = x0 - found_base;           // quads into sequence b
+  plan = found_plan;
+  int64_t pos = x0 - found_base;  // quads into sequence b
 
   const uint32_t ring = smem_addr(smem) + warp * kStages * S::kStage;
   const uint32_t q_area = smem_addr(smem) + S::kBytes - S::kQBytes;
@@ -284,7 +283,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, (attend_blocks(sizeof(T) ==
     const Run run = plan.r;
     if (tid == 0 && x == x0) 
       a.rec[blockIdx.x] = {static_cast<int>(min(chunk, static_cast<int64_t>(1) << 30)), static_cast<int>(qa), static_cast<int>(plan.quads),
-                           run.first, run.count, h, cb, 0};
+                           run.first, run.count, h, cb, static_cast<int>(blockIdx.x)};
 
     // ---- the warp's tiles: 4 q + warp for quads q in [qa, qe)
     const int n = max(0, static_cast<int>(min(qe, (static_cast<int64_t>(sp.tiles) - warp + 3) / 4) - qa));
@@ -321,7 +320,6 @@ __global__ void __launch_bounds__(kAttendWarps * 32, (attend_blocks(sizeof(T) ==
       if (i < n) {
         const int stage = i % kStages;
         const int p0 = __shfl_sync(0xffffffffu, blk0, i & 31), p1 = __shfl_sync(0xffffffffu, blk1, i & 31);
-        if (lane == (i & 31)) stage_ex[warp][stage] = ex;
         const uint32_t to = ring + stage * S::kStage;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -335,6 +333,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, (attend_blocks(sizeof(T) ==
             }
           }
         }
+        if (lane == (i & 31)) stage_ex[warp][stage] = ex;      // behind the copies: it waits for the exponents
       }
       commit();
     };
