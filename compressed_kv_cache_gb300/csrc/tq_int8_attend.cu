@@ -1,6 +1,7 @@
 // Attention of a step's tokens over the 8-bit paged cache (tq_attend_int8): two launches, the second a programmatic
 // dependent of the first.
-//   split   tq_int8_split.cuh: every unit's sums, written out where one block of threads had all of it
+//   split   tq_int8_split.cuh, or tq_int8_prompt.cu for pieces of prompts: every unit's sums, written out where one
+//           block of threads had all of it
 //   join    the parts of a unit that lies across blocks
 #include "tq_int8_split.cuh"
 
@@ -142,27 +143,29 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
   }
 }
 
-// Columns of 8 that a unit holds: as many as an average sequence fills, 4 at most (registers).  The
-// cache is read once for all columns of a unit, and a second time, from L2, for the next ones.
-int column_tiles(int n, int B, int G) {
+// Columns of a unit: 8, 16 or 32 in the warp-wide form, as many as an average sequence fills (the cache is read
+// once for all columns of a unit, and again, from L2, for the next ones); 256 in the prompts' form, for bf16 queries with more than 32.
+int columns_of(int n, int B, int G, bool f32) {
   const int64_t columns = (static_cast<int64_t>(n) * G + B - 1) / B;
-  return columns <= 8 ? 1 : columns <= 16 ? 2 : 4;
+  return columns <= 8 ? 8 : columns <= 16 ? 16 : columns <= 32 || f32 ? 32 : 256;
 }
 
 struct Space {
   size_t top, part, all;
-  Space(int nt, int D) {
-    size_t at = paged_round(kAttendCtas * sizeof(AttendRecord));
-    top = at;
-    at += paged_round(static_cast<size_t>(kAttendCtas) * 2 * 8 * nt * sizeof(float4));
-    part = at;
-    all = at + static_cast<size_t>(kAttendCtas) * 2 * 8 * nt * D * sizeof(float);
+  Space(int NC, int D) {
+    const size_t parts = static_cast<size_t>(NC == 256 ? kPromptCtas : kAttendCtas) * 2 * NC;
+    top = paged_round(kAttendCtas * sizeof(AttendRecord));
+    part = top + paged_round(parts * sizeof(float4));
+    all = part + parts * D * sizeof(float);
   }
 };
 
 }  // namespace
 
-size_t attend_int8_bytes(int n, int B, int H, int G, int D) { return Space(column_tiles(n, B, G), D).all; }
+size_t attend_int8_bytes(int n, int B, int H, int G, int D) {
+  const size_t one = Space(columns_of(n, B, G, false), D).all, two = Space(columns_of(n, B, G, true), D).all;
+  return one > two ? one : two;
+}
 
 cudaError_t launch_attend_int8(const tq_int8_cache& c, const void* Q, tq_qtype type, const Step& step, int G,
                                const int* table, int max_pages, int window, int sinks, float scale, void* out,
@@ -177,14 +180,15 @@ cudaError_t launch_attend_int8(const tq_int8_cache& c, const void* Q, tq_qtype t
     if (e != cudaSuccess) return e;
     sms_cache[dev & 63].store(sms, std::memory_order_relaxed);
   }
-  const int nt = column_tiles(step.n, step.B, G), blocks = attend_blocks(type == TQ_Q_F32, c.D, nt);
-  const int ctas = blocks * sms < kAttendCtas ? blocks * sms : kAttendCtas;
-  const Space sp(nt, c.D);
+  const bool f32 = type == TQ_Q_F32;
+  const int NC = columns_of(step.n, step.B, G, f32), nt = NC / 8, room = NC == 256 ? kPromptCtas : kAttendCtas;
+  const int blocks = NC == 256 ? 1 : attend_blocks(f32, c.D, nt), ctas = blocks * sms < room ? blocks * sms : room;
+  const Space sp(NC, c.D);
   char* w = static_cast<char*>(ws);
   const AttendArgs a = {int8_view(c, table, max_pages), step, Q, out, G, window, sinks, scale * 1.4426950408889634f,
                         reinterpret_cast<AttendRecord*>(w), reinterpret_cast<float4*>(w + sp.top), reinterpret_cast<float*>(w + sp.part)};
-  const bool f32 = type == TQ_Q_F32;
-  if (c.D == 64) e = f32 ? launch_attend_split_f32_64(a, nt, ctas, st) : launch_attend_split_bf16_64(a, nt, ctas, st);
+  if (NC == 256) e = launch_attend_prompt(a, c.D, ctas, st);
+  else if (c.D == 64) e = f32 ? launch_attend_split_f32_64(a, nt, ctas, st) : launch_attend_split_bf16_64(a, nt, ctas, st);
   else e = f32 ? launch_attend_split_f32_128(a, nt, ctas, st) : launch_attend_split_bf16_128(a, nt, ctas, st);
   if (e != cudaSuccess) return e;
 
@@ -198,10 +202,10 @@ cudaError_t launch_attend_int8(const tq_int8_cache& c, const void* Q, tq_qtype t
   cfg.gridDim = dim3(2 * sms);
   cfg.blockDim = dim3(kJoinWarps * 32);
   if (c.D == 64)
-    return f32 ? cudaLaunchKernelEx(&cfg, attend_join_kernel<float, 64>, a, 8 * nt, ctas)
-               : cudaLaunchKernelEx(&cfg, attend_join_kernel<__nv_bfloat16, 64>, a, 8 * nt, ctas);
-  return f32 ? cudaLaunchKernelEx(&cfg, attend_join_kernel<float, 128>, a, 8 * nt, ctas)
-             : cudaLaunchKernelEx(&cfg, attend_join_kernel<__nv_bfloat16, 128>, a, 8 * nt, ctas);
+    return f32 ? cudaLaunchKernelEx(&cfg, attend_join_kernel<float, 64>, a, NC, ctas)
+               : cudaLaunchKernelEx(&cfg, attend_join_kernel<__nv_bfloat16, 64>, a, NC, ctas);
+  return f32 ? cudaLaunchKernelEx(&cfg, attend_join_kernel<float, 128>, a, NC, ctas)
+             : cudaLaunchKernelEx(&cfg, attend_join_kernel<__nv_bfloat16, 128>, a, NC, ctas);
 }
 
 cudaError_t take_faults_int8_attend(unsigned int* bits) {
@@ -209,6 +213,7 @@ cudaError_t take_faults_int8_attend(unsigned int* bits) {
   if (e == cudaSuccess) e = take_faults_attend_bf16_128(bits);
   if (e == cudaSuccess) e = take_faults_attend_f32_64(bits);
   if (e == cudaSuccess) e = take_faults_attend_f32_128(bits);
+  if (e == cudaSuccess) e = take_faults_attend_prompt(bits);
   return e;
 }
 

@@ -29,6 +29,7 @@
 namespace tq {
 
 constexpr int kAttendCtas = 480;      // room for the parts of this many blocks
+constexpr int kPromptCtas = 160;      // of the prompts' form
 constexpr int kAttendWarps = 4;
 constexpr int kTileSlots = 32, kQuadTiles = kAttendWarps;
 
@@ -59,6 +60,8 @@ cudaError_t launch_attend_split_bf16_64(const AttendArgs& a, int nt, int ctas, c
 cudaError_t launch_attend_split_bf16_128(const AttendArgs& a, int nt, int ctas, cudaStream_t st);
 cudaError_t launch_attend_split_f32_64(const AttendArgs& a, int nt, int ctas, cudaStream_t st);
 cudaError_t launch_attend_split_f32_128(const AttendArgs& a, int nt, int ctas, cudaStream_t st);
+cudaError_t launch_attend_prompt(const AttendArgs& a, int D, int ctas, cudaStream_t st);
+cudaError_t take_faults_attend_prompt(unsigned int* bits);
 cudaError_t take_faults_attend_bf16_64(unsigned int* bits);
 cudaError_t take_faults_attend_bf16_128(unsigned int* bits);
 cudaError_t take_faults_attend_f32_64(unsigned int* bits);
@@ -122,6 +125,98 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, const Run& r, int c
   if (s.lo > s.hi) s.tiles = s.sunk;
   return s;
 }
+
+// A block's share of all quads: [x, x1), from quad pos of sequence b on.
+template <int kWarps>
+struct ShareScan {
+  int64_t sums[kWarps];
+  int64_t base;
+  int b;
+  Plan plan;
+};
+
+template <int NC, int kWarps>
+struct Share {
+  int64_t chunk, x, x1, pos;
+  int b;
+  Plan plan;
+
+  // The quads of all sequences are counted (as many at a time as there are threads), then the sequence that the share starts in
+  // is looked for.  All threads of the block take part; false, and the record says so, where nothing is left.
+  __device__ __forceinline__ bool find(const AttendArgs& a, ShareScan<kWarps>& scan) {
+    constexpr int kAt = kWarps * 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.step.B;
+    int64_t own, upto;              // quads of this thread's sequence; of those up to it, within the round
+    auto count = [&](int b0) {
+      own = 0;
+      if (b0 + tid < B) {
+        plan = plan_of<NC>(a, b0 + tid);
+        own = plan.quads * plan.ncb * a.c.H;
+      }
+      upto = own;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      __syncthreads();
+      if (lane == 31) scan.sums[warp] = upto;
+      __syncthreads();
+      int64_t sum = 0;
+      for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) upto += scan.sums[i];
+        sum += scan.sums[i];
+      }
+      return sum;
+    };
+    int64_t sum0 = count(0), all = sum0;
+    for (int b0 = kAt; b0 < B; b0 += kAt) all += count(b0);
+    chunk = (all + gridDim.x - 1) / gridDim.x;
+    x = chunk * blockIdx.x;
+    x1 = min(x + chunk, all);
+    if (x >= x1) {
+      if (tid == 0) a.rec[blockIdx.x].off = 0;
+      return false;
+    }
+    int64_t base = 0;
+    for (int b0 = 0;; b0 += kAt) {
+      if (B > kAt) sum0 = count(b0);
+      const int64_t lo = base + upto - own;
+      if (lo <= x && x < lo + own) {
+        scan.b = b0 + tid;
+        scan.base = lo;
+        scan.plan = plan;
+      }
+      base += sum0;
+      if (base > x) break;          // the same for all threads
+    }
+    __syncthreads();
+    b = scan.b;
+    plan = scan.plan;
+    pos = x - scan.base;
+    return true;
+  }
+
+  // The sequence, head and column block at pos: quads [qa, qe) of the unit are this share's.
+  __device__ __forceinline__ void unit(const AttendArgs& a, int& h, int& cb, int64_t& qa, int64_t& qe) {
+    while (pos >= plan.quads * plan.ncb * a.c.H) {
+      pos -= plan.quads * plan.ncb * a.c.H;
+      plan = plan_of<NC>(a, ++b);
+    }
+    const int64_t u = pos / plan.quads;
+    qa = pos - u * plan.quads;
+    qe = min(plan.quads, qa + (x1 - x));
+    h = static_cast<int>(u / plan.ncb);
+    cb = static_cast<int>(u - static_cast<int64_t>(h) * plan.ncb);
+  }
+  __device__ __forceinline__ void advance(int64_t quads) {
+    x += quads;
+    pos += quads;
+  }
+  __device__ __forceinline__ AttendRecord record(int h, int cb, int64_t qa) const {
+    return {static_cast<int>(min(chunk, static_cast<int64_t>(1) << 30)), static_cast<int>(qa), static_cast<int>(plan.quads),
+            plan.r.first, plan.r.count, h, cb, static_cast<int>(blockIdx.x)};
+  }
+};
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
@@ -202,65 +297,17 @@ __global__ void __launch_bounds__(kAttendWarps * 32, (attend_blocks(sizeof(T) ==
   using S = Shape<T, D, NT>;
   constexpr int NC = S::NC, MT = S::kTiles, kStages = S::kStages;
   extern __shared__ __align__(128) char smem[];
-  __shared__ int64_t scan_of[kAttendWarps];
-  __shared__ int64_t found_base;
-  __shared__ int found_b;
-  __shared__ Plan found_plan;
+  __shared__ ShareScan<kAttendWarps> scan;
   __shared__ float4 stage_ex[kAttendWarps][kStages];      // of the two blocks: 2^(key's exponent), 0 for an absent one; value's exponent
   __shared__ float3 warp_top[kAttendWarps][NC];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const int B = a.step.B, H = a.c.H;
+  const int H = a.c.H;
 
-  // ---- this block's share: the quads of all sequences counted (128 at a time), then the sequence that the share starts in
-  constexpr int kAt = kAttendWarps * 32;
-  Plan plan;
-  int64_t own, upto;              // quads of this thread's sequence; of those up to it, within the 128
-  auto count = [&](int b0) {
-    own = 0;
-    if (b0 + tid < B) {
-      plan = plan_of<NC>(a, b0 + tid);
-      own = plan.quads * plan.ncb * H;
-    }
-    upto = own;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += y;
-    }
-    __syncthreads();
-    if (lane == 31) scan_of[warp] = upto;
-    __syncthreads();
-    int64_t sum = 0;
-    for (int i = 0; i < kAttendWarps; ++i) {
-      if (i < warp) upto += scan_of[i];
-      sum += scan_of[i];
-    }
-    return sum;
-  };
-  int64_t sum0 = count(0), all = sum0;
-  for (int b0 = kAt; b0 < B; b0 += kAt) all += count(b0);
-  const int64_t chunk = (all + gridDim.x - 1) / gridDim.x;
-  const int64_t x0 = chunk * blockIdx.x, x1 = min(x0 + chunk, all);
-  if (x0 >= x1) {
-    if (tid == 0) a.rec[blockIdx.x].off = 0;
-    return;
-  }
-  int64_t base = 0;
-  for (int b0 = 0;; b0 += kAt) {
-    if (B > kAt) sum0 = count(b0);
-    const int64_t lo = base + upto - own;
-    if (lo <= x0 && x0 < lo + own) {
-      found_b = b0 + tid;
-      found_base = lo;
-      found_plan = plan;
-    }
-    base += sum0;
-    if (base > x0) break;         // the same for all threads
-  }
-  __syncthreads();
-  int b = found_b;
-  plan = found_plan;
-  int64_t pos = x0 - found_base;  // quads into sequence b
+  Share<NC, kAttendWarps> share;
+  if (!share.find(a, scan)) return;
+  const Plan& plan = share.plan;
+  const int& b = share.b;
 
   const uint32_t ring = smem_addr(smem) + warp * kStages * S::kStage;
   const uint32_t q_area = smem_addr(smem) + S::kBytes - S::kQBytes;
@@ -272,18 +319,15 @@ __global__ void __launch_bounds__(kAttendWarps * 32, (attend_blocks(sizeof(T) ==
   const uint32_t k_at = D == 128 ? g * 128 : (g >> 1) * 128;
   const int k_chunk = D == 128 ? t : (g & 1) * 4 + t;
 
-  for (int64_t x = x0; x < x1;) {
-    while (pos >= plan.quads * plan.ncb * H) {
-      pos -= plan.quads * plan.ncb * H;
-      plan = plan_of<NC>(a, ++b);
-    }
-    const int64_t unit = pos / plan.quads, qa = pos - unit * plan.quads, qe = min(plan.quads, qa + (x1 - x));
-    const int h = static_cast<int>(unit / plan.ncb), cb = static_cast<int>(unit - static_cast<int64_t>(h) * plan.ncb);
+  bool begun = false;
+  while (share.x < share.x1) {
+    int h, cb;
+    int64_t qa, qe;
+    share.unit(a, h, cb, qa, qe);
     const Span sp = span_of<NC>(a, plan.r, cb);
     const Run run = plan.r;
-    if (tid == 0 && x == x0) 
-      a.rec[blockIdx.x] = {static_cast<int>(min(chunk, static_cast<int64_t>(1) << 30)), static_cast<int>(qa), static_cast<int>(plan.quads),
-                           run.first, run.count, h, cb, static_cast<int>(blockIdx.x)};
+    if (tid == 0 && !begun) a.rec[blockIdx.x] = share.record(h, cb, qa);
+    begun = true;
 
     // ---- the warp's tiles: 4 q + warp for quads q in [qa, qe)
     const int n = max(0, static_cast<int>(min(qe, (static_cast<int64_t>(sp.tiles) - warp + 3) / 4) - qa));
@@ -669,8 +713,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, (attend_blocks(sizeof(T) ==
         *reinterpret_cast<float2*>(a.part + (place + col) * D + 2 * pair) = o;
       }
     }
-    x += qe - qa;
-    pos += qe - qa;
+    share.advance(qe - qa);
   }
 }
 

@@ -115,7 +115,7 @@ def device_faults() -> int:
     """Fault bits the bounded waits of libtq's kernels set on the current device since the
     last call (0 = none; 1 lookup-table scorers, 2 tensor-core scorer, 4 decode, 8
     compressor, 16 check_wait_expiry, 32 a length, slot or page number out of range in a paged
-    call, 64 append_paged); reading clears them.  Synchronises with the device."""
+    call, 64 append_paged, 128 attend_int8); reading clears them.  Synchronises with the device."""
     v = ctypes.c_uint(0)
     _check("tq_device_faults", lib().tq_device_faults(ctypes.byref(v)))
     return int(v.value)
