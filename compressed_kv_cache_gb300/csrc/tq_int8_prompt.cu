@@ -37,6 +37,11 @@ __device__ __forceinline__ void arrive(uint32_t bar) {
 __device__ __forceinline__ void commit_to(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void operands_written() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -61,19 +66,27 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
                "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
                : "memory");
 }
+// The load is under way until tmem_loaded(), which its values have to pass.
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
-  uint32_t r[32];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
       "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]),
-        "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-        "=r"(r[31])
-      : "r"(addr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]),
+        "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]),
+        "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]),
+        "=f"(v[31])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_loaded(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]),
+                 "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]),
+                 "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]),
+                 "+f"(v[28])
+               :
+               : "memory");
+  asm volatile("" : "+f"(v[29]), "+f"(v[30]), "+f"(v[31])::"memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -90,6 +103,10 @@ struct BlockInfo {
   float ek, ev;
   int blk;
 };
+// Of all eight: lowest slot, highest, whether all are there.
+struct TileInfo {
+  int lo, hi, all;
+};
 
 template <int D>
 struct PromptShape {
@@ -105,10 +122,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
   extern __shared__ char smem_raw[];
   __shared__ ShareScan<kWarps> scan;
   __shared__ BlockInfo info[P::kInfo][kBatch * 8];
+  __shared__ TileInfo tile_info[P::kInfo][kBatch];
   __shared__ __align__(8) uint64_t bars[21];
   __shared__ uint32_t tmem_slot;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   const uint32_t base = smem_addr(smem);
   // barriers: keys full / free, values full / free (2 stages each), queries, logits, weights, products done (2 halves each), infos (4)
@@ -140,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
   before_sync();
   __syncthreads();
   after_sync();
-  const uint32_t tmem = tmem_slot;      // logits (and weights) of the halves at 0 and 128, sums at 256 and 384
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);      // logits (and weights) of the halves at 0 and 128, sums at 256 and 384
 
   bool lost = false, begun = false;
   auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -162,42 +180,51 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
     const int n = max(0, static_cast<int>(min(qe, static_cast<int64_t>((sp.tiles + 3) / 4)) - qa));
 
     if (warp >= 12) {
-      // ---- the products
-      if (lane == 0 && n > 0) {
-        auto logits = [&](int i, int half) {
-          const uint32_t k = base + P::kK + ((tiles_done + i) & 1) * P::kSide, q = base + P::kQ + half * P::kSide;
-          after_sync();
-#pragma unroll
-          for (int s = 0; s < D / 16; ++s) {
-            const uint32_t at = (s >> 2) * P::kPart + (s & 3) * 32;
-            mma_ss(tmem + half * 128, operand(q + at, 16), operand(k + at, 16), shape_of(kTileKeys, false), s > 0);
-          }
-          commit_to(s_full + 8 * half);
+      // ---- the products: the whole warp keeps step, so that operands stay in its uniform registers; one lane issues
+      if (n > 0) {
+        auto wait_all = [&](uint32_t bar, uint32_t parity) {
+          wait(bar, parity);
+          lost = __any_sync(0xffffffffu, lost);
         };
-        auto k_there = [&](int i) { wait(k_full + 8 * ((tiles_done + i) & 1), (tiles_done + i) >> 1); };
+        auto logits = [&](int i, int half) {
+          const uint64_t kd = operand(base + P::kK + ((tiles_done + i) & 1) * P::kSide, 16), qd = operand(base + P::kQ + half * P::kSide, 16);
+          after_sync();
+          if (elected()) {
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s) {
+              const uint32_t at = ((s >> 2) * P::kPart + (s & 3) * 32) >> 4;      // operands are below 2^18: no carry
+              mma_ss(tmem + half * 128, qd + at, kd + at, shape_of(kTileKeys, false), s > 0);
+            }
+            commit_to(s_full + 8 * half);
+            if (half == halves - 1) commit_to(k_free + 8 * ((tiles_done + i) & 1));
+          }
+          __syncwarp();
+        };
+        auto k_there = [&](int i) { wait_all(k_full + 8 * ((tiles_done + i) & 1), (tiles_done + i) >> 1); };
         k_there(0);
         for (int half = 0; half < halves; ++half) {
-          wait(q_full + 8 * half, units_done[half]);
+          wait_all(q_full + 8 * half, units_done[half]);
           if (!lost) logits(0, half);
         }
-        if (!lost) commit_to(k_free + 8 * (tiles_done & 1));
         for (int i = 0; i < n && !lost; ++i) {
-          const uint32_t v = base + P::kV + ((tiles_done + i) & 1) * P::kSide;
-          wait(v_full + 8 * ((tiles_done + i) & 1), (tiles_done + i) >> 1);
+          const uint64_t vd = operand(base + P::kV + ((tiles_done + i) & 1) * P::kSide, P::kPart);
+          wait_all(v_full + 8 * ((tiles_done + i) & 1), (tiles_done + i) >> 1);
           for (int half = 0; half < halves; ++half) {
-            wait(p_full + 8 * half, half_tiles[half] + i);
+            wait_all(p_full + 8 * half, half_tiles[half] + i);
             if (lost) break;
             after_sync();
+            if (elected()) {
 #pragma unroll
-            for (int s = 0; s < kTileKeys / 16; ++s)
-              mma_ts(tmem + 256 + half * 128, tmem + half * 128 + s * 8, operand(v + s * 2048, P::kPart), shape_of(D, true), i > 0 || s > 0);
-            commit_to(o_done + 8 * half);
-            if (half == halves - 1) commit_to(v_free + 8 * ((tiles_done + i) & 1));
+              for (int s = 0; s < kTileKeys / 16; ++s)
+                mma_ts(tmem + 256 + half * 128, tmem + half * 128 + s * 8, vd + s * 128, shape_of(D, true), i > 0 || s > 0);
+              commit_to(o_done + 8 * half);
+              if (half == halves - 1) commit_to(v_free + 8 * ((tiles_done + i) & 1));
+            }
+            __syncwarp();
             if (i + 1 < n) {
               if (half == 0) k_there(i + 1);
               if (lost) break;
               logits(i + 1, half);
-              if (half == halves - 1) commit_to(k_free + 8 * ((tiles_done + i + 1) & 1));
             }
           }
         }
@@ -227,6 +254,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             }
           }
           to = f;
+          int lo = f.slot, hi = f.slot + kBlockSlots - 1, all = f.ek != 0.0f;
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) {
+            lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+            hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+            all &= __shfl_xor_sync(0xffffffffu, all, o);
+          }
+          if ((me & 7) == 0) tile_info[batch & 3][me / 8] = {lo, hi, all};
           arrive(info_full + 8 * (batch & 3));
           wait(info_full + 8 * (batch & 3), batch >> 2);
         }
@@ -343,23 +378,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         if (lost) break;
         after_sync();
         const BlockInfo* f = info[batch & 3] + (i % kBatch) * 8;
-        bool plain = true;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int s = f[k].slot;
-          plain = plain && f[k].ek != 0.0f && s + kBlockSlots - 1 <= own && (a.window <= 0 || s > own - a.window || s + kBlockSlots <= a.sinks);
-        }
+        const TileInfo ti = tile_info[batch & 3][i % kBatch];
+        bool plain = ti.all && ti.hi <= own && (a.window <= 0 || ti.lo > own - a.window || ti.hi < a.sinks);
         plain = __all_sync(0xffffffffu, plain || !there);
         auto seen = [&](int k, int c) {
           const int s = f[k].slot + c;
           return f[k].ek != 0.0f && s <= own && (a.window <= 0 || s > own - a.window || s < a.sinks);
         };
-        // largest logits of the blocks
+        // largest logits of the blocks, two at a time; the next two are on their way meanwhile.  (Loops are kept short: the
+        // warps' programs share an instruction cache.)
         float top = -INFINITY, topv = -INFINITY;
-#pragma unroll
-        for (int c4 = 0; c4 < 4; ++c4) {
-          float z[32];
-          tmem_ld32(s_at + 32 * c4, z);
+        float za[32], zb[32];
+        auto largest = [&](const float (&z)[32], int c4) {
 #pragma unroll
           for (int k2 = 0; k2 < 2; ++k2) {
             const int k = 2 * c4 + k2;
@@ -375,6 +405,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             top = fmaxf(top, v);
             topv = fmaxf(topv, v + f[k].ev);
           }
+        };
+        tmem_ld32(s_at, za);
+#pragma unroll 1
+        for (int c4 = 0; c4 < 4; c4 += 2) {
+          tmem_loaded(za);
+          tmem_ld32(s_at + 32 * c4 + 32, zb);
+          largest(za, c4);
+          tmem_loaded(zb);
+          tmem_ld32(s_at + (c4 == 0 ? 64 : 0), za);      // the first again, for the weights
+          largest(zb, c4 + 1);
         }
         const bool over = top > m + kSlack || topv > M + kSlack;
         if (__any_sync(0xffffffffu, over)) {
@@ -388,10 +428,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             lost = __any_sync(0xffffffffu, lost);
             if (lost) break;
             after_sync();
-#pragma unroll
+            tmem_loaded(za);
+#pragma unroll 1
             for (int c4 = 0; c4 < D / 32; ++c4) {
               float o[32];
               tmem_ld32(o_at + 32 * c4, o);
+              tmem_loaded(o);
               uint32_t w[2][16];
 #pragma unroll
               for (int c = 0; c < 32; ++c) w[c >> 4][c & 15] = __float_as_uint(o[c] * fv);
@@ -406,30 +448,53 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
 #pragma unroll
         for (int k = 0; k < 8; ++k) ratio = fmaxf(ratio, m + f[k].ev - M);
         const bool quick = plain && !__any_sync(0xffffffffu, ratio > 100.0f);
-#pragma unroll
-        for (int c4 = 0; c4 < 4; ++c4) {
-          float z[32];
-          tmem_ld32(s_at + 32 * c4, z);
+        float more = 0.0f;
+        auto weigh = [&](const float (&z)[32], int c4) {
           uint32_t w[16];
 #pragma unroll
           for (int k2 = 0; k2 < 2; ++k2) {
             const int k = 2 * c4 + k2;
-            const float scale = factor * f[k].ek, at = half_sum * scale;
-            if (quick) {
-              const float up = exp2_fast(m + f[k].ev - M + kLift);
+            const float scale = factor * f[k].ek, at = half_sum * scale - m, up = exp2_fast(m + f[k].ev - M + kLift);
 #pragma unroll
-              for (int c = 0; c < 16; c += 2) {
-                const float p0 = exp2_fast(fmaf(z[16 * k2 + c], scale, at - m)), p1 = exp2_fast(fmaf(z[16 * k2 + c + 1], scale, at - m));
-                sum += p0 + p1;
-                w[8 * k2 + c / 2] = pack(p0 * up, p1 * up);
-              }
-            } else {
+            for (int c = 0; c < 16; c += 2) {
+              const float p0 = exp2_fast(fmaf(z[16 * k2 + c], scale, at)), p1 = exp2_fast(fmaf(z[16 * k2 + c + 1], scale, at));
+              sum += p0;
+              more += p1;
+              w[8 * k2 + c / 2] = pack(p0 * up, p1 * up);
+            }
+          }
+          tmem_st16(s_at + 16 * c4, w);      // over logits that have been read
+        };
+        if (quick) {
+#pragma unroll 1
+          for (int c4 = 0; c4 < 4; c4 += 2) {
+            tmem_loaded(za);
+            tmem_ld32(s_at + 32 * c4 + 32, zb);
+            weigh(za, c4);
+            tmem_loaded(zb);
+            if (c4 == 0) tmem_ld32(s_at + 64, za);
+            weigh(zb, c4 + 1);
+          }
+          sum += more;
+        } else {
+          tmem_loaded(za);
+#pragma unroll 1
+          for (int c4 = 0; c4 < 4; ++c4) {
+            if (c4 > 0) {
+              tmem_ld32(s_at + 32 * c4, za);
+              tmem_loaded(za);
+            }
+            uint32_t w[16];
+#pragma unroll
+            for (int k2 = 0; k2 < 2; ++k2) {
+              const int k = 2 * c4 + k2;
+              const float scale = factor * f[k].ek;
 #pragma unroll
               for (int c = 0; c < 16; c += 2) {
                 float q[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                  const float v = (z[16 * k2 + c + e] + half_sum) * scale;
+                  const float v = (za[16 * k2 + c + e] + half_sum) * scale;
                   const bool on = seen(k, c + e);
                   sum += on ? exp2_fast(v - m) : 0.0f;
                   q[e] = on ? exp2_fast(v + (f[k].ev + kLift - M)) : 0.0f;
@@ -437,8 +502,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                 w[8 * k2 + c / 2] = pack(q[0], q[1]);
               }
             }
+            tmem_st16(s_at + 16 * c4, w);
           }
-          tmem_st16(s_at + 16 * c4, w);      // over logits that have been read
         }
         tmem_stored();
         before_sync();
@@ -454,11 +519,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
       const float nan = __int_as_float(0x7fffffff);
       const float f = lost ? nan : sum == 0.0f ? 0.0f : exp2f(M - m - kLift - 1.0f) / sum;
       if (!entire && there) a.top[place] = make_float4(m, M, lost ? nan : sum, 0.0f);
-#pragma unroll
+#pragma unroll 1
       for (int c4 = 0; c4 < D / 32; ++c4) {
         float o[32];
         if (n > 0 && !lost) {
           tmem_ld32(o_at + 32 * c4, o);
+          tmem_loaded(o);
         } else {
 #pragma unroll
           for (int c = 0; c < 32; ++c) o[c] = 0.0f;
@@ -494,10 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
     share.advance(qe - qa);
   }
   if (warp == 12) {
-    if (lane == 0) {              // nothing is in flight, whatever ran out
-      commit_to(drained);
-      wait_parity_bounded(drained, 0, kFaultAttendWait);
-    }
+    if (elected()) commit_to(drained);      // nothing is in flight, whatever ran out
+    wait_parity_bounded(drained, 0, kFaultAttendWait);
     __syncwarp();
   }
   before_sync();
