@@ -16,8 +16,9 @@ constexpr float kLifted = 7.0f;      // weights were taken 2^7 above their range
 // columns.  Many columns: a warp each.  Few (one long sequence): a block each, its warps taking every eighth part, so
 // that all parts are on their way at once.  A lane holds D / 32 dimensions.
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const AttendArgs a, int NC, int ctas) {
+__global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const AttendArgs a, int nc_log2, int ctas) {
   constexpr int kDims = D / 32;
+  const int NC = 1 << nc_log2;
   __shared__ AttendRecord records[kAttendCtas];
   __shared__ int warp_count[kJoinWarps];
   __shared__ float4 warp_top[kJoinWarps];
@@ -57,10 +58,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
   const bool shared = items < static_cast<int>(gridDim.x) * 2;      // a block an item
   const int step = shared ? kJoinWarps : 1, w0 = shared ? warp : 0;
   for (int item = shared ? blockIdx.x : blockIdx.x * kJoinWarps + warp; item < items; item += gridDim.x * (shared ? 1 : kJoinWarps)) {
-    const AttendRecord r = records[item / NC];
-    const int i = r.block, col = item % NC;
-    const int64_t cc = static_cast<int64_t>(r.cb) * NC + col;
-    if (cc >= static_cast<int64_t>(r.count) * a.G) continue;
+    const AttendRecord& r = records[item >> nc_log2];
+    const int i = r.block, col = item & (NC - 1), cc = r.cb * NC + col;      // all columns of a step are below 2^31
+    if (cc >= r.count * a.G) continue;
     const int pieces = 1 + (r.quads - r.off + r.chunk - 1) / r.chunk;
     float mt = -3.4e38f, Mt = -3.4e38f, l = 0.0f, acc[kDims];
 #pragma unroll
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
       }
     }
     const float f = 1.0f / l, up = exp2f(Mt - mt - kLifted);
-    const int token = static_cast<int>(cc / a.G), head = static_cast<int>(cc - static_cast<int64_t>(token) * a.G);
+    const int token = static_cast<unsigned>(cc) / static_cast<unsigned>(a.G), head = cc - token * a.G;
     T* to = static_cast<T*>(a.out) + ((static_cast<size_t>(r.first) + token) * a.c.H * a.G + static_cast<size_t>(r.h) * a.G + head) * D + lane * kDims;
 #pragma unroll
     for (int d = 0; d < kDims; ++d) {
@@ -192,6 +192,8 @@ cudaError_t launch_attend_int8(const tq_int8_cache& c, const void* Q, tq_qtype t
   else e = f32 ? launch_attend_split_f32_128(a, nt, ctas, st) : launch_attend_split_bf16_128(a, nt, ctas, st);
   if (e != cudaSuccess) return e;
 
+  int nc_log2 = 3;
+  while (1 << nc_log2 < NC) ++nc_log2;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -202,10 +204,10 @@ cudaError_t launch_attend_int8(const tq_int8_cache& c, const void* Q, tq_qtype t
   cfg.gridDim = dim3(2 * sms);
   cfg.blockDim = dim3(kJoinWarps * 32);
   if (c.D == 64)
-    return f32 ? cudaLaunchKernelEx(&cfg, attend_join_kernel<float, 64>, a, NC, ctas)
-               : cudaLaunchKernelEx(&cfg, attend_join_kernel<__nv_bfloat16, 64>, a, NC, ctas);
-  return f32 ? cudaLaunchKernelEx(&cfg, attend_join_kernel<float, 128>, a, NC, ctas)
-             : cudaLaunchKernelEx(&cfg, attend_join_kernel<__nv_bfloat16, 128>, a, NC, ctas);
+    return f32 ? cudaLaunchKernelEx(&cfg, attend_join_kernel<float, 64>, a, nc_log2, ctas)
+               : cudaLaunchKernelEx(&cfg, attend_join_kernel<__nv_bfloat16, 64>, a, nc_log2, ctas);
+  return f32 ? cudaLaunchKernelEx(&cfg, attend_join_kernel<float, 128>, a, nc_log2, ctas)
+             : cudaLaunchKernelEx(&cfg, attend_join_kernel<__nv_bfloat16, 128>, a, nc_log2, ctas);
 }
 
 cudaError_t take_faults_int8_attend(unsigned int* bits) {

@@ -13,7 +13,7 @@
 //
 // Warps: 0-3 and 4-7 the two halves' columns (weights, rescaling, output), 8-11 bring the codes from memory and lay them
 // out as operands (128-byte swizzle; keys with the dimension, values with the slot as the outer index), 12 issues the
-// products.  Weights go to tensor memory over the logits that they come from and are read there as an operand.
+// products (13-15 only give up registers: 168 a thread for the columns, 104 for the codes, 72 here, 65536 in all).  Weights go to tensor memory over the logits that they come from and are read there as an operand.
 // Two stages of keys and of values; the next tile's codes are on their way in registers while a stage is waited for.
 //
 // Every wait gives up after the library's budget: the block then writes NaN for what it has not done, sets fault bit 128,
@@ -25,7 +25,7 @@ namespace tq {
 namespace {
 
 constexpr int kHalf = 128, kNC = 2 * kHalf, kTileKeys = 128, kBatch = 16;
-constexpr int kWarps = 13, kThreads = kWarps * 32, kMakers = 128;
+constexpr int kWarps = 16, kThreads = kWarps * 32, kMakers = 128;
 constexpr unsigned int kFaultAttendWait = 128u;
 
 __device__ __forceinline__ void bar_init(uint32_t bar, int count) {
@@ -97,15 +97,38 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
 }
 __device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Two fp32 values an instruction.
+__device__ __forceinline__ uint64_t two(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float2 apart(uint64_t v) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // What the columns' threads need of a tile's eight blocks: first slot, 2^(key's exponent) (0: absent), value's exponent.
-struct BlockInfo {
+struct alignas(16) BlockInfo {
   int slot;
   float ek, ev;
   int blk;
 };
-// Of all eight: lowest slot, highest, whether all are there.
-struct TileInfo {
-  int lo, hi, all;
+// Of all eight: lowest slot, highest (2^31 - 1 unless all are there), least and largest exponent of the values.
+struct alignas(16) TileInfo {
+  int lo, hi;
+  float ev_lo, ev_hi;
 };
 
 template <int D>
@@ -126,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
   __shared__ __align__(8) uint64_t bars[21];
   __shared__ uint32_t tmem_slot;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   const uint32_t base = smem_addr(smem);
   // barriers: keys full / free, values full / free (2 stages each), queries, logits, weights, products done (2 halves each), infos (4)
@@ -166,22 +189,40 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
   };
   uint32_t tiles_done = 0, batches_done = 0, units_done[2] = {0, 0}, half_tiles[2] = {0, 0};
 
-  while (share.x < share.x1) {
-    int h, cb;
-    int64_t qa, qe;
+  // The roles go through the same units, each in a loop of its own: registers are dealt out anew between them.
+  int h, cb, b, columns, halves, n;
+  int64_t qa, qe;
+  Run run;
+  Span sp;
+  auto begin = [&]() {
+    if (share.x >= share.x1) return false;
     share.unit(a, h, cb, qa, qe);
-    const Run run = share.plan.r;
-    const Span sp = span_of<kNC>(a, run, cb);
-    const int b = share.b;
+    run = share.plan.r;
+    sp = span_of<kNC>(a, run, cb);
+    b = share.b;
     if (tid == 0 && !begun) a.rec[blockIdx.x] = share.record(h, cb, qa);
     begun = true;
-    const int columns = static_cast<int>(min(static_cast<int64_t>(kNC), static_cast<int64_t>(run.count) * a.G - static_cast<int64_t>(cb) * kNC));
-    const int halves = columns > kHalf ? 2 : 1;
-    const int n = max(0, static_cast<int>(min(qe, static_cast<int64_t>((sp.tiles + 3) / 4)) - qa));
+    columns = static_cast<int>(min(static_cast<int64_t>(kNC), static_cast<int64_t>(run.count) * a.G - static_cast<int64_t>(cb) * kNC));
+    halves = columns > kHalf ? 2 : 1;
+    n = max(0, static_cast<int>(min(qe, static_cast<int64_t>((sp.tiles + 3) / 4)) - qa));
+    return true;
+  };
+  auto end = [&]() {
+    __syncwarp();
+    tiles_done += n;
+    batches_done += (n + kBatch - 1) / kBatch;
+    for (int half = 0; half < halves; ++half) {
+      units_done[half] += n > 0;
+      half_tiles[half] += n;
+    }
+    share.advance(qe - qa);
+  };
 
-    if (warp >= 12) {
+  if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    while (begin()) {
       // ---- the products: the whole warp keeps step, so that operands stay in its uniform registers; one lane issues
-      if (n > 0) {
+      if (warp == 12 && n > 0) {
         auto wait_all = [&](uint32_t bar, uint32_t parity) {
           wait(bar, parity);
           lost = __any_sync(0xffffffffu, lost);
@@ -229,11 +270,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           }
         }
       }
-    } else if (warp >= 8) {
+      end();
+    }
+  } else if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    while (begin()) {
       // ---- codes to operands
       const int me = tid - 256;
       constexpr int kPieces = D / 16, kAt = kMakers / kPieces, kIt = kTileKeys / kAt;      // 16-byte pieces a row, rows at a time, times
-      const int col = me % kPieces, sub = me / kPieces;
+      // a quarter warp's stores: four pieces of 64 columns of two rows, which the swizzle spreads over all banks
+      const int col = D == 128 ? (me & 3) | (me >> 3 & 1) << 2 : me & 3, sub = D == 128 ? (me >> 2 & 1) | (me >> 4) << 1 : me >> 2;
       for (int i = 0; i < n && !lost; ++i) {
         const uint32_t tile = tiles_done + i, stage = tile & 1, batch = batches_done + i / kBatch;
         if (i % kBatch == 0) {
@@ -254,14 +300,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             }
           }
           to = f;
-          int lo = f.slot, hi = f.slot + kBlockSlots - 1, all = f.ek != 0.0f;
+          int lo = f.slot, hi = f.ek != 0.0f ? f.slot + kBlockSlots - 1 : INT32_MAX;
+          float ev_lo = f.ev, ev_hi = f.ev;
 #pragma unroll
           for (int o = 1; o < 8; o <<= 1) {
             lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
             hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-            all &= __shfl_xor_sync(0xffffffffu, all, o);
+            ev_lo = fminf(ev_lo, __shfl_xor_sync(0xffffffffu, ev_lo, o));
+            ev_hi = fmaxf(ev_hi, __shfl_xor_sync(0xffffffffu, ev_hi, o));
           }
-          if ((me & 7) == 0) tile_info[batch & 3][me / 8] = {lo, hi, all};
+          if ((me & 7) == 0) tile_info[batch & 3][me / 8] = {lo, hi, ev_lo, ev_hi};
           arrive(info_full + 8 * (batch & 3));
           wait(info_full + 8 * (batch & 3), batch >> 2);
         }
@@ -277,19 +325,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             v[r] = __ldg(reinterpret_cast<const uint4*>(a.c.vc + at));
           }
         }
-        // 16 codes are two 16-byte chunks; lanes of the second 64 columns write theirs in the other order (banks)
-        auto put = [&](int side, int row, const uint32_t (&w)[8]) {
-          const uint32_t to = base + side + stage * P::kSide + (col >> 2) * P::kPart + row * 128;
-          const int c0 = (2 * col) & 7;
-          const int flip = col >> 2 & 1;
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int c = u ^ flip;
-            const uint32_t at = to + (((c0 + c) ^ (row & 7)) << 4);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(c ? w[4] : w[0]), "r"(c ? w[5] : w[1]), "r"(c ? w[6] : w[2]),
-                         "r"(c ? w[7] : w[3])
-                         : "memory");
-          }
+        // 16 codes are two 16-byte chunks; rows of a thread are a multiple of 8 apart
+        auto put = [&](int side, int r, const uint32_t (&w)[8]) {
+          const uint32_t to = base + side + stage * P::kSide + (col >> 2) * P::kPart + (r * kAt + sub) * 128;
+          const uint32_t c0 = static_cast<uint32_t>((2 * col & 7) ^ (sub & 7)) << 4;
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + c0), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (c0 ^ 16)), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
         };
         wait(k_free + 8 * stage, (tile >> 1) + 1);
         if (lost) break;
@@ -302,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             w[2 * u] = whole(c[u], 0x4140);
             w[2 * u + 1] = whole(c[u], 0x4342);
           }
-          put(P::kK, r * kAt + sub, w);
+          put(P::kK, r, w);
         }
         operands_written();
         arrive(k_full + 8 * stage);
@@ -319,12 +360,21 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&bias));
             w[u] = *reinterpret_cast<const uint32_t*>(&y);
           }
-          put(P::kV, r * kAt + sub, w);
+          put(P::kV, r, w);
         }
         operands_written();
         arrive(v_full + 8 * stage);
       }
-    } else if (const int half = warp >> 2; half < halves) {
+      end();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    const int half = warp >> 2;
+    while (begin()) {
+      if (half >= halves) {
+        end();
+        continue;
+      }
       // ---- a column: its query, weights, sums
       const int r = tid & 127;
       const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);
@@ -379,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         after_sync();
         const BlockInfo* f = info[batch & 3] + (i % kBatch) * 8;
         const TileInfo ti = tile_info[batch & 3][i % kBatch];
-        bool plain = ti.all && ti.hi <= own && (a.window <= 0 || ti.lo > own - a.window || ti.hi < a.sinks);
+        bool plain = ti.hi <= own && (a.window <= 0 || ti.lo > own - a.window || ti.hi < a.sinks);
         plain = __all_sync(0xffffffffu, plain || !there);
         auto seen = [&](int k, int c) {
           const int s = f[k].slot + c;
@@ -395,8 +445,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             const int k = 2 * c4 + k2;
             float best = -INFINITY;
             if (plain) {
+              float u[4];
 #pragma unroll
-              for (int c = 0; c < 16; ++c) best = fmaxf(best, z[16 * k2 + c]);
+              for (int c = 0; c < 4; ++c) u[c] = fmaxf(fmaxf(z[16 * k2 + c], z[16 * k2 + 4 + c]), fmaxf(z[16 * k2 + 8 + c], z[16 * k2 + 12 + c]));
+              best = fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3]));
             } else {
 #pragma unroll
               for (int c = 0; c < 16; ++c) best = seen(k, c) ? fmaxf(best, z[16 * k2 + c]) : best;
@@ -442,26 +494,27 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             }
           }
         }
-        // a factor for a block's weights beyond fp32's range (values 2^100 apart): two exponentials a logit then, as
-        // where slots are hidden
-        float ratio = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) ratio = fmaxf(ratio, m + f[k].ev - M);
-        const bool quick = plain && !__any_sync(0xffffffffu, ratio > 100.0f);
-        float more = 0.0f;
+        // where exponents of values are so far apart that a weight and its p do not fit one range, and where slots are hidden,
+        // two exponentials a logit
+        const float apart_by = m - M;
+        const bool quick = plain && !__any_sync(0xffffffffu, apart_by + ti.ev_hi > 100.0f || apart_by + ti.ev_lo < -60.0f);
         auto weigh = [&](const float (&z)[32], int c4) {
           uint32_t w[16];
 #pragma unroll
           for (int k2 = 0; k2 < 2; ++k2) {
-            const int k = 2 * c4 + k2;
-            const float scale = factor * f[k].ek, at = half_sum * scale - m, up = exp2_fast(m + f[k].ev - M + kLift);
+            const BlockInfo& at = f[2 * c4 + k2];
+            const float scale = factor * at.ek, up = at.ev - M + kLift, shift = fmaf(half_sum, scale, up);
+            const uint64_t scale2 = two(scale, scale), off = two(shift, shift);
+            uint64_t all = two(0.0f, 0.0f);
 #pragma unroll
             for (int c = 0; c < 16; c += 2) {
-              const float p0 = exp2_fast(fmaf(z[16 * k2 + c], scale, at)), p1 = exp2_fast(fmaf(z[16 * k2 + c + 1], scale, at));
-              sum += p0;
-              more += p1;
-              w[8 * k2 + c / 2] = pack(p0 * up, p1 * up);
+              const float2 v = apart(fma2(two(z[16 * k2 + c], z[16 * k2 + c + 1]), scale2, off));
+              const float w0 = exp2_fast(v.x), w1 = exp2_fast(v.y);
+              all = add2(all, two(w0, w1));
+              w[8 * k2 + c / 2] = pack(w0, w1);
             }
+            const float2 sums = apart(all);
+            sum = fmaf(sums.x + sums.y, exp2_fast(-m - up), sum);      // p is the weight less its block's factor
           }
           tmem_st16(s_at + 16 * c4, w);      // over logits that have been read
         };
@@ -475,7 +528,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             if (c4 == 0) tmem_ld32(s_at + 64, za);
             weigh(zb, c4 + 1);
           }
-          sum += more;
         } else {
           tmem_loaded(za);
 #pragma unroll 1
@@ -549,15 +601,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         }
         __syncwarp();
       }
+      end();
     }
-    __syncwarp();
-    tiles_done += n;
-    batches_done += (n + kBatch - 1) / kBatch;
-    for (int half = 0; half < halves; ++half) {
-      units_done[half] += n > 0;
-      half_tiles[half] += n;
-    }
-    share.advance(qe - qa);
   }
   if (warp == 12) {
     if (elected()) commit_to(drained);      // nothing is in flight, whatever ran out
