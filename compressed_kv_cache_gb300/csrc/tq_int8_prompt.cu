@@ -6,14 +6,18 @@
 // 2 c + 1, odd below 256 and exact in fp16, which saves the sum of weights.  The weights of 16 slots are p times
 // one factor 2^(e - M + m).
 //
-// What bounds it: a tile of 128 slots is 2 x 2 products of 128 x 128 x D (2048 cycles of the tensor core for
-// D = 128), 32768 exponentials (2048 cycles at 16 a cycle) and about 1800 cycles of issue: conversion of the codes (2.5
-// instructions a code) and 5.5 instructions a logit.  256 columns share a conversion; their halves alternate, so that one
-// half's products run under the other's weights.
+// What bounds it: a tile of 128 slots is 2 x 2 products of 128 x 128 x D (2048 cycles of the tensor core for D = 128)
+// and 32768 exponentials (2048 cycles at 16 a cycle).  What it takes is 5200 cycles, the way of one half from its logits to its next
+// ones: 1700 for the maxima, 1700 for the weights, 1700 for the two products and the barriers between; the other half's runs
+// beside it and the tensor core is busy for 40 % of them.  256 columns share a conversion of the codes (800 cycles a side).
+// 1021 tokens over 8192 slots, 32 heads on 8: 209 us with the join (20), 615 TFLOP/s; the warp-wide form 700 us.
+// Weights with the maxima so far, kept in registers until they are known to hold, would read the logits once: 250 us,
+// as registers no longer suffice; one lane that waits and arrives for its warp: 245 us.
 //
 // Warps: 0-3 and 4-7 the two halves' columns (weights, rescaling, output), 8-11 bring the codes from memory and lay them
 // out as operands (128-byte swizzle; keys with the dimension, values with the slot as the outer index), 12 issues the
-// products (13-15 only give up registers: 168 a thread for the columns, 104 for the codes, 72 here, 65536 in all).  Weights go to tensor memory over the logits that they come from and are read there as an operand.
+// products (13-15 only give up registers: 144 a thread for the columns, 112 for the others, 65536 in all; with fewer for the
+// others their loops spill).  Weights go to tensor memory over the logits that they come from and are read there as an operand.
 // Two stages of keys and of values; the next tile's codes are on their way in registers while a stage is waited for.
 //
 // Every wait gives up after the library's budget: the block then writes NaN for what it has not done, sets fault bit 128,
@@ -219,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
   };
 
   if (warp >= 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
     while (begin()) {
       // ---- the products: the whole warp keeps step, so that operands stay in its uniform registers; one lane issues
       if (warp == 12 && n > 0) {
@@ -273,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
       end();
     }
   } else if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
     while (begin()) {
       // ---- codes to operands
       const int me = tid - 256;
@@ -368,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
       end();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
     const int half = warp >> 2;
     while (begin()) {
       if (half >= halves) {
