@@ -531,7 +531,7 @@ tq_status tq_attend_int8(const tq_int8_cache* cache, const void* Q, tq_qtype typ
   tq_status st = check_int8(cache, starts, lengths, page_table, n, B, max_pages);
   if (st != TQ_OK) return st;
   if (bad_type(type) || window < 0 || sinks < 0 || !std::isfinite(scale)) return TQ_ERR_INVALID_VALUE;
-  if (G < 1 || G > kMaxGridYZ || static_cast<int64_t>(n) * cache->H * G > INT_MAX) return TQ_ERR_INVALID_VALUE;
+  if (G < 1 || G > kMaxGridYZ || static_cast<int64_t>(n) * cache->H * G > INT_MAX - 4096) return TQ_ERR_INVALID_VALUE;
   if (n == 0) return TQ_OK;
   if ((st = check_ptrs(Q, out)) != TQ_OK) return st;
   if (workspace == nullptr) return TQ_ERR_WORKSPACE;

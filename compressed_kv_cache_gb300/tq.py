@@ -760,7 +760,7 @@ def norm_rope(q, k, positions, rotary: Rotary, q_weight=None, k_weight=None, eps
             wtype = t.dtype
         weights.append(None if t is None else _on(dev, t, name, t.dtype, (D,)))
     if out is None:
-        out = q.new_empty((n, Hq, D)), None if k is None else q.new_empty((n, Hk, D))
+        out = tuple(None if t is None else torch.empty(t.shape, device=t.device, dtype=dtype) for t in (q, k))
     qs = q.stride()
     _paged_call("tq_norm_rope", dev, qp, qs[0], qs[1], kp, ks[0], ks[1], QTYPE[dtype], weights[0], weights[1], QTYPE.get(wtype, 0),
                 eps, _on(dev, positions, "positions", torch.int32, (n,) if positions.dim() == 1 else (n, axes)), axes,
@@ -829,7 +829,7 @@ def read_int8(cache: Int8Cache, page_table, starts, lengths, n: int, dtype=torch
     dev, shape = cache._index, (int(n), cache.H, cache.D)
     tp, B, M = _table(dev, page_table)
     if out is None:
-        out = torch.empty((2, *shape), device=cache.device, dtype=dtype).unbind(0)
+        out = tuple(torch.empty(shape, device=cache.device, dtype=dtype) for _ in range(2))
     _paged_call("tq_read_int8", dev, cache._ref, _on(dev, out[0], "K", dtype, shape), _on(dev, out[1], "V", dtype, shape),
                 QTYPE[dtype], *_step(dev, starts, lengths, B), shape[0], tp, B, M)
     return out

@@ -465,9 +465,13 @@ tq_status tq_read_int8(const tq_int8_cache* cache, void* K, void* V, tq_qtype ty
  * all of them):
  *   z[s] = scale <q, k_s>,  p = softmax(z),  out = sum_s p[s] v_s    (zeros if it sees no slot)
  * Q: [n, H*G, D] of `type`, query head h*G + g reads KV head h.  out: the same shape and type.
- * fp32 queries: fp32 accuracy throughout.  bf16 queries: logits to fp32 accuracy, weights rounded
- * to fp16 (2^-12 at most) before the sum of values, sums in fp32, the output rounded to bf16.
- * The same inputs give the same bits.  Sequences may share pages.  scale: finite.
+ * fp32 queries: products to 22 bits, sums in fp32; |err| <= 1e-5 (1 + |out|) for values of order one and
+ * logits of order ten.  bf16 queries: logits to fp32 accuracy (2^-17 of scale sum |q_d k_d|), weights
+ * rounded to fp16 (2^-11) before the sum of values, sums in fp32, the output rounded to bf16.
+ * The same inputs give the same bits; the same token in a step of other tokens may not (the work
+ * is cut by the whole step).  Sequences may share pages.  scale: finite.  One token a sequence
+ * or a few read the cache once; more than 32 columns (tokens times G) of a sequence, with bf16 queries,
+ * take the tensor core's larger tiles, with fp32 ones the cache is read once for every 32.
  * workspace: at least tq_attend_int8_workspace_bytes(n, B, H, G, D) bytes, scratch, not
  * shared by concurrent calls or by graphs that may run concurrently.
  * ---------------------------------------------------------------------- */
