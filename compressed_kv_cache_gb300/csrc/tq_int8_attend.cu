@@ -201,7 +201,8 @@ cudaError_t launch_attend_int8(const tq_int8_cache& c, const void* Q, tq_qtype t
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3(2 * sms);
+  // the prompts' 256 columns a unit are many short joins, each a trip to memory: all warps that fit
+  cfg.gridDim = dim3((NC == 256 ? 4 : 2) * sms);
   cfg.blockDim = dim3(kJoinWarps * 32);
   if (c.D == 64)
     return f32 ? cudaLaunchKernelEx(&cfg, attend_join_kernel<float, 64>, a, nc_log2, ctas)
