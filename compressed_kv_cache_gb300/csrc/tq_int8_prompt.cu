@@ -7,12 +7,12 @@
 // one factor 2^(e - M + m).
 //
 // What bounds it: a tile of 128 slots is 2 x 2 products of 128 x 128 x D (2048 cycles of the tensor core for D = 128)
-// and 32768 exponentials (2048 cycles at 16 a cycle).  What it takes is 5200 cycles, the way of one half from its logits to its next
-// ones: 1700 for the maxima, 1700 for the weights, 1700 for the two products and the barriers between; the other half's runs
-// beside it and the tensor core is busy for 40 % of them.  256 columns share a conversion of the codes (800 cycles a side).
-// 1021 tokens over 8192 slots, 32 heads on 8: 209 us with the join (20), 615 TFLOP/s; the warp-wide form 700 us.
-// Weights with the maxima so far, kept in registers until they are known to hold, would read the logits once: 250 us,
-// as registers no longer suffice; one lane that waits and arrives for its warp: 245 us.
+// and 32768 exponentials (2048 cycles at 16 a cycle).  What it takes is the way of one half from its logits to its next
+// ones, some 5000 cycles: a third each for the maxima, the weights, and the two products with the barriers between; the other
+// half's runs beside it and the tensor core is busy for 40 % of them.  256 columns share a conversion of the codes (800
+// cycles a side).  1021 tokens over 8192 slots, 32 heads on 8: 187 us with the join (8), 690 TFLOP/s; the warp-wide form 700 us.
+// Weights with the maxima so far, kept in registers until they are known to hold, would read the logits once: slower by
+// a fifth, as registers no longer suffice; so is one lane that waits and arrives for its warp.
 //
 // Warps: 0-3 and 4-7 the two halves' columns (weights, rescaling, output), 8-11 bring the codes from memory and lay them
 // out as operands (128-byte swizzle; keys with the dimension, values with the slot as the outer index), 12 issues the
@@ -79,18 +79,27 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
         "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]),
         "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]),
         "=f"(v[31])
-      : "r"(addr)
-      : "memory");
+      : "r"(addr));
 }
 __device__ __forceinline__ void tmem_loaded(float (&v)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]),
                  "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]),
                  "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]),
-                 "+f"(v[28])
-               :
-               : "memory");
-  asm volatile("" : "+f"(v[29]), "+f"(v[30]), "+f"(v[31])::"memory");
+                 "+f"(v[28]));
+  asm volatile("" : "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]),
+        "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_loaded(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]),
+                 "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -427,50 +436,48 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
       for (int i = 0; i < n && !lost; ++i) {
         const uint32_t batch = batches_done + i / kBatch;
         if (i % kBatch == 0) wait(info_full + 8 * (batch & 3), batch >> 2);
-        wait(s_full + 8 * half, half_tiles[half] + i);
-        lost = __any_sync(0xffffffffu, lost);      // the whole warp's
-        if (lost) break;
-        after_sync();
         const BlockInfo* f = info[batch & 3] + (i % kBatch) * 8;
         const TileInfo ti = tile_info[batch & 3][i % kBatch];
         bool plain = ti.hi <= own && (a.window <= 0 || ti.lo > own - a.window || ti.hi < a.sinks);
         plain = __all_sync(0xffffffffu, plain || !there);
+        wait(s_full + 8 * half, half_tiles[half] + i);
+        lost = __any_sync(0xffffffffu, lost);      // the whole warp's
+        if (lost) break;
+        after_sync();
         auto seen = [&](int k, int c) {
           const int s = f[k].slot + c;
           return f[k].ek != 0.0f && s <= own && (a.window <= 0 || s > own - a.window || s < a.sinks);
         };
-        // largest logits of the blocks, two at a time; the next two are on their way meanwhile.  (Loops are kept short: the
-        // warps' programs share an instruction cache.)
+        // largest logits of the blocks; the next block's are on their way meanwhile, its exponents read before they are waited
+        // for.  (Loops are kept short: the warps' programs share an instruction cache.)
+        auto exponents = [&](int k) { return make_float2(f[k].ek, f[k].ev); };
         float top = -INFINITY, topv = -INFINITY;
-        float za[32], zb[32];
-        auto largest = [&](const float (&z)[32], int c4) {
+        float za[16], zb[16];
+        auto largest = [&](const float (&z)[16], int k, float2 e) {
+          float best = -INFINITY;
+          if (plain) {
+            float u[4];
 #pragma unroll
-          for (int k2 = 0; k2 < 2; ++k2) {
-            const int k = 2 * c4 + k2;
-            float best = -INFINITY;
-            if (plain) {
-              float u[4];
+            for (int c = 0; c < 4; ++c) u[c] = fmaxf(fmaxf(z[c], z[4 + c]), fmaxf(z[8 + c], z[12 + c]));
+            best = fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3]));
+          } else {
 #pragma unroll
-              for (int c = 0; c < 4; ++c) u[c] = fmaxf(fmaxf(z[16 * k2 + c], z[16 * k2 + 4 + c]), fmaxf(z[16 * k2 + 8 + c], z[16 * k2 + 12 + c]));
-              best = fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3]));
-            } else {
-#pragma unroll
-              for (int c = 0; c < 16; ++c) best = seen(k, c) ? fmaxf(best, z[16 * k2 + c]) : best;
-            }
-            const float v = best == -INFINITY ? best : (best + half_sum) * (factor * f[k].ek);
-            top = fmaxf(top, v);
-            topv = fmaxf(topv, v + f[k].ev);
+            for (int c = 0; c < 16; ++c) best = seen(k, c) ? fmaxf(best, z[c]) : best;
           }
+          const float v = best == -INFINITY ? best : (best + half_sum) * (factor * e.x);
+          top = fmaxf(top, v);
+          topv = fmaxf(topv, v + e.y);
         };
-        tmem_ld32(s_at, za);
+        tmem_ld16(s_at, za);
 #pragma unroll 1
-        for (int c4 = 0; c4 < 4; c4 += 2) {
+        for (int k = 0; k < 8; k += 2) {
+          const float2 e0 = exponents(k), e1 = exponents(k + 1);
           tmem_loaded(za);
-          tmem_ld32(s_at + 32 * c4 + 32, zb);
-          largest(za, c4);
+          tmem_ld16(s_at + 16 * k + 16, zb);
+          largest(za, k, e0);
           tmem_loaded(zb);
-          tmem_ld32(s_at + (c4 == 0 ? 64 : 0), za);      // the first again, for the weights
-          largest(zb, c4 + 1);
+          tmem_ld16(s_at + (k < 6 ? 16 * k + 32 : 0), za);      // at the end the first again, for the weights
+          largest(zb, k + 1, e1);
         }
         const bool over = top > m + kSlack || topv > M + kSlack;
         if (__any_sync(0xffffffffu, over)) {
@@ -502,63 +509,60 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         // two exponentials a logit
         const float apart_by = m - M;
         const bool quick = plain && !__any_sync(0xffffffffu, apart_by + ti.ev_hi > 100.0f || apart_by + ti.ev_lo < -60.0f);
-        auto weigh = [&](const float (&z)[32], int c4) {
-          uint32_t w[16];
+        auto weigh = [&](const float (&z)[16], float2 e, uint32_t* w) {
+          const float scale = factor * e.x, up = e.y - M + kLift, shift = fmaf(half_sum, scale, up);
+          const uint64_t scale2 = two(scale, scale), off = two(shift, shift);
+          uint64_t all = two(0.0f, 0.0f);
 #pragma unroll
-          for (int k2 = 0; k2 < 2; ++k2) {
-            const BlockInfo& at = f[2 * c4 + k2];
-            const float scale = factor * at.ek, up = at.ev - M + kLift, shift = fmaf(half_sum, scale, up);
-            const uint64_t scale2 = two(scale, scale), off = two(shift, shift);
-            uint64_t all = two(0.0f, 0.0f);
-#pragma unroll
-            for (int c = 0; c < 16; c += 2) {
-              const float2 v = apart(fma2(two(z[16 * k2 + c], z[16 * k2 + c + 1]), scale2, off));
-              const float w0 = exp2_fast(v.x), w1 = exp2_fast(v.y);
-              all = add2(all, two(w0, w1));
-              w[8 * k2 + c / 2] = pack(w0, w1);
-            }
-            const float2 sums = apart(all);
-            sum = fmaf(sums.x + sums.y, exp2_fast(-m - up), sum);      // p is the weight less its block's factor
+          for (int c = 0; c < 16; c += 2) {
+            const float2 v = apart(fma2(two(z[c], z[c + 1]), scale2, off));
+            const float w0 = exp2_fast(v.x), w1 = exp2_fast(v.y);
+            all = add2(all, two(w0, w1));
+            w[c / 2] = pack(w0, w1);
           }
-          tmem_st16(s_at + 16 * c4, w);      // over logits that have been read
+          const float2 sums = apart(all);
+          sum = fmaf(sums.x + sums.y, exp2_fast(-m - up), sum);      // p is the weight less its block's factor
         };
         if (quick) {
 #pragma unroll 1
-          for (int c4 = 0; c4 < 4; c4 += 2) {
+          for (int k = 0; k < 8; k += 2) {
+            const float2 e0 = exponents(k), e1 = exponents(k + 1);
+            uint32_t w[16];
             tmem_loaded(za);
-            tmem_ld32(s_at + 32 * c4 + 32, zb);
-            weigh(za, c4);
+            tmem_ld16(s_at + 16 * k + 16, zb);
+            weigh(za, e0, w);
             tmem_loaded(zb);
-            if (c4 == 0) tmem_ld32(s_at + 64, za);
-            weigh(zb, c4 + 1);
+            if (k < 6) tmem_ld16(s_at + 16 * k + 32, za);
+            weigh(zb, e1, w + 8);
+            tmem_st16(s_at + 8 * k, w);      // over logits that have been read
           }
         } else {
           tmem_loaded(za);
 #pragma unroll 1
-          for (int c4 = 0; c4 < 4; ++c4) {
-            if (c4 > 0) {
-              tmem_ld32(s_at + 32 * c4, za);
-              tmem_loaded(za);
-            }
+          for (int k = 0; k < 8; k += 2) {
             uint32_t w[16];
 #pragma unroll
             for (int k2 = 0; k2 < 2; ++k2) {
-              const int k = 2 * c4 + k2;
-              const float scale = factor * f[k].ek;
+              if (k + k2 > 0) {
+                tmem_ld16(s_at + 16 * (k + k2), za);
+                tmem_loaded(za);
+              }
+              const float2 e = exponents(k + k2);
+              const float scale = factor * e.x;
 #pragma unroll
               for (int c = 0; c < 16; c += 2) {
                 float q[2];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const float v = (za[16 * k2 + c + e] + half_sum) * scale;
-                  const bool on = seen(k, c + e);
+                for (int u = 0; u < 2; ++u) {
+                  const float v = (za[c + u] + half_sum) * scale;
+                  const bool on = seen(k + k2, c + u);
                   sum += on ? exp2_fast(v - m) : 0.0f;
-                  q[e] = on ? exp2_fast(v + (f[k].ev + kLift - M)) : 0.0f;
+                  q[u] = on ? exp2_fast(v + (e.y + kLift - M)) : 0.0f;
                 }
                 w[8 * k2 + c / 2] = pack(q[0], q[1]);
               }
             }
-            tmem_st16(s_at + 16 * c4, w);
+            tmem_st16(s_at + 8 * k, w);
           }
         }
         tmem_stored();
