@@ -37,7 +37,8 @@ constexpr int kPromptCtas = 160;      // of the prompts' form
 constexpr int kAttendWarps = 4;
 constexpr int kTileSlots = 32, kQuadTiles = kAttendWarps;
 
-// Blocks an SM: what registers allow.  More of them hide a tile's latency better than deeper rings.
+// Blocks an SM: what registers allow.  Heads of 64 with 8 columns: three (8 ragged sequences of 2049 slots in fp32 19.9 us, two
+// 22.3); heads of 128 with 8 columns would fit three only with two stages (32 x 32768 slots 337 us, two blocks with three 327).
 constexpr int attend_blocks(bool f32, int D, int nt) { return D == 64 && nt == 1 ? 3 : 2; }
 
 // What a block leaves for the join: the unit that it starts in the middle of.
