@@ -760,7 +760,8 @@ def norm_rope(q, k, positions, rotary: Rotary, q_weight=None, k_weight=None, eps
             wtype = t.dtype
         weights.append(None if t is None else _on(dev, t, name, t.dtype, (D,)))
     if out is None:
-        out = tuple(None if t is None else torch.empty(t.shape, device=t.device, dtype=dtype) for t in (q, k))
+        dense = torch.contiguous_format
+        out = torch.empty_like(q, memory_format=dense), None if k is None else torch.empty_like(k, memory_format=dense)
     qs = q.stride()
     _paged_call("tq_norm_rope", dev, qp, qs[0], qs[1], kp, ks[0], ks[1], QTYPE[dtype], weights[0], weights[1], QTYPE.get(wtype, 0),
                 eps, _on(dev, positions, "positions", torch.int32, (n,) if positions.dim() == 1 else (n, axes)), axes,
@@ -829,7 +830,8 @@ def read_int8(cache: Int8Cache, page_table, starts, lengths, n: int, dtype=torch
     dev, shape = cache._index, (int(n), cache.H, cache.D)
     tp, B, M = _table(dev, page_table)
     if out is None:
-        out = tuple(torch.empty(shape, device=cache.device, dtype=dtype) for _ in range(2))
+        out = torch.empty(shape, device=cache.device, dtype=dtype)
+        out = out, torch.empty_like(out)
     _paged_call("tq_read_int8", dev, cache._ref, _on(dev, out[0], "K", dtype, shape), _on(dev, out[1], "V", dtype, shape),
                 QTYPE[dtype], *_step(dev, starts, lengths, B), shape[0], tp, B, M)
     return out
