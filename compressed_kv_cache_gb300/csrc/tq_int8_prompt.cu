@@ -200,6 +200,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
   auto wait = [&](uint32_t bar, uint32_t parity) {
     if (!lost) lost = !wait_parity_bounded(bar, parity & 1, kFaultAttendWait);
   };
+  // A wait that ran out is the whole warp's: its lanes stay together for the votes and exchanges that follow.
+  auto wait_all = [&](uint32_t bar, uint32_t parity) {
+    wait(bar, parity);
+    lost = __any_sync(0xffffffffu, lost);
+  };
   uint32_t tiles_done = 0, batches_done = 0, units_done[2] = {0, 0}, half_tiles[2] = {0, 0};
 
   // The roles go through the same units, each in a loop of its own: registers are dealt out anew between them.
@@ -236,10 +241,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
     while (begin()) {
       // ---- the products: the whole warp keeps step, so that operands stay in its uniform registers; one lane issues
       if (warp == 12 && n > 0) {
-        auto wait_all = [&](uint32_t bar, uint32_t parity) {
-          wait(bar, parity);
-          lost = __any_sync(0xffffffffu, lost);
-        };
         auto logits = [&](int i, int half) {
           const uint64_t kd = operand(base + P::kK + ((tiles_done + i) & 1) * P::kSide, 16), qd = operand(base + P::kQ + half * P::kSide, 16);
           after_sync();
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           }
           if ((me & 7) == 0) tile_info[batch & 3][me / 8] = {lo, hi, ev_lo, ev_hi};
           arrive(info_full + 8 * (batch & 3));
-          wait(info_full + 8 * (batch & 3), batch >> 2);
+          wait_all(info_full + 8 * (batch & 3), batch >> 2);
         }
         uint4 k[kIt], v[kIt];
 #pragma unroll
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + c0), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (c0 ^ 16)), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
         };
-        wait(k_free + 8 * stage, (tile >> 1) + 1);
+        wait_all(k_free + 8 * stage, (tile >> 1) + 1);
         if (lost) break;
 #pragma unroll
         for (int r = 0; r < kIt; ++r) {
@@ -360,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         }
         operands_written();
         arrive(k_full + 8 * stage);
-        wait(v_free + 8 * stage, (tile >> 1) + 1);
+        wait_all(v_free + 8 * stage, (tile >> 1) + 1);
         if (lost) break;
 #pragma unroll
         for (int r = 0; r < kIt; ++r) {
@@ -435,13 +436,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
       }
       for (int i = 0; i < n && !lost; ++i) {
         const uint32_t batch = batches_done + i / kBatch;
-        if (i % kBatch == 0) wait(info_full + 8 * (batch & 3), batch >> 2);
+        if (i % kBatch == 0) wait_all(info_full + 8 * (batch & 3), batch >> 2);
         const BlockInfo* f = info[batch & 3] + (i % kBatch) * 8;
         const TileInfo ti = tile_info[batch & 3][i % kBatch];
         bool plain = ti.hi <= own && (a.window <= 0 || ti.lo > own - a.window || ti.hi < a.sinks);
         plain = __all_sync(0xffffffffu, plain || !there);
-        wait(s_full + 8 * half, half_tiles[half] + i);
-        lost = __any_sync(0xffffffffu, lost);      // the whole warp's
+        wait_all(s_full + 8 * half, half_tiles[half] + i);
         if (lost) break;
         after_sync();
         auto seen = [&](int k, int c) {
@@ -487,8 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           M = v;
           sum *= fm;
           if (i > 0) {
-            wait(o_done + 8 * half, half_tiles[half] + i - 1);
-            lost = __any_sync(0xffffffffu, lost);
+            wait_all(o_done + 8 * half, half_tiles[half] + i - 1);
             if (lost) break;
             after_sync();
             tmem_loaded(za);
@@ -570,8 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         arrive(p_full + 8 * half);
       }
       // ---- out, or a part for the join
-      if (n > 0) wait(o_done + 8 * half, half_tiles[half] + n - 1);
-      lost = __any_sync(0xffffffffu, lost);
+      if (n > 0) wait_all(o_done + 8 * half, half_tiles[half] + n - 1);
       after_sync();
       const bool entire = qa == 0 && qe == share.plan.quads;
       const size_t place = (static_cast<size_t>(blockIdx.x) * 2 + (qa == 0 ? 1 : 0)) * kNC + half * kHalf + r;

@@ -11,6 +11,8 @@ def test_every_wait_is_bounded_and_ends_its_role():
     waits = re.findall(r"wait_parity_bounded\(([^;]*)\);", t)
     assert len(waits) == 2 and all("kFaultAttendWait" in w for w in waits)
     assert re.search(r"if \(!lost\) lost = !wait_parity_bounded\(bar, parity & 1, kFaultAttendWait\)", t)
+    # a warp's lanes stay together: the votes and exchanges behind a wait need them all
+    assert re.findall(r"\bwait\(([^)]*)\)", t) == ["bar, parity"] and "lost = __any_sync(0xffffffffu, lost)" in block(t, "auto wait_all")
     # each role's loop over tiles stops, and none waits for other threads in between but at the end
     assert t.count("for (int i = 0; i < n && !lost; ++i)") == 3
     assert "bar.sync" not in t and len(re.findall(r"__syncthreads\(\)", t)) == 2
