@@ -594,11 +594,13 @@ def _table(index: int, page_table: torch.Tensor) -> tuple[int, int, int]:
     return _on(index, page_table, "page_table", torch.int32, (B, M)), B, M
 
 
-def _workspace_of(index: int, workspace, need: int) -> tuple[int, int]:
+def _workspace_of(index: int, workspace, need: int):
+    """The scratch of a paged call, its pointer and size.  The caller holds the tensor until the kernels are launched: memory
+    given back before is what the allocator hands out next, to an output of the same call for one."""
     if workspace is None:
         workspace = torch.empty(need, device=torch.device("cuda", index), dtype=torch.uint8)
     n = workspace.numel()
-    return _on(index, workspace, "workspace", torch.uint8, (n,)), n
+    return workspace, _on(index, workspace, "workspace", torch.uint8, (n,)), n
 
 
 def append_paged(K, V, rows, cache: PagedCache, page_table, mass=None, positions=None) -> None:
@@ -650,8 +652,8 @@ def decode_paged(Q, cache: PagedCache, page_table, lengths, mass=None, scale=Non
         if S < 1:
             raise ValueError("mass must be a [B, H, S] tensor with S >= 1")
         mp = _on(dev, mass, "mass", torch.float32, (B, H, S))
-    wp, wn = _workspace_of(dev, workspace, 0 if workspace is not None else
-                           decode_paged_workspace_bytes(B, H, G, S, mass is not None))
+    held, wp, wn = _workspace_of(dev, workspace, 0 if workspace is not None else
+                                 decode_paged_workspace_bytes(B, H, G, S, mass is not None))
     if out is None:
         out = torch.empty_like(Q)
     _paged_call("tq_decode_paged", dev, cache._ref, qp, QTYPE[dtype], tp, _on(dev, lengths, "lengths", torch.int32, (B,)),
@@ -680,8 +682,8 @@ def evict_paged(cache: PagedCache, page_table, lengths, seen, mass, positions, b
     budget, recent = max(-1, min(int(budget), S)), max(-1, min(int(recent), 2 ** 31 - 1))   # both fit an int
     if out is None:
         out = torch.zeros_like(mass), torch.full_like(positions, -1)
-    wp, wn = _workspace_of(dev, workspace, 0 if workspace is not None else
-                           evict_paged_workspace_bytes(B, cache.H, S, budget))
+    held, wp, wn = _workspace_of(dev, workspace, 0 if workspace is not None else
+                                 evict_paged_workspace_bytes(B, cache.H, S, budget))
     _paged_call("tq_evict_paged", dev, cache._ref, tp, _on(dev, lengths, "lengths", torch.int32, (B,)),
                 _on(dev, seen, "seen", torch.int32, (B,)), B, M, mp, pp, S, budget, recent,
                 _on(dev, out[0], "mass_out", torch.float32, shape),
@@ -857,7 +859,7 @@ def attend_int8(Q, starts, cache: Int8Cache, page_table, lengths, window=None, s
         raise ValueError("window must be positive or None, sinks not negative, both below 2^31")
     G, shape = heads // H, (n, heads, D)
     qp = _on(dev, Q, "Q", dtype, shape)
-    wp, wn = _workspace_of(dev, workspace, 0 if workspace is not None else attend_int8_workspace_bytes(n, B, H, G, D))
+    held, wp, wn = _workspace_of(dev, workspace, 0 if workspace is not None else attend_int8_workspace_bytes(n, B, H, G, D))
     if out is None:
         out = torch.empty_like(Q)
     _paged_call("tq_attend_int8", dev, cache._ref, qp, QTYPE[dtype], *_step(dev, starts, lengths, B), n, G, tp, B, M,
