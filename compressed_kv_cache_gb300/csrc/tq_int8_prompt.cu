@@ -159,16 +159,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
   __shared__ ShareScan<kWarps> scan;
   __shared__ BlockInfo info[P::kInfo][kBatch * 8];
   __shared__ TileInfo tile_info[P::kInfo][kBatch];
-  __shared__ __align__(8) uint64_t bars[21];
+  __shared__ __align__(8) uint64_t bars[25];
   __shared__ uint32_t tmem_slot;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   const uint32_t base = smem_addr(smem);
-  // barriers: keys full / free, values full / free (2 stages each), queries, logits, weights, products done (2 halves each), infos (4)
+  // barriers: keys full / free, values full / free (2 stages each), queries, logits, weights, products done (2 halves each),
+  // infos full / free (4 each)
   const uint32_t bar0 = smem_addr(bars);
   const uint32_t k_full = bar0, k_free = bar0 + 16, v_full = bar0 + 32, v_free = bar0 + 48, q_full = bar0 + 64, s_full = bar0 + 80,
-                 p_full = bar0 + 96, o_done = bar0 + 112, info_full = bar0 + 128, drained = bar0 + 160;
+                 p_full = bar0 + 96, o_done = bar0 + 112, info_full = bar0 + 128, info_free = bar0 + 160, drained = bar0 + 192;
 
   Share<kNC, kWarps> share;
   if (!share.find(a, scan)) return;
@@ -184,7 +185,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
       bar_init(o_done + 8 * i, 1);
     }
     bar_init(drained, 1);
-    for (int i = 0; i < P::kInfo; ++i) bar_init(info_full + 8 * i, kMakers);
+    for (int i = 0; i < P::kInfo; ++i) {
+      bar_init(info_full + 8 * i, kMakers);
+      bar_init(info_free + 8 * i, 8);      // a lane of each of the columns' warps
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 12) {
@@ -297,6 +301,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
       for (int i = 0; i < n && !lost; ++i) {
         const uint32_t tile = tiles_done + i, stage = tile & 1, batch = batches_done + i / kBatch;
         if (i % kBatch == 0) {
+          wait_all(info_free + 8 * (batch & 3), (batch >> 2) + 1);
+          if (lost) break;
           BlockInfo& to = info[batch & 3][me];
           const int64_t q = qa + i + me / 8;
           const int j = static_cast<int>(4 * q) + (me & 7) / 2;
@@ -384,8 +390,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
     const int half = warp >> 2;
+    // A batch of infos is given back when a half is done with it.
+    auto give_back = [&](uint32_t batch) {
+      __syncwarp();
+      if ((tid & 31) == 0) arrive(info_free + 8 * (batch & 3));
+    };
     while (begin()) {
       if (half >= halves) {
+        // Nothing to do but to go along: a wait by parity tells only neighbouring phases apart, so that a half that had left the
+        // batches of such units out would take an older one for the next unit's.
+        for (int i = 0; i < n && !lost; i += kBatch) {
+          const uint32_t batch = batches_done + i / kBatch;
+          wait_all(info_full + 8 * (batch & 3), batch >> 2);
+          if (!lost) give_back(batch);
+        }
         end();
         continue;
       }
@@ -567,6 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         tmem_stored();
         before_sync();
         arrive(p_full + 8 * half);
+        if (i % kBatch == kBatch - 1 || i == n - 1) give_back(batch);
       }
       // ---- out, or a part for the join
       if (n > 0) wait_all(o_done + 8 * half, half_tiles[half] + n - 1);
