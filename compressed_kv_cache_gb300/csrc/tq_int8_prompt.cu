@@ -505,10 +505,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           M = v;
           sum *= fm;
           if (i > 0) {
+            tmem_loaded(za);      // nothing is under way where the wait gives up
             wait_all(o_done + 8 * half, half_tiles[half] + i - 1);
             if (lost) break;
             after_sync();
-            tmem_loaded(za);
 #pragma unroll 1
             for (int c4 = 0; c4 < D / 32; ++c4) {
               float o[32];

@@ -158,3 +158,12 @@ def test_the_kernel_follows_the_ring():
     assert "arrive(info_free" in SOURCE[SOURCE.index("auto give_back"):SOURCE.index("if (half >= halves)")]
     skip = SOURCE[SOURCE.index("if (half >= halves)"):SOURCE.index("a column: its query")]
     assert skip.index("wait_all(info_full") < skip.index("give_back(batch)") < skip.index("end();")
+
+
+def test_no_load_is_under_way_where_the_columns_give_up():
+    """The logits read ahead land in registers: they are waited for before the loop can be left, whose end uses registers anew."""
+    role = SOURCE[SOURCE.index("a column: its query"):]
+    ahead = role.index("at the end the first again, for the weights")
+    leave = role.index("if (lost) break;", ahead)
+    assert ahead < role.index("tmem_loaded(za);", role.index("largest(zb, k + 1, e1);")) < leave
+    assert "break" not in role[leave + len("if (lost) break;"):role.index("out, or a part for the join")]
