@@ -85,9 +85,12 @@ inline Int8View int8_view(const tq_int8_cache& c, const int* table, int max_page
 struct Run {
   int first, count, len;
 };
+__device__ __forceinline__ bool fits(const Step& s, int a, int z, int len) {
+  return a >= 0 && a <= z && z <= s.n && len >= 0 && len <= INT32_MAX - 4096 - (z - a);
+}
 __device__ __forceinline__ Run run_of(const Step& s, int b) {
   const int a = s.starts[b], z = s.starts[b + 1], len = s.lengths[b];
-  if (a >= 0 && a <= z && z <= s.n && len >= 0 && len <= INT32_MAX - 4096 - (z - a)) return {a, z - a, len};
+  if (fits(s, a, z, len)) return {a, z - a, len};
   atomicOr(&g_wait_fault, static_cast<unsigned int>(kFaultPaged));
   return {0, 0, 0};
 }

@@ -30,20 +30,50 @@ struct Unit {
   bool old;                           // rows before rows0 are live
 };
 
-// The sequence is looked for by 32 lanes at a time: 2 loads in a row for 1024 sequences.
+__device__ __forceinline__ int64_t first_unit(int start, int b) { return (start >> 4) + 2 * static_cast<int64_t>(b); }
+
+// The sequence is looked for by 32 lanes at a time: 2 loads in a row for 1024 sequences.  Where starts do not ascend the search may end
+// anywhere.  It is right where it ends at a sequence whose numbers fit and whose unit this is, or before the first
+// or behind the last (tokens of none); else every sequence is asked whether it has rows in this unit, so that what is wrong of
+// one costs no other its rows.  (Of two that have tokens in common, and this unit both, one is served.)
 __device__ __forceinline__ bool unit_of(const Step& s, int u, int lane, Unit& t) {
   int lo = 0, hi = s.B;
   while (hi - lo > 1) {
     const int stride = (hi - lo + 31) / 32;
     const int i = lo + lane * stride;
-    const bool below = i < hi && (s.starts[i] >> 4) + 2 * static_cast<int64_t>(i) <= u;
+    const bool below = i < hi && first_unit(s.starts[i], i) <= u;
     const int n = __popc(__ballot_sync(0xffffffffu, below));
     lo += (n > 0 ? n - 1 : 0) * stride;
     hi = min(hi, lo + stride);
   }
-  const Run r = run_of(s, lo);
-  const int64_t k = u - ((r.first >> 4) + 2 * static_cast<int64_t>(lo));
-  if (r.count == 0 || k < 0) return false;
+  int a = s.starts[lo], z = s.starts[lo + 1], len = s.lengths[lo];
+  const bool good = fits(s, a, z, len), before = u < first_unit(a, lo), behind = u >= first_unit(z, lo + 1);
+  if (!good || before || behind) {
+    if (good && (before ? lo == 0 : lo == s.B - 1)) return false;
+    atomicOr(&g_wait_fault, static_cast<unsigned int>(kFaultPaged));
+    uint32_t owners = 0;
+    int b0 = -32;
+    while (owners == 0 && b0 + 32 < s.B) {
+      b0 += 32;
+      const int b = b0 + lane;
+      bool own = false;
+      if (b < s.B) {
+        a = s.starts[b];
+        z = s.starts[b + 1];
+        len = s.lengths[b];
+        const int64_t k = u - first_unit(a, b);
+        own = a < z && fits(s, a, z, len) && k >= 0 && ((len >> 4) + k) << 4 < static_cast<int64_t>(len) + z - a;
+      }
+      owners = __ballot_sync(0xffffffffu, own);
+    }
+    if (owners == 0) return false;
+    lo = b0 + __ffs(owners) - 1;
+    a = s.starts[lo];
+    z = s.starts[lo + 1];
+    len = s.lengths[lo];
+  }
+  const Run r = {a, z - a, len};
+  const int64_t k = u - first_unit(a, lo);
   const int64_t slot = ((r.len >> 4) + k) << 4;
   const int64_t first = slot > r.len ? slot : r.len, stop = min(slot + kBlockSlots, static_cast<int64_t>(r.len) + r.count);
   if (first >= stop) return false;

@@ -418,7 +418,9 @@ tq_status tq_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_str
  * page_table [B, max_pages] int32: slot s of sequence b is row s % page_size of page
  * page_table[b, s / page_size].  Only entries of slots that a call writes or sees are read: pages
  * that a window has left behind may go back to the pool.
- * A sequence whose starts descend or leave [0, n], or whose length is negative, has no tokens; a
+ * A sequence whose starts descend or leave [0, n], or whose length is negative, has no tokens, and
+ * the others have theirs (where starts out of order give tokens to two sequences, the append and the
+ * read may leave out rows of one); a
  * slot beyond max_pages * page_size or on a page outside [0, n_pages) is absent.  Each sets
  * fault bit 32 (tq_device_faults) where it is met, and nothing out of range is read or written.
  *
