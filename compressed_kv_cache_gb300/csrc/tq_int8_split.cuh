@@ -126,8 +126,8 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, const Run& r, int c
   s.from = min(s.lo, s.hi + 1) / kTileSlots;
   s.sunk = min((min(a.sinks, s.hi + 1) + kTileSlots - 1) / kTileSlots, s.from);
   if (a.window <= 0) s.sunk = 0;
+  // where the window lies beyond the table (lo > hi) the last tile may still hold first slots
   s.tiles = s.sunk + max(0, s.hi / kTileSlots - s.from + 1);
-  if (s.lo > s.hi) s.tiles = s.sunk;
   return s;
 }
 
