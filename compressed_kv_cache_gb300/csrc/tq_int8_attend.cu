@@ -145,6 +145,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
 
 // Columns of a unit: 8, 16 or 32 in the warp-wide form, as many as an average sequence fills (the cache is read
 // once for all columns of a unit, and again, from L2, for the next ones); 256 in the prompts' form, for bf16 queries with more than 32.
+// The average of the step decides for all of its sequences, known to the host without a look at `starts`.  Steps of both kinds pay
+// for it: 255 single tokens and a piece of 512, behind 2048 slots each, 32 heads on 8, take 340 us (172 and 64 apart), 32 and a piece of
+// 2048 take 281 (33 and 201).
 int columns_of(int n, int B, int G, bool f32) {
   const int64_t columns = (static_cast<int64_t>(n) * G + B - 1) / B;
   return columns <= 8 ? 8 : columns <= 16 ? 16 : columns <= 32 || f32 ? 32 : 256;

@@ -8,9 +8,10 @@
 //
 // What bounds it: a tile of 128 slots is 2 x 2 products of 128 x 128 x D (2048 cycles of the tensor core for D = 128)
 // and 32768 exponentials (2048 cycles at 16 a cycle).  What it takes is the way of one half from its logits to its next
-// ones, some 5000 cycles: a third each for the maxima, the weights, and the two products with the barriers between; the other
-// half's runs beside it and the tensor core is busy for 40 % of them.  256 columns share a conversion of the codes (800
-// cycles a side).  1021 tokens over 8192 slots, 32 heads on 8: 187 us with the join (8), 690 TFLOP/s; the warp-wide form 700 us.
+// ones, some 4900 cycles: 1100 to 1500 for the maxima, 1900 to 2200 for the weights, the rest for the two products with the
+// barriers between; the other half's runs beside it and the tensor core is busy for 34 % of them.  256 columns share a conversion of
+// the codes (1000 cycles for keys, 700 for values).  1021 tokens over 8192 slots, 32 heads on 8: 187 us with the join (8), 690 TFLOP/s;
+// the warp-wide form 700 us.  From an empty cache, where shares are uneven, 8192 tokens take 1.13 ms, 480 TFLOP/s.
 // Weights with the maxima so far, kept in registers until they are known to hold, would read the logits once: slower by
 // a fifth, as registers no longer suffice; so is one lane that waits and arrives for its warp.
 //
@@ -18,7 +19,8 @@
 // out as operands (128-byte swizzle; keys with the dimension, values with the slot as the outer index), 12 issues the
 // products (13-15 only give up registers: 144 a thread for the columns, 112 for the others, 65536 in all; with fewer for the
 // others their loops spill).  Weights go to tensor memory over the logits that they come from and are read there as an operand.
-// Two stages of keys and of values; the next tile's codes are on their way in registers while a stage is waited for.
+// Two stages of keys and of values; the next tile's codes are on their way in registers while a stage is waited for.  What is to be
+// known of 16 tiles is a batch in a ring of four, which both halves follow and give back, with columns in the unit or without.
 //
 // Every wait gives up after the library's budget: the block then writes NaN for what it has not done, sets fault bit 128,
 // lets the products in flight end, frees its tensor memory and returns.

@@ -781,7 +781,8 @@ class Int8Cache:
     """A paged cache of keys and values in 8 bits with an exponent for each 16 slots of a head: the handle
     the int8 calls take, made once per layer.  k_codes, v_codes uint8 [N,H,page,D], exponents int8
     [N,H,page/16,2]; D 64 or 128, page a power of two from 16 to 256.  Fresh pages need no
-    initial values.  The tensors stay the caller's, as for PagedCache.
+    initial values.  The tensors stay the caller's and every array of a call begins on a 16-byte boundary (slices of starts,
+    lengths and positions too), as for PagedCache.
 
     The calls share a step's form: tokens one behind the other, those of sequence b from starts[b] to
     starts[b+1] (int32 [B+1]), at its slots from lengths[b] (int32 [B], slots in use before the step) on."""

@@ -390,7 +390,8 @@ tq_status tq_evict_paged(const tq_paged_cache* cache, const int* page_table, con
  * q_out, k_out: [n, Hq, D] and [n, Hk, D] dense.  q_out may be q itself where q is dense, k_out
  * likewise; else no output may overlap an input or the other output.
  * D a multiple of 8, 8 <= D <= 256; pairs a multiple of 4, 4 <= pairs <= D / 2; 1 <= axes <= 8; eps >= 0.
- * fp32 arithmetic, rounded once; the angle keeps 2^-32 of a turn at every position.
+ * fp32 arithmetic, rounded once; the angle is off by at most 2^-26 of a turn at every position (reduced to 2^-32 of
+ * a turn in whole numbers, then an fp32 number of half turns).
  * Errors: TQ_ERR_INVALID_VALUE, TQ_ERR_MISALIGNED, TQ_ERR_UNSUPPORTED (D or pairs), TQ_ERR_LAUNCH.
  * ---------------------------------------------------------------------- */
 tq_status tq_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
@@ -471,9 +472,11 @@ tq_status tq_read_int8(const tq_int8_cache* cache, void* K, void* V, tq_qtype ty
  * logits of order ten.  bf16 queries: logits to fp32 accuracy (2^-17 of scale sum |q_d k_d|), weights
  * rounded to fp16 (2^-11) before the sum of values, sums in fp32, the output rounded to bf16.
  * The same inputs give the same bits; the same token in a step of other tokens may not (the work
- * is cut by the whole step).  Sequences may share pages.  scale: finite.  One token a sequence
- * or a few read the cache once; more than 32 columns (tokens times G) of a sequence, with bf16 queries,
- * take the tensor core's larger tiles, with fp32 ones the cache is read once for every 32.
+ * is cut by the whole step).  Sequences may share pages.  scale: finite.  The form goes by the step's
+ * average of columns (tokens times G; n * G / B): up to 32 the cache is read once for every 8, 16 or 32 columns of
+ * a sequence, above that, with bf16 queries, every sequence takes the tensor core's larger tiles (256 columns),
+ * with fp32 ones the cache is read once for every 32.  A step of one kind is served best: a piece of a prompt
+ * among many single tokens, or a few of these beside a long piece, cost less in a call of their own.
  * workspace: at least tq_attend_int8_workspace_bytes(n, B, H, G, D) bytes, scratch, not
  * shared by concurrent calls or by graphs that may run concurrently.
  * ---------------------------------------------------------------------- */
